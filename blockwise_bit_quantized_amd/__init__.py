@@ -401,3 +401,17 @@ def matmul(X, pw: PackedWeight, adapter: Adapter | None = None, path: int = MNB_
     _check(mnb_matmul_bias(_ptr(X), _ptr(pw.wq), _ptr(pw.sc), _ptr(pw.zp), ad, _ptr(bias), _ptr(Y), M,
                            pw.N, K, pw.bits, 32, _ptr(ws), ws.numel(), _stream(dev), opt))
     return Y
+
+
+# ---------------------------------------------------------------------------------------
+# The operators beside MatMulNBits (include/mnb_ops.h)
+# ---------------------------------------------------------------------------------------
+
+from . import ops as _ops  # noqa: E402
+
+_ops._bind(lib, mnb_status_string)
+from .ops import (  # noqa: E402,F401
+    MNB_BF16, MNB_F16, MNB_F32, MNB_LOGPROBS_MAX_TOP, MNB_MX_FP4, MNB_MX_FP8, LogProbs, MxTensor, MxWeight, Normed,
+    logprobs, mnb_logprobs, mnb_logprobs_workspace_bytes, mnb_mx_dequantize, mnb_mx_describe_route, mnb_mx_matmul,
+    mnb_mx_pack, mnb_mx_packed_sizes, mnb_mx_quantize, mnb_mx_workspace_bytes, mnb_ops_version, mnb_rmsnorm,
+    mx_dequantize, mx_matmul, mx_pack, mx_quantize, mx_tensor, rmsnorm)

@@ -1,0 +1,31 @@
+// mx_mfma.h -- the scaled matrix instruction of the MX product, shared by its kernels.
+//
+// v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16 weight rows (FP4, the row operand) with
+// 16 X rows (the column operand) over 128 k, applying one scale byte per operand row and
+// block of 32.  Operand layouts (measured on the part): FP4, lane 16 b + r holds row r,
+// k = 32 b .. 32 b + 31 in 16 bytes; FP8, lane 16 g + r holds row r, k = 16 g .. + 15 in the
+// first 16 bytes and k = 64 + 16 g .. in the next; the scale byte of block b of row r comes
+// from lane 16 b + r in either case, taken from byte J of the lane's dword.  The result's
+// lane 16 g + c holds weight rows 4 g .. 4 g + 3 of X row c.
+#pragma once
+
+#include <type_traits>
+
+#include "ops.h"
+
+namespace mnb {
+
+template <int FMT, int J>
+__device__ __forceinline__ f4_t mx_mfma(u4_t w, u4_t x0, u4_t x1, f4_t acc, uint32_t sw, uint32_t sx) {
+  const i8_t a = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+  const i8_t b = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, FMT == MX_FP4 ? 4 : 0, J, (int)sw, 0, (int)sx);
+}
+
+template <int DT>
+__device__ __forceinline__ void store_cols(const MxMatmulParams &p, int64_t m, int64_t n, float v) {
+  if (p.bias) v += to_f32<DT>(p.bias[n]);
+  p.y[m * p.N + n] = from_f32<DT>(v);
+}
+
+}  // namespace mnb

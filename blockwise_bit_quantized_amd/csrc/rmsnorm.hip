@@ -1,0 +1,163 @@
+// rmsnorm.hip -- y = h / sqrt(mean(h^2) + eps) * w, h = x + residual, with the new residual
+// stream h and y in 16 bits or MX as outputs, each rounded once from 32 bits.
+//
+// The sum of squares, the root and the products are in 64 bits: bfloat16 rows may have
+// squares past the range of 32, and an MX output then has the codes of the exact y all but
+// always (an error of 2^-24 moves about one element in a million to its neighbour).  The part
+// runs 64-bit multiply-adds at the rate of 32-bit ones, so this hides behind the loads.
+//
+// Bound by memory: each input is read once and each output written once.  The aligned
+// kernel keeps a row's h in registers between the sum of squares and the outputs (CH pieces
+// of 8 elements a thread); rows longer than that read the inputs a second time for the
+// pieces past it (from L2).  Rows of other alignment take the element-wise kernel.
+#include "ops.h"
+
+namespace mnb {
+namespace {
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// sum over the workgroup, the same in every thread
+template <int WAVES>
+__device__ __forceinline__ double block_sum(double v) {
+  v = wave_sum(v);
+  if constexpr (WAVES > 1) {
+    __shared__ double part[WAVES];
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) v += part[i];
+  }
+  return v;
+}
+
+template <int DT>
+__device__ __forceinline__ void load_h(const NormParams &p, const uint16_t *x, const uint16_t *res, int64_t c, float *h) {
+  load8<DT>(x + 8 * c, h);
+  if (res) {
+    float r[8];
+    load8<DT>(res + 8 * c, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] += r[i];
+  }
+}
+
+// K % 8 == 0, every row 16-byte aligned; with codes K % 32 == 0.  The piece loops run to a
+// multiple of THREADS so that the four lanes of a block meet in the exchanges.
+template <int DT, int FMT, int WAVES, int CH>
+__global__ __launch_bounds__(WAVES * 64) void norm_kernel(NormParams p) {
+  constexpr int THREADS = WAVES * 64;
+  const int64_t row = blockIdx.x;
+  const int t = threadIdx.x, pieces = p.K / 8;
+  const uint16_t *x = p.x + row * p.ldx, *res = p.res ? p.res + row * p.ldr : nullptr;
+  float h[CH][8];
+  double ss = 0.0;
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    const int c = j * THREADS + t;
+    if (c < pieces) {
+      load_h<DT>(p, x, res, c, h[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fma((double)h[j][i], (double)h[j][i], ss);
+    }
+  }
+  for (int c = CH * THREADS + t; c < pieces; c += THREADS) {
+    float v[8];
+    load_h<DT>(p, x, res, c, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fma((double)v[i], (double)v[i], ss);
+  }
+  ss = block_sum<WAVES>(ss);
+  const double rstd = 1.0 / sqrt(ss / p.K + (double)p.eps);
+
+  auto finish = [&](int c, float *v) {
+    if (p.hidden) store8<DT>(p.hidden + row * p.ldh + 8 * (int64_t)c, v);
+    float w[8];
+    load8<DT>(p.w + 8 * (int64_t)c, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (float)((double)v[i] * rstd * (double)w[i]);
+    if (p.y) store8<DT>(p.y + row * p.ldy + 8 * (int64_t)c, v);
+    if constexpr (FMT >= 0) {
+      uint32_t amax = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = max(amax, __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu);
+      amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1));
+      amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2));
+      const uint32_t e = mx_scale<FMT>(amax);
+      const float inv = mx_inverse(e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = e == 255 ? 0.f : v[i] * inv;
+      uint8_t *out = p.codes + row * p.ldc;
+      if constexpr (FMT == MX_FP4) *reinterpret_cast<uint32_t *>(out + 4 * (int64_t)c) = fp4_codes(v);
+      else *reinterpret_cast<u2_t *>(out + 8 * (int64_t)c) = u2_t{fp8_codes4(v), fp8_codes4(v + 4)};
+      if ((c & 3) == 0) p.scales[row * p.lds + (c >> 2)] = (uint8_t)e;
+    }
+  };
+  // K % 32 == 0 with codes: the four threads of a block are all inside the row or all past it
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    const int c = j * THREADS + t;
+    if (c < pieces) finish(c, h[j]);
+  }
+  for (int c = CH * THREADS + t; c < pieces; c += THREADS) {
+    float v[8];
+    load_h<DT>(p, x, res, c, v);
+    finish(c, v);
+  }
+}
+
+// any K and alignment, 16-bit outputs only: one element at a time, the inputs read twice
+template <int DT>
+__global__ __launch_bounds__(256) void norm_any_kernel(NormParams p) {
+  const int64_t row = blockIdx.x;
+  const uint16_t *x = p.x + row * p.ldx, *res = p.res ? p.res + row * p.ldr : nullptr;
+  double ss = 0.0;
+  for (int k = threadIdx.x; k < p.K; k += 256) {
+    const float h = to_f32<DT>(x[k]) + (res ? to_f32<DT>(res[k]) : 0.f);
+    ss = fma((double)h, (double)h, ss);
+  }
+  ss = block_sum<4>(ss);
+  const double rstd = 1.0 / sqrt(ss / p.K + (double)p.eps);
+  for (int k = threadIdx.x; k < p.K; k += 256) {
+    const float h = to_f32<DT>(x[k]) + (res ? to_f32<DT>(res[k]) : 0.f);
+    if (p.hidden) p.hidden[row * p.ldh + k] = from_f32<DT>(h);
+    p.y[row * p.ldy + k] = from_f32<DT>((float)((double)h * rstd * (double)to_f32<DT>(p.w[k])));
+  }
+}
+
+bool aligned16(const void *p, int64_t ld) { return !p || (((uintptr_t)p | (uintptr_t)(2 * ld)) & 15) == 0; }
+
+template <int DT, int FMT>
+hipError_t launch(const NormParams &p, hipStream_t s) {
+  const dim3 grid((uint32_t)p.M);
+  if constexpr (FMT < 0) {
+    if (p.K % 8 || !aligned16(p.x, p.ldx) || !aligned16(p.res, p.ldr) || !aligned16(p.hidden, p.ldh) ||
+        !aligned16(p.y, p.ldy) || !aligned16(p.w, 0)) {
+      hipLaunchKernelGGL((norm_any_kernel<DT>), grid, dim3(256), 0, s, p);
+      return hipGetLastError();
+    }
+  }
+  if (p.K <= 2048) hipLaunchKernelGGL((norm_kernel<DT, FMT, 4, 1>), grid, dim3(256), 0, s, p);
+  else if (p.K <= 8192) hipLaunchKernelGGL((norm_kernel<DT, FMT, 4, 4>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((norm_kernel<DT, FMT, 16, 4>), grid, dim3(1024), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(int dtype, int fmt, const NormParams &p, hipStream_t s) {
+  if (dtype == DT_F16)
+    return fmt < 0          ? launch<DT_F16, -1>(p, s)
+           : fmt == MX_FP4 ? launch<DT_F16, MX_FP4>(p, s)
+                           : launch<DT_F16, MX_FP8>(p, s);
+  return fmt < 0          ? launch<DT_BF16, -1>(p, s)
+         : fmt == MX_FP4 ? launch<DT_BF16, MX_FP4>(p, s)
+                         : launch<DT_BF16, MX_FP8>(p, s);
+}
+
+}  // namespace mnb
