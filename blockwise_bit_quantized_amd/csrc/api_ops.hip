@@ -48,7 +48,8 @@ bool bad_ld(int64_t ld, int64_t least) { return ld < least || ld > (1ll << 40); 
 int check_matmul_sizes(int M, int N, int K, int fmt) {
   if (M < 0 || N < 0 || K < 0) return MNB_ERR_INVALID_ARG;
   if (fmt != MNB_MX_FP4 && fmt != MNB_MX_FP8) return MNB_ERR_INVALID_ARG;
-  if (K % kBlock || K >= kMaxK) return MNB_ERR_UNSUPPORTED;
+  // 32-bit offsets from a tile's first row reach its 256 rows of X
+  if (K % kBlock || K >= kMxMaxK) return MNB_ERR_UNSUPPORTED;
   // a launch has fewer than 2^32 threads: 256 per (row group, step) of the packer and at most
   // 512 per range and tile of 64 x 128 outputs of the product
   if (cdiv(N, 64) * cdiv(K, kMxStep) >= 1 << 24) return MNB_ERR_UNSUPPORTED;
@@ -158,6 +159,7 @@ int mnb_mx_matmul(const void *codes, int64_t ldc, const void *scales, int64_t ld
   if (!wq || !sc || bad_ld(ldc, 0) || bad_ld(lds, 0)) return MNB_ERR_INVALID_ARG;
   st = check_mx(fmt, K, codes, ldc, scales, lds);
   if (st) return st;
+  if (ldc > 2 * kMxMaxK || lds > 2 * kMxMaxK) return MNB_ERR_UNSUPPORTED;
   if (off16(wq) || off16(sc) || off16(workspace)) return MNB_ERR_MISALIGNED;
   const size_t need = mnb_mx_workspace_bytes(M, N, K, fmt);
   if (need && (!workspace || ws_bytes < need)) return MNB_ERR_WORKSPACE;

@@ -1,129 +1,313 @@
-// mx_gemm.hip -- MX product for more than 16 rows.
+// mx_gemm.hip -- MX product for more rows than the weight-streaming kernel takes.
 //
-// 128 x 128 outputs per workgroup of 4 waves, each 64 x 64 (4 x 4 scaled 16x16x128 matrix
-// instructions per step of 128 k).  The X tile goes through LDS (two buffers, the next
-// step's loads in registers meanwhile), 16-byte chunks XOR-swizzled so that the 16 rows an
-// operand read touches fall on distinct banks; the weights are packed in operand order and
-// load straight into registers.
+// Bound by the matrix cores where there is enough work: an instruction of 16 x 16 outputs and
+// 128 k takes 16 cycles (FP4 X) or 32 (FP8 X).  A workgroup owns BM x BN outputs, a wave
+// MF x NF operands of 16 rows and 16 columns.
+//
+// X goes through LDS in steps of 128 bytes a row (128 k of FP8, 256 of FP4), a ring of
+// D + 1 slots filled by direct-to-LDS loads D steps ahead; a row's eight 16-byte chunks are
+// XOR-swizzled by the row through the source address (the loads write lanes
+// consecutively), so that the 16 rows of an operand read fall on distinct banks.  Weights are
+// packed in operand order and load straight into registers, D steps ahead as well: a wave's
+// loads complete in order, so neither may run further ahead than the other.  The X scales of
+// up to 8192 k are staged in LDS before the steps ([chunk of 512 k][row][16 bytes], where
+// the 16 rows of an operand are 256 consecutive bytes) and read one byte per lane, the byte
+// the instruction wants; weight scales are one dword per operand and 512 k.
+//
+// With PRE the X operands of the next step are read into a second register set before the
+// current step's instructions are issued, so a single wave per SIMD does not wait for LDS.
 #include "mx_mfma.h"
 
 namespace mnb {
 namespace {
 
-constexpr int BM = 128, BN = 128, kThreads = 256;
+typedef __attribute__((address_space(3))) void lds_void;
 
-// LDS byte of 16-byte chunk c of row m: rows of 128 bytes (FP8) or 64 (FP4)
-template <int FMT>
-__device__ __forceinline__ int x_chunk(int m, int c) {
-  return FMT == MX_FP8 ? m * 128 + ((c ^ ((m >> 1) & 7)) << 4) : m * 64 + ((c ^ ((m >> 2) & 3)) << 4);
+// 16 bytes per lane to LDS at dst + 16 lane: address = descriptor base + voff + soff
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, uint8_t *dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)dst, 16, voff, soff, 0, 0);
+}
+// s_waitcnt with vmcnt = N (gfx9 encoding: vmcnt bits 3:0 and 15:14), other counters free
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+// LDS accesses done, workgroup barrier; the clobber keeps memory accesses on their side
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));   // lgkmcnt(0)
+  asm volatile("s_barrier" ::: "memory");
+}
+// keeps the order of the loads on either side, which the vmcnt waits count
+__device__ __forceinline__ void pin() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int DT, int FMT>
-__global__ __launch_bounds__(kThreads) void gemm_kernel(MxMatmulParams p) {
-  constexpr int XB = FMT == MX_FP4 ? 64 : 128, XC = XB / 16;
-  constexpr int LD = BM * XC / kThreads;   // 16-byte loads per thread and step
-  __shared__ uint8_t xt[2][BM * XB] __attribute__((aligned(16)));
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+// the value is computed here (an empty use the compiler cannot move)
+__device__ __forceinline__ void keep(f4_t &v) { asm volatile("" : "+v"(v)); }
+
+constexpr int kPanel = 16;   // 512-k chunks of X scales in LDS at a time
+
+template <int I, int N, typename F>
+__device__ __forceinline__ void unroll(F &&f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    unroll<I + 1, N>(f);
+  }
+}
+
+template <int DT, int FMT, int BM, int WM, int WN, int NF, int D, bool PRE>
+__global__ __launch_bounds__(WM * WN * 64, WM * WN * 64 == 512 ? 2 : 1) void gemm_kernel(MxMatmulParams p) {
+  constexpr int WAVES = WM * WN, BN = WN * NF * 16, MF = BM / WM / 16;
+  constexpr int SUB = FMT == MX_FP4 ? 2 : 1;      // instructions per step, operand pair
+  constexpr int SLOTS = D + 1, SLOT = BM * 128;
+  constexpr int XQ = BM / 8 / WAVES;              // X loads per wave and step (8 rows each)
+  constexpr int WQ = SUB * NF;                    // weight loads per wave and step
+  constexpr int WS = PRE ? SLOTS * SUB : SUB + 1; // weight register sets, one instruction's each
+  constexpr int U = !PRE && SUB == 2 ? 6 : 4;     // steps per unrolled loop body
+  static_assert(U % SLOTS == 0 && U * SUB % WS == 0 && U * SUB % 4 == 0, "slots, sets and scale bytes are compile-time");
+  static_assert(PRE || D == 1, "without PRE the weights run one step ahead");
+  static_assert(XQ >= 1 && 8 * XQ * WAVES == BM, "X rows per wave");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[SLOTS * SLOT + kPanel * BM * 16];
+  uint8_t *sxl = smem + SLOTS * SLOT;
+
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);   // uniform: addresses stay scalar
   const int r = lane & 15, b = lane >> 4;
-  const int MT = (p.M + BM - 1) / BM;
-  const int tile = blockIdx.x;
-  const int64_t m0 = (int64_t)(tile % MT) * BM, n0 = (int64_t)(tile / MT) * BN;
-  const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
+  const int wm = wave % WM, wn = wave / WM;
+  // workgroup ids are dealt to the 8 XCDs by id modulo 8: each XCD takes a contiguous range of
+  // tiles, in bands of 8 tile rows, so that it shares X rows and weight columns in its L2
+  const int MT = (p.M + BM - 1) / BM, NT = (p.N + BN - 1) / BN, tiles = MT * NT;
+  const int per = (tiles + 7) / 8, xcd = blockIdx.x & 7;
+  const int tile = xcd * per + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || tile >= tiles) return;
+  const int band = tile / (8 * NT), rows_in = min(8, MT - band * 8), in = tile - band * 8 * NT;
+  const int64_t m0 = (int64_t)(band * 8 + in % rows_in) * BM, n0 = (int64_t)(in / rows_in) * BN;
+
   const int xbytes = FMT == MX_FP4 ? p.K / 2 : p.K, blocks = p.K / kBlock;
-
-  const int64_t g = min((n0 + wn) / 64, (int64_t)p.NG - 1);   // past the end: a copy, not stored
-  const uint8_t *wbase = p.wq + g * p.KS * 4096 + lane * 16;
-  const uint32_t *sbase = reinterpret_cast<const uint32_t *>(p.sc) + g * p.KB * 256 + lane;
-
-  const uint8_t *xsrc[LD];
-  int xcol[LD], xdst[LD];
+  const int steps = (xbytes + 127) / 128;
+  const int tail = (xbytes & 127) >> 4;   // 16-byte chunks of a last step that K ends inside, 0: whole
+  const int64_t last_row = (int64_t)min((int64_t)BM, p.M - m0) - 1;   // of this tile; further rows repeat it
+  // every address is in range by construction (rows are clamped, offsets stay below 2^31)
+  const __amdgpu_buffer_rsrc_t xr = buffer_rsrc(p.codes + m0 * p.ldc, 0x7fffffffL);
+  const __amdgpu_buffer_rsrc_t sr = buffer_rsrc(p.scales + m0 * p.lds, 0x7fffffffL);
+  uint32_t xvoff[XQ];
 #pragma unroll
-  for (int i = 0; i < LD; ++i) {
-    const int id = i * kThreads + t, m = id / XC, c = id % XC;
-    xsrc[i] = p.codes + min(m0 + m, (int64_t)p.M - 1) * p.ldc;
-    xcol[i] = c * 16;
-    xdst[i] = x_chunk<FMT>(m, c);
+  for (int q = 0; q < XQ; ++q) {
+    const int row = (wave * XQ + q) * 8 + (lane >> 3);
+    xvoff[q] = (uint32_t)(min((int64_t)row, last_row) * p.ldc) + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
   }
-  const uint8_t *srow[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) srow[i] = p.scales + min(m0 + wm + 16 * i + r, (int64_t)p.M - 1) * p.lds;
+  // packed operands: NF = 4 a whole group of 64 rows, NF = 2 half of one
+  const int64_t col = n0 + wn * NF * 16;
+  const int64_t g = min(col / 64, (int64_t)p.NG - 1);     // past the end: a copy, not stored
+  const int f0 = (int)(col % 64) / 16;
+  const uint8_t *wbase = p.wq + g * p.KS * 4096 + f0 * 1024 + lane * 16;
+  const uint32_t *sbase = reinterpret_cast<const uint32_t *>(p.sc) + (g * p.KB * 4 + f0) * 64 + lane;
 
-  u4_t xr[LD], w[4];
-  auto load = [&](int step) {
+  f4_t acc[MF][NF];
 #pragma unroll
-    for (int i = 0; i < LD; ++i) {
-      const int o = step * XB + xcol[i];
-      const u4_t zero = {0, 0, 0, 0};
-      xr[i] = o < xbytes ? *reinterpret_cast<const u4_t *>(xsrc[i] + o) : zero;
-    }
+  for (int i = 0; i < MF; ++i)
 #pragma unroll
-    for (int f = 0; f < 4; ++f) w[f] = *reinterpret_cast<const u4_t *>(wbase + (int64_t)step * 4096 + f * 1024);
-  };
+    for (int f = 0; f < NF; ++f) acc[i][f] = f4_t{0.f, 0.f, 0.f, 0.f};
 
-  f4_t acc[4][4];
+  u4_t w[WS][NF];
+  auto load_x = [&](int step, int slot) {
+    uint8_t *dst = smem + slot * SLOT + wave * XQ * 1024;
+    const uint32_t soff = (uint32_t)min(step, steps - 1) * 128;
+    if (tail && step >= steps - 1) {
+      // chunks past K hold the next row's bytes, or nothing: an offset past the descriptor's
+      // range reads nothing and puts zeros into LDS
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+      for (int q = 0; q < XQ; ++q) {
+        const int row = (wave * XQ + q) * 8 + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+        dma16(xr, c < tail ? xvoff[q] : 0x7fffffffu, soff, dst + q * 1024);
+      }
+    } else {
 #pragma unroll
-    for (int f = 0; f < 4; ++f) acc[i][f] = f4_t{0.f, 0.f, 0.f, 0.f};
-
-  load(0);
-  uint32_t sw[4];
-  u4_t sx[4];
-  auto step_body = [&](auto jc, int kb) {
-    constexpr int J = decltype(jc)::value;
-    const int step = kb * 4 + J;
-    if (step >= p.KS) return;
-    uint8_t *buf = xt[J & 1];   // 4 steps per scale dword: the parity of the step is J's
-#pragma unroll
-    for (int i = 0; i < LD; ++i) *reinterpret_cast<u4_t *>(buf + xdst[i]) = xr[i];
-    u4_t wc[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f) wc[f] = w[f];
-    __syncthreads();
-    if (step + 1 < p.KS) load(step + 1);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int m = wm + 16 * i + r;
-      const u4_t x0 = *reinterpret_cast<const u4_t *>(buf + x_chunk<FMT>(m, b));
-      u4_t x1 = {0, 0, 0, 0};
-      if constexpr (FMT == MX_FP8) x1 = *reinterpret_cast<const u4_t *>(buf + x_chunk<FMT>(m, b + 4));
-      const uint32_t s = step * 4 + b < blocks ? sx[i][J] >> (8 * b) : 0u;
-#pragma unroll
-      for (int f = 0; f < 4; ++f) acc[i][f] = mx_mfma<FMT, J>(wc[f], x0, x1, acc[i][f], sw[f], s);
+      for (int q = 0; q < XQ; ++q) dma16(xr, xvoff[q], soff, dst + q * 1024);
     }
   };
-  for (int kb = 0; kb < p.KB; ++kb) {
+  // operands of instruction s of a step into register set `set`
+  auto load_w = [&](int step, int s, int set) {
+    const uint8_t *src = wbase + (int64_t)min(min(step, steps - 1) * SUB + s, p.KS - 1) * 4096;
 #pragma unroll
-    for (int f = 0; f < 4; ++f) sw[f] = sbase[(int64_t)kb * 256 + f * 64];
+    for (int f = 0; f < NF; ++f) w[set][f] = *reinterpret_cast<const u4_t *>(src + f * 1024);
+  };
+  // this lane's chunk addresses in a slot: chunk b and chunk b + 4 of row r of operand 0
+  const int row0 = wm * MF * 16 + r;
+  const int xa = row0 * 128 + ((b ^ ((row0 >> 1) & 7)) << 4), xb = xa ^ 64;
+  constexpr int XR = FMT == MX_FP8 ? 2 : 1;       // 16-byte pieces of an X operand
+  struct Frag {            // one X operand: 16 rows, one instruction
+    u4_t x[XR];
+    uint32_t s;
+  };
+  // operand i of the instruction whose index mod 4 is `byte`; sub: which of the step's
+  auto read_x = [&](Frag &o, int i, int sub, const uint8_t *xs, const uint8_t *ss, int byte) {
+    o.x[0] = *reinterpret_cast<const u4_t *>(xs + (sub ? xb : xa) + i * 2048);
+    if constexpr (XR == 2) o.x[1] = *reinterpret_cast<const u4_t *>(xs + xb + i * 2048);
+    o.s = ss[i * 256 + (byte & 3) * 4];
+  };
+  auto multiply = [&](auto hc, int i, const Frag &x, const uint32_t (&sw)[NF]) {
+    constexpr int h = decltype(hc)::value;        // instruction index within the loop body
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sx[i] = *reinterpret_cast<const u4_t *>(srow[i] + kb * 16);
-    step_body(std::integral_constant<int, 0>{}, kb);
-    step_body(std::integral_constant<int, 1>{}, kb);
-    step_body(std::integral_constant<int, 2>{}, kb);
-    step_body(std::integral_constant<int, 3>{}, kb);
+    for (int f = 0; f < NF; ++f) acc[i][f] = mx_mfma<FMT, h & 3>(w[h % WS][f], x.x[0], x.x[XR - 1], acc[i][f], sw[f], x.s);
+  };
+
+  // K in panels whose X scales fit LDS
+  for (int c0 = 0; c0 < p.KB; c0 += kPanel) {
+    const int chunks = min(kPanel, p.KB - c0);
+    const int s0 = c0 * (4 / SUB), s1 = min(steps, s0 + chunks * (4 / SUB));   // steps of the panel
+    uint32_t sw[NF], sw_next[NF];         // weight scales of this 512-k chunk and the next
+    auto load_sw = [&](int kb) {
+#pragma unroll
+      for (int f = 0; f < NF; ++f) sw_next[f] = sbase[(int64_t)min(kb, p.KB - 1) * 256 + f * 64];
+    };
+    load_sw(c0);
+    lds_barrier();                        // the panel before has been read
+    for (int q = wave; q < chunks * (BM / 64); q += WAVES) {
+      const int c = q / (BM / 64), row = (q % (BM / 64)) * 64 + lane;
+      dma16(sr, (uint32_t)(min((int64_t)row, last_row) * p.lds), (uint32_t)(c0 + c) * 16,
+            sxl + (c * BM + (q % (BM / 64)) * 64) * 16);
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      pin();
+      load_x(s0 + d, d);
+      pin();
+#pragma unroll
+      for (int h = 0; h < SUB; ++h) load_w(s0 + d, h, (d * SUB + h) % WS);
+    }
+    pin();
+    const int left = (blocks & 15);
+    if (left && c0 + chunks == p.KB) {    // scale bytes past K may hold anything, a NaN among it
+      wait_vmcnt<0>();
+      lds_barrier();
+      for (int id = t; id < BM * 16; id += WAVES * 64)
+        if ((id & 15) >= left) sxl[(chunks - 1) * BM * 16 + id] = 0;
+      lds_barrier();
+    }
+    const uint8_t *ss = sxl + row0 * 16 + b;
+    constexpr int AHEAD = FMT == MX_FP8 ? 2 : 3;  // without PRE: operands read ahead
+    Frag fr[PRE ? 2 * SUB : 1][PRE ? MF : AHEAD + 1];
+    if constexpr (PRE) {
+      wait_vmcnt<(D - 1) * (XQ + WQ)>();
+      lds_barrier();
+#pragma unroll
+      for (int h = 0; h < SUB; ++h)
+#pragma unroll
+        for (int i = 0; i < MF; ++i) read_x(fr[h][i], i, h, smem, ss, h);
+    }
+    for (int base = s0; base < s1; base += U) {
+      unroll<0, U>([&](auto uc) {
+        constexpr int u = decltype(uc)::value;
+        const int step = base + u;
+        if (step >= s1) return;
+        // waits count the loads younger than the ones needed; more of them only wait longer
+        if constexpr (PRE) {
+          if (step + 1 < s1) {
+            wait_vmcnt<(D - 2) * (XQ + WQ) + WQ>();
+            lds_barrier();
+            const uint8_t *xs = smem + (u + 1) % SLOTS * SLOT, *sp = ss + (step + 1 - s0) * SUB / 4 * BM * 16;
+#pragma unroll
+            for (int h = 0; h < SUB; ++h)
+#pragma unroll
+              for (int i = 0; i < MF; ++i) read_x(fr[((u + 1) & 1) * SUB + h][i], i, h, xs, sp, (u + 1) * SUB + h);
+          }
+        } else {
+          wait_vmcnt<0>();
+          lds_barrier();
+        }
+        constexpr bool next_chunk = u * SUB % 4 == 0;
+        if constexpr (next_chunk) {
+#pragma unroll
+          for (int f = 0; f < NF; ++f) sw[f] = sw_next[f];
+        }
+        pin();
+        load_x(step + D, (u + D) % SLOTS);
+        pin();
+        if constexpr (PRE) {
+#pragma unroll
+          for (int h = 0; h < SUB; ++h) load_w(step + D, h, ((u + D) * SUB + h) % WS);
+        }
+        if constexpr (next_chunk) load_sw(c0 + (step - s0) * SUB / 4 + 1);
+        pin();
+        if constexpr (PRE) {
+          unroll<0, SUB * MF>([&](auto jc) {
+            constexpr int h = decltype(jc)::value / MF, i = decltype(jc)::value % MF;
+            multiply(std::integral_constant<int, u * SUB + h>{}, i, fr[(u & 1) * SUB + h][i], sw);
+          });
+        } else {
+          const uint8_t *xs = smem + u % SLOTS * SLOT, *sp = ss + (step - s0) * SUB / 4 * BM * 16;
+#pragma unroll
+          for (int j = 0; j < AHEAD; ++j) read_x(fr[0][j], j % MF, j / MF, xs, sp, u * SUB + j / MF);
+          unroll<0, SUB * MF>([&](auto jc) {
+            constexpr int j = decltype(jc)::value, h = j / MF, i = j % MF, n = j + AHEAD;
+            __builtin_amdgcn_sched_barrier(0);
+            // set (u SUB + h + SUB) mod WS: its last use was the instruction before this one
+            if constexpr (i == 0) load_w(step + 1, h, (u * SUB + h + SUB) % WS);
+            if constexpr (n < SUB * MF) read_x(fr[0][n % (AHEAD + 1)], n % MF, n / MF, xs, sp, u * SUB + n / MF);
+            multiply(std::integral_constant<int, u * SUB + h>{}, i, fr[0][j % (AHEAD + 1)], sw);
+            // the products stay between the reads around them (the compiler would sink them
+            // past the step's end, holding every operand of the step in registers)
+#pragma unroll
+            for (int f = 0; f < NF; ++f) keep(acc[i][f]);
+          });
+        }
+      });
+    }
+    wait_vmcnt<0>();   // loads past the last step land before their slots are reused
   }
 
-  const int64_t n = n0 + wn + 16 * b;   // 16 consecutive columns per lane
+  // a lane holds NF * 4 consecutive columns of each of its rows
+  const int64_t n = col - (int64_t)f0 * 16 + 16 * b + 4 * f0;
+  const bool whole = n + 4 * NF <= p.N && (p.N & 7) == 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + wm + 16 * i + r;
+  for (int i = 0; i < MF; ++i) {
+    const int64_t m = m0 + row0 + 16 * i;
     if (m >= p.M) continue;
+    if (whole) {
 #pragma unroll
-    for (int f = 0; f < 4; ++f)
+      for (int h = 0; h < NF / 2; ++h) {
+        float v[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n + 4 * f + e < p.N) store_cols<DT>(p, m, n + 4 * f + e, acc[i][f][e]);
+        for (int e = 0; e < 8; ++e) v[e] = acc[i][2 * h + e / 4][e % 4] + (p.bias ? to_f32<DT>(p.bias[n + 8 * h + e]) : 0.f);
+        store8<DT>(p.y + m * p.N + n + 8 * h, v);
+      }
+    } else {
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + 4 * f + e < p.N) store_cols<DT>(p, m, n + 4 * f + e, acc[i][f][e]);
+    }
   }
+}
+
+template <int DT, int FMT, int BM, int WM, int WN, int NF, int D, bool PRE>
+hipError_t launch_tile(const MxMatmulParams &p, hipStream_t s) {
+  const int64_t tiles = ((int64_t)p.M + BM - 1) / BM * (((int64_t)p.N + WN * NF * 16 - 1) / (WN * NF * 16));
+  hipLaunchKernelGGL((gemm_kernel<DT, FMT, BM, WM, WN, NF, D, PRE>), dim3((uint32_t)((tiles + 7) / 8 * 8)), dim3(WM * WN * 64),
+                     0, s, p);
+  return hipGetLastError();
 }
 
 template <int DT, int FMT>
 hipError_t launch(const MxMatmulParams &p, hipStream_t s) {
-  const int64_t tiles = ((int64_t)p.M + BM - 1) / BM * (((int64_t)p.N + BN - 1) / BN);
-  hipLaunchKernelGGL((gemm_kernel<DT, FMT>), dim3((uint32_t)tiles), dim3(kThreads), 0, s, p);
-  return hipGetLastError();
+  const int rows = mx_gemm_rows(p.M, p.N);
+  if (rows == 256) return launch_tile<DT, FMT, 256, 2, 4, 4, 1, false>(p, s);
+  if (rows == 128) return launch_tile<DT, FMT, 128, 1, 4, 2, 3, true>(p, s);
+  return launch_tile<DT, FMT, 64, 1, 4, 2, 3, true>(p, s);
 }
 
 }  // namespace
+
+int mx_gemm_rows(int M, int N) {
+  const int64_t big = ((int64_t)M + 255) / 256 * (((int64_t)N + 255) / 256);
+  if (big >= kCUs) return 256;
+  const int64_t mid = ((int64_t)M + 127) / 128 * (((int64_t)N + 127) / 128);
+  return mid >= kCUs / 2 ? 128 : 64;
+}
 
 int mx_gemm_splits(int M, int N, int K, int fmt) {
   (void)M; (void)N; (void)K; (void)fmt;

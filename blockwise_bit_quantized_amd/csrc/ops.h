@@ -10,6 +10,7 @@ enum { DT_F16 = 0, DT_BF16 = 1, DT_F32 = 2 };
 enum { MX_FP4 = 0, MX_FP8 = 1 };
 
 constexpr int kMxStep = 128;   // k of one matrix instruction (4 blocks)
+constexpr int kMxMaxK = 1 << 22;   // K limit of the product; its row distances stay below twice that
 constexpr int kMxScaleK = 512; // k of one scale dword per lane (4 steps, one byte each)
 
 typedef float f4_t __attribute__((ext_vector_type(4)));
@@ -164,6 +165,7 @@ constexpr int kMxGemvMaxM = 16;
 hipError_t launch_mx_gemv(int dtype, int fmt, const MxMatmulParams &p, hipStream_t s);
 hipError_t launch_mx_gemm(int dtype, int fmt, const MxMatmulParams &p, hipStream_t s);
 int mx_gemv_ksplit(int N, int K);                    // waves that share a weight row's K: 1, 2, 4 or 8
+int mx_gemm_rows(int M, int N);                      // rows of an output tile: 64, 128 or 256
 int mx_gemm_splits(int M, int N, int K, int fmt);    // K ranges per output tile
 
 struct NormParams {

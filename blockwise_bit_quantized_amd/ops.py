@@ -11,7 +11,6 @@ on several streams, and graph captures, need no workspace of their own.
 from __future__ import annotations
 
 import ctypes as C
-from dataclasses import dataclass
 from typing import Any, NamedTuple
 
 try:
@@ -116,36 +115,47 @@ def _check(st: int):
 
 def _call(dev, f, *args):
     """f(*args, stream) on the current stream of ``dev``, with ``dev`` current."""
-    if dev.type != "cuda":
+    i = dev.index
+    if i is None or dev.type != "cuda":
         raise ValueError("tensors must be on a GPU, got %s" % dev)
-    if dev.index == torch.cuda.current_device():
-        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if i == torch.cuda.current_device():
+        st = f(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = f(*args, _raw_stream(i))
     if st != _OK:
         raise RuntimeError(_status_text(st))
 
 
-def _rows(t, name, dtype=None, shape=None, dev=None):
-    """A 2-D tensor whose rows are contiguous and do not overlap; returns its row distance."""
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+def _raw_stream(index):
+    # the handle alone: building torch's Stream object costs as much as half a launch
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _ld(t, name):
+    """The row distance of a 2-D tensor whose rows are contiguous and do not overlap."""
     if t.dim() != 2:
         raise ValueError("%s must be 2-D, got shape %s" % (name, tuple(t.shape)))
-    if shape is not None and t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if dev is not None and t.device != dev:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
     n, k = t.shape
     ld, inner = t.stride()
-    if k > 1 and inner != 1:
+    if inner != 1 and k > 1:
         raise ValueError("the rows of %s must be contiguous" % name)
     if n <= 1:
-        return max(k, 1)
+        return k or 1
     if ld < k:
         raise ValueError("the rows of %s must not overlap" % name)
     return ld
+
+
+def _beside(t, name, dtype, shape, dev):
+    """_ld of a tensor that has to match another's type, shape and device."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.device != dev:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    return _ld(t, name)
 
 
 def _float_type(t, name, f32=True):
@@ -158,94 +168,84 @@ def _float_type(t, name, f32=True):
 def _vector(t, name, dtype, n, dev):
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
         raise ValueError("%s must be a contiguous [%d], got shape %s" % (name, n, tuple(t.shape)))
     if t.device != dev:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
 
 
-def _blocks(K, name="the last axis"):
+def _blocks(K, name):
     if K % 32:
         raise ValueError("%s must be a multiple of 32, got %d" % (name, K))
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _format(fmt):
+    if fmt != MNB_MX_FP4 and fmt != MNB_MX_FP8:
+        raise ValueError("unknown MX format %r" % (fmt,))
 
 
-@dataclass
+def _scale_row(K):
+    return (K + 511) // 512 * 16
+
+
 class MxTensor:
     """An MX tensor [rows, K]: ``codes`` uint8 [rows, K / 2] (MNB_MX_FP4, even k in the low
     nibble) or [rows, K] (MNB_MX_FP8; ``codes.view(torch.float8_e4m3fn)`` are its elements),
     ``scales`` uint8 [rows, K / 32] (``scales.view(torch.float8_e8m0fnu)``), whose rows lie a
-    multiple of 16 bytes and at least 16 ceil(K / 512) apart."""
-    codes: Any
-    scales: Any
-    fmt: int
+    multiple of 16 bytes and at least 16 ceil(K / 512) apart.  Checked when it is made; the
+    tensors may be written to, but not resized."""
+    __slots__ = ("codes", "scales", "fmt", "rows", "K", "ldc", "lds")
 
-    @property
-    def K(self) -> int:
-        return self.codes.shape[1] * (2 if self.fmt == MNB_MX_FP4 else 1)
-
-    @property
-    def rows(self) -> int:
-        return self.codes.shape[0]
-
-    def check(self, dev):
-        """(row distance of the codes, of the scales) after checking both tensors."""
-        if self.fmt not in (MNB_MX_FP4, MNB_MX_FP8):
-            raise ValueError("unknown MX format %r" % (self.fmt,))
-        K = self.K
-        ldc = _rows(self.codes, "MX codes", torch.uint8, None, dev)
+    def __init__(self, codes, scales, fmt: int):
+        _format(fmt)
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise TypeError("MX codes and scales must be uint8")
+        ldc = _ld(codes, "MX codes")
+        rows, per_row = codes.shape
+        K = per_row * 2 if fmt == MNB_MX_FP4 else per_row
         _blocks(K, "the last axis of an MX tensor")
-        s = self.scales
-        _rows(s, "MX scales", torch.uint8, (self.rows, K // 32), dev)
-        if K == 0 or self.rows == 0:
-            return 0, 0
-        need = -(-K // 512) * 16
+        _beside(scales, "MX scales", torch.uint8, (rows, K // 32), codes.device)
+        need = _scale_row(K)
         # the row distance counts for one row too, as its scales are read in 16-byte pieces
-        lds = s.stride(0) if self.rows > 1 else need
-        if lds % 16 or lds < need or s.untyped_storage().nbytes() - s.storage_offset() < (self.rows - 1) * lds + need:
+        lds = scales.stride(0) if rows > 1 else need
+        if K and rows and (lds % 16 or lds < need or scales.untyped_storage().nbytes() - scales.storage_offset()
+                           < (rows - 1) * lds + need):
             raise ValueError("the rows of MX scales must lie a multiple of 16 bytes and at least %d apart "
                              "(mx_tensor lays them out so)" % need)
-        if self.rows <= 1:
-            ldc = -(-self.codes.shape[1] // 16) * 16
-        return ldc, lds
+        self.codes, self.scales, self.fmt, self.rows, self.K, self.ldc, self.lds = codes, scales, fmt, rows, K, ldc, lds
 
+    @classmethod
+    def _new(cls, like, rows, K, fmt):
+        """Uninitialised, on the device of ``like``."""
+        _format(fmt)
+        q = object.__new__(cls)
+        ldc, lds = K // 2 if fmt == MNB_MX_FP4 else K, _scale_row(K)
+        s = like.new_empty((rows, lds), dtype=torch.uint8)
+        q.codes = like.new_empty((rows, ldc), dtype=torch.uint8)
+        q.scales = s if lds == K // 32 else s[:, :K // 32]
+        q.fmt, q.rows, q.K, q.ldc, q.lds = fmt, rows, K, ldc, lds
+        return q
 
-def _new_scales(rows, K, dev):
-    return torch.empty((rows, -(-K // 512) * 16), dtype=torch.uint8, device=dev)[:, :K // 32]
-
-
-def _new_mx(rows, K, fmt, dev):
-    if fmt not in (MNB_MX_FP4, MNB_MX_FP8):
-        raise ValueError("unknown MX format %r" % (fmt,))
-    return MxTensor(torch.empty((rows, K // 2 if fmt == MNB_MX_FP4 else K), dtype=torch.uint8, device=dev),
-                    _new_scales(rows, K, dev), fmt)
+    def __repr__(self):
+        return "MxTensor([%d, %d], %s, %s)" % (self.rows, self.K, "FP4" if self.fmt == MNB_MX_FP4 else "FP8",
+                                               self.codes.device)
 
 
 def mx_tensor(codes, scales, fmt: int) -> MxTensor:
     """An MxTensor of existing codes and scales (uint8, as a checkpoint holds them); scales
     whose rows are not spaced as MxTensor needs are copied."""
-    t = MxTensor(codes, scales, fmt)
-    if fmt not in (MNB_MX_FP4, MNB_MX_FP8):
-        raise ValueError("unknown MX format %r" % (fmt,))
+    _format(fmt)
     if codes.dim() != 2 or scales.dim() != 2:
-        raise ValueError("codes and scales must be 2-D")
-    rows, K = t.rows, t.K
-    _blocks(K, "the last axis of an MX tensor")
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
-        raise TypeError("codes and scales must be uint8")
-    if tuple(scales.shape) != (rows, K // 32) or scales.device != codes.device:
-        raise ValueError("scales must be [%d, %d] beside the codes, got %s" % (rows, K // 32, tuple(scales.shape)))
-    need = -(-K // 512) * 16
-    if (K // 32 > 1 and scales.stride(1) != 1) or scales.stride(0) % 16 or scales.stride(0) < need or \
-            scales.data_ptr() % 16 or \
-            scales.untyped_storage().nbytes() - scales.storage_offset() < (rows - 1) * scales.stride(0) + need:
-        t.scales = _new_scales(rows, K, codes.device)
-        t.scales.copy_(scales)
-    t.check(codes.device)
-    return t
+        raise ValueError("MX codes and scales must be 2-D")
+    rows, K = codes.shape[0], codes.shape[1] * (2 if fmt == MNB_MX_FP4 else 1)
+    if scales.dtype == torch.uint8 and scales.shape == (rows, K // 32):
+        need, ld = _scale_row(K), scales.stride(0)
+        if (K > 32 and scales.stride(1) != 1) or ld % 16 or ld < need or scales.data_ptr() % 16 or \
+                scales.untyped_storage().nbytes() - scales.storage_offset() < (rows - 1) * ld + need:
+            spaced = scales.new_empty((rows, need))[:, :K // 32]
+            spaced.copy_(scales)
+            scales = spaced
+    return MxTensor(codes, scales, fmt)
 
 
 def mx_quantize(x, fmt: int = MNB_MX_FP4) -> MxTensor:
@@ -253,89 +253,79 @@ def mx_quantize(x, fmt: int = MNB_MX_FP4) -> MxTensor:
     each 32 elements, 2^(floor(log2 max|x|) - 2 (FP4) or - 8 (FP8)), elements rounded to
     nearest even and clamped.  A block with an infinity or NaN stands for NaN throughout."""
     code = _float_type(x, "x")
-    ldx = _rows(x, "x")
+    ldx = _ld(x, "x")
     M, K = x.shape
     _blocks(K, "the last axis of x")
-    dev = x.device
-    q = _new_mx(M, K, fmt, dev)
-    _call(dev, lib.mnb_mx_quantize, x.data_ptr(), code, M, K, ldx, fmt, q.codes.data_ptr(), q.codes.shape[1],
-          q.scales.data_ptr(), -(-K // 512) * 16)
+    q = MxTensor._new(x, M, K, fmt)
+    _call(x.device, lib.mnb_mx_quantize, x.data_ptr(), code, M, K, ldx, fmt, q.codes.data_ptr(), q.ldc,
+          q.scales.data_ptr(), q.lds)
     return q
 
 
 def mx_dequantize(q: MxTensor, dtype=None, out=None):
     """The values of an MX tensor in ``dtype`` (fp16 by default), each rounded once."""
     dtype = dtype or torch.float16
-    dev = q.codes.device
-    ldc, lds = q.check(dev)
     M, K = q.rows, q.K
-    y = out if out is not None else torch.empty((M, K), dtype=dtype, device=dev)
-    ldy = _rows(y, "out", dtype, (M, K), dev)
-    _call(dev, lib.mnb_mx_dequantize, q.codes.data_ptr(), ldc, q.scales.data_ptr(), lds, q.fmt, M, K, y.data_ptr(),
-          _float_type(y, "out"), ldy)
-    return y
+    if out is None:
+        out, ldy = q.codes.new_empty((M, K), dtype=dtype), K
+    else:
+        ldy = _beside(out, "out", dtype, (M, K), q.codes.device)
+    _call(q.codes.device, lib.mnb_mx_dequantize, q.codes.data_ptr(), q.ldc, q.scales.data_ptr(), q.lds, q.fmt, M, K,
+          out.data_ptr(), _float_type(out, "out"), ldy)
+    return out
 
 
-@dataclass
 class MxWeight:
-    """An FP4 weight [N, K] in the layout of mx_matmul."""
-    wq: Any             # torch.uint8 device tensor
-    sc: Any             # torch.uint8 device tensor
-    N: int
-    K: int
+    """An FP4 weight [N, K] in the layout of mx_matmul: ``wq`` and ``sc`` uint8 device buffers of
+    mnb_mx_packed_sizes bytes.  Checked when it is made."""
+    __slots__ = ("wq", "sc", "N", "K")
 
-    def check(self, dev):
-        wqb, scb = _packed_sizes(self.N, self.K)
-        for t, name, n in ((self.wq, "packed codes", wqb), (self.sc, "packed scales", scb)):
-            if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != dev or t.numel() < n:
-                raise ValueError("%s must be a contiguous uint8 tensor of at least %d bytes on %s" % (name, n, dev))
-
-
-def _packed_sizes(N, K):
-    if N < 0 or K < 0 or K % 32 or K >= 1 << 25:
-        _check(mnb_mx_packed_sizes(N, K)[0])
-    groups = (N + 63) // 64
-    return groups * ((K + 127) // 128) * 4096, groups * ((K + 511) // 512) * 1024
+    def __init__(self, wq, sc, N: int, K: int):
+        st, wqb, scb = mnb_mx_packed_sizes(N, K)
+        _check(st)
+        for t, name, n in ((wq, "packed codes", wqb), (sc, "packed scales", scb)):
+            if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != wq.device or t.numel() < n:
+                raise ValueError("%s must be a contiguous uint8 tensor of at least %d bytes on %s" % (name, n, wq.device))
+        self.wq, self.sc, self.N, self.K = wq, sc, N, K
 
 
 def mx_pack(q: MxTensor) -> MxWeight:
     """An FP4 tensor [N, K] (mx_quantize, or mx_tensor of a checkpoint's) packed for mx_matmul."""
     if q.fmt != MNB_MX_FP4:
         raise ValueError("weights are packed from MNB_MX_FP4")
-    dev = q.codes.device
-    ldc, lds = q.check(dev)
-    N, K = q.rows, q.K
-    st, wqb, scb = mnb_mx_packed_sizes(N, K)
+    st, wqb, scb = mnb_mx_packed_sizes(q.rows, q.K)
     _check(st)
-    w = MxWeight(torch.empty(wqb, dtype=torch.uint8, device=dev), torch.empty(scb, dtype=torch.uint8, device=dev), N, K)
-    _call(dev, lib.mnb_mx_pack, q.codes.data_ptr(), ldc, q.scales.data_ptr(), lds, N, K, w.wq.data_ptr(), w.sc.data_ptr())
+    w = MxWeight(q.codes.new_empty(wqb), q.codes.new_empty(scb), q.rows, q.K)
+    _call(q.codes.device, lib.mnb_mx_pack, q.codes.data_ptr(), q.ldc, q.scales.data_ptr(), q.lds, q.rows, q.K,
+          w.wq.data_ptr(), w.sc.data_ptr())
     return w
 
 
 def mx_matmul(x: MxTensor, w: MxWeight, bias=None, dtype=None, out=None):
     """Y [M, N] = x . w^T (+ bias [N]) in ``dtype`` (fp16 by default, or bf16; the bias's type too),
     summed in 32 bits and rounded once; x FP8 or FP4 from mx_quantize, rmsnorm or mx_tensor."""
+    codes = x.codes
+    dev, M, K, N = codes.device, x.rows, x.K, w.N
     dtype = dtype or torch.float16
-    dev = x.codes.device
-    ldc, lds = x.check(dev)
-    M, K, N = x.rows, x.K, w.N
+    code = _DTYPES.get(dtype)
+    if code is None or code == MNB_F32:
+        raise TypeError("the output must be float16 or bfloat16, got %s" % dtype)
     if K != w.K:
         raise ValueError("x has K=%d, weight has K=%d" % (K, w.K))
-    w.check(dev)
+    if w.wq.device != dev:
+        raise ValueError("the weight is on %s, expected %s" % (w.wq.device, dev))
     if out is None:
-        y = torch.empty((M, N), dtype=dtype, device=dev)
-    else:
-        y = out
-        if y.dtype != dtype or tuple(y.shape) != (M, N) or not y.is_contiguous() or y.device != dev:
-            raise ValueError("out must be a contiguous %s [%d, %d] on %s" % (dtype, M, N, dev))
-    code = _float_type(y, "the output", f32=False)
+        out = codes.new_empty((M, N), dtype=dtype)
+    elif out.dtype != dtype or out.shape != (M, N) or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be a contiguous %s [%d, %d] on %s" % (dtype, M, N, dev))
     if bias is not None:
         _vector(bias, "bias", dtype, N, dev)
+        bias = bias.data_ptr()
     need = lib.mnb_mx_workspace_bytes(M, N, K, x.fmt)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _call(dev, lib.mnb_mx_matmul, x.codes.data_ptr(), ldc, x.scales.data_ptr(), lds, x.fmt, w.wq.data_ptr(),
-          w.sc.data_ptr(), _ptr(bias), y.data_ptr(), code, M, N, K, _ptr(ws), need)
-    return y
+    ws = codes.new_empty(need) if need else None
+    _call(dev, lib.mnb_mx_matmul, codes.data_ptr(), x.ldc, x.scales.data_ptr(), x.lds, x.fmt, w.wq.data_ptr(),
+          w.sc.data_ptr(), bias, out.data_ptr(), code, M, N, K, ws.data_ptr() if need else None, need)
+    return out
 
 
 class Normed(NamedTuple):
@@ -352,31 +342,33 @@ def rmsnorm(x, weight, eps: float = 1e-6, residual=None, fmt: int | None = None,
     residual) receives h in x's type and may be ``residual`` or ``x`` itself; ``out`` receives y
     and may be ``x``.  Each output is rounded once from 32 bits."""
     code = _float_type(x, "x", f32=False)
-    ldx = _rows(x, "x")
-    M, K = x.shape
-    dev, dtype, shape = x.device, x.dtype, x.shape
+    ldx = _ld(x, "x")
+    shape, dev, dtype = x.shape, x.device, x.dtype
+    M, K = shape
     _vector(weight, "weight", dtype, K, dev)
+    rp = hp = yp = cp = sp = y = q = None
     ldr = ldh = ldy = ldc = lds = 0
     if residual is not None:
-        ldr = _rows(residual, "residual", dtype, shape, dev)
+        ldr = _beside(residual, "residual", dtype, shape, dev)
         if hidden is None:
-            hidden, ldh = torch.empty((M, K), dtype=dtype, device=dev), K
+            hidden, ldh = x.new_empty(shape), K
         else:
-            ldh = _rows(hidden, "hidden", dtype, shape, dev)
+            ldh = _beside(hidden, "hidden", dtype, shape, dev)
+        rp, hp = residual.data_ptr(), hidden.data_ptr()
     elif hidden is not None:
         raise ValueError("hidden needs a residual")
-    y = q = None
     if fmt is None or keep16 or out is not None:
         if out is None:
-            y, ldy = torch.empty((M, K), dtype=dtype, device=dev), K
+            y, ldy = x.new_empty(shape), K
         else:
-            y, ldy = out, _rows(out, "out", dtype, shape, dev)
+            y, ldy = out, _beside(out, "out", dtype, shape, dev)
+        yp = y.data_ptr()
     if fmt is not None:
         _blocks(K, "the last axis of x")
-        q = _new_mx(M, K, fmt, dev)
-        ldc, lds = q.codes.shape[1], -(-K // 512) * 16
-    _call(dev, lib.mnb_rmsnorm, x.data_ptr(), ldx, _ptr(residual), ldr, weight.data_ptr(), eps, code, M, K, _ptr(hidden),
-          ldh, _ptr(y), ldy, fmt or 0, q.codes.data_ptr() if q else None, ldc, q.scales.data_ptr() if q else None, lds)
+        q = MxTensor._new(x, M, K, fmt)
+        cp, ldc, sp, lds = q.codes.data_ptr(), q.ldc, q.scales.data_ptr(), q.lds
+    _call(dev, lib.mnb_rmsnorm, x.data_ptr(), ldx, rp, ldr, weight.data_ptr(), eps, code, M, K, hp, ldh, yp, ldy,
+          fmt or 0, cp, ldc, sp, lds)
     return Normed(y, q, hidden)
 
 
@@ -392,22 +384,25 @@ def logprobs(logits, tokens=None, top: int = 0) -> LogProbs:
     (int64; 0 for a negative token, NaN for one past V), the entropy, and the ``top`` (at most 32)
     likeliest tokens in falling order, equal ones by the lower index."""
     code = _float_type(logits, "logits")
-    ldl = _rows(logits, "logits")
+    ldl = _ld(logits, "logits")
     M, V = logits.shape
     dev = logits.device
     if not 0 <= top <= min(MNB_LOGPROBS_MAX_TOP, V):
         raise ValueError("top must be from 0 to %d, got %d" % (min(MNB_LOGPROBS_MAX_TOP, V), top))
     if V == 0 and M > 0:
         raise ValueError("logits have no columns")
-    lp = None
+    tp = lp = lpp = tl = tlp = tt = ttp = ws = None
     if tokens is not None:
         _vector(tokens, "tokens", torch.int64, M, dev)
-        lp = torch.empty(M, dtype=torch.float32, device=dev)
-    ent = torch.empty(M, dtype=torch.float32, device=dev)
-    tl = torch.empty((M, top), dtype=torch.float32, device=dev) if top else None
-    tt = torch.empty((M, top), dtype=torch.int64, device=dev) if top else None
+        lp = logits.new_empty(M, dtype=torch.float32)
+        tp, lpp = tokens.data_ptr(), lp.data_ptr()
+    ent = logits.new_empty(M, dtype=torch.float32)
+    if top:
+        tl, tt = logits.new_empty((M, top), dtype=torch.float32), logits.new_empty((M, top), dtype=torch.int64)
+        tlp, ttp = tl.data_ptr(), tt.data_ptr()
     need = lib.mnb_logprobs_workspace_bytes(M, V, code, top)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _call(dev, lib.mnb_logprobs, logits.data_ptr(), code, M, V, ldl, _ptr(tokens), top, _ptr(lp), ent.data_ptr(), _ptr(tl),
-          _ptr(tt), _ptr(ws), need)
+    if need:
+        ws = logits.new_empty(need, dtype=torch.uint8)
+    _call(dev, lib.mnb_logprobs, logits.data_ptr(), code, M, V, ldl, tp, top, lpp, ent.data_ptr(), tlp, ttp,
+          ws.data_ptr() if need else None, need)
     return LogProbs(lp, ent, tl, tt)

@@ -53,7 +53,7 @@ int mnb_mx_dequantize(const void *codes, int64_t ldc, const void *scales, int64_
                       int M, int K, void *Y, int dtype, int64_t ldy, void *stream);
 
 /*
- * Device layout of an FP4 weight [N, K] for mnb_mx_matmul (K % 32 == 0, K < 2^25):
+ * Device layout of an FP4 weight [N, K] for mnb_mx_matmul (K % 32 == 0, K < 2^22):
  * rows in groups of 64, K in steps of 128; the 4 KiB of a (group, step) hold four matrix
  * operands of 16 rows, each 16 bytes (32 consecutive k of one row) for each of 64 lanes.
  * mnb_mx_packed_sizes (host only) gives the two buffers' bytes.  Rows past N and k past K
@@ -66,7 +66,7 @@ int mnb_mx_pack(const void *codes, int64_t ldc, const void *scales, int64_t lds,
 /*
  * Y[M,N] = X . W^T (+ bias), X an MX tensor [M, K] (fmt FP8 or FP4), W an FP4 weight packed
  * by mnb_mx_pack; Y fp16 or bf16 [M, N] row-major, rounded once from FP32 accumulation; bias
- * [N] of Y's type or NULL.  K % 32 == 0, K < 2^25.  A NaN scale or element of X reaches its
+ * [N] of Y's type or NULL.  K % 32 == 0, K < 2^22; ldc and lds at most 2^23.  A NaN scale or element of X reaches its
  * own row of Y only, one of W its own column.  codes, scales, wq, sc and Y 16-byte aligned, as
  * are ldc and lds; bias 16-byte aligned.  Y must not overlap the inputs or the workspace.
  *

@@ -167,6 +167,22 @@ def test_matmul_exact_sums(M, N, K, fmt):
     assert np.array_equal(got, rounded(want + bias, torch.bfloat16))
 
 
+@pytest.mark.parametrize("fmt", [FP4, FP8])
+@pytest.mark.parametrize("M,N,K", [(4097, 4100, 416), (2100, 9000, 1120), (4352, 4096, 8864), (1000, 2100, 8864), (40, 300, 17056)])
+def test_matmul_exact_sums_large(M, N, K, fmt):
+    """Tiles of every height, K past one panel of scales and ending inside a step; the reference is
+    a 64-bit product on the GPU.  Partial sums here stay below 2^18 (they are random walks of at
+    most 17056 terms up to 144), multiples of 2^-4: exact in 32 bits."""
+    r = rng(17, M, N, K, fmt)
+    (xq, xs), (wq, ws) = exact_operands(r, M, N, K, fmt)
+    x, w = to_mx(xq, xs, fmt), mnb.mx_pack(to_mx(wq, ws, FP4))
+    xv = dev(xq) * dev(np.ldexp(1.0, xs - 127)).repeat_interleave(32, 1)
+    wv = dev(wq) * dev(np.ldexp(1.0, ws - 127)).repeat_interleave(32, 1)
+    want = xv @ wv.t().contiguous()
+    for dt in (torch.float16, torch.bfloat16):
+        assert torch.equal(mnb.mx_matmul(x, w, dtype=dt), want.float().to(dt)), dt
+
+
 def random_mx(r, n, K, fmt, spread=1.0):
     q, s = ref.quantize(r.standard_normal((n, K)) * np.exp(spread * r.standard_normal((n, K // 32))).repeat(32, 1), fmt)
     return q, s
