@@ -6,14 +6,16 @@
 // A workgroup holds its part of a row (E pieces of 8 elements a thread) in registers, so
 // the logits are read once: the maximum first, then S and T against it.
 //
-// Alternatives.  An element's key is its order-preserving bits over the complement of its
-// index: keys are distinct and order by value, then by the lower index.  The largest key of
-// each of 64 groups of threads is known after the maximum pass; the top-th largest of those
-// 64 is a threshold that at least `top` elements reach, and few more do (about 64 ln(64 /
-// (64 - top)) of an unordered row).  Elements at or above it are collected in LDS and ranked
-// by counting larger ones, which does not depend on the order of collection.  If they do not
-// fit (rows arranged so that one group holds most large values), the workgroup takes the
-// maxima one at a time below the last one taken instead.
+// Alternatives.  The maxima of 64 groups of threads come with the maximum pass; the top-th
+// largest of them is a threshold that at least `top` elements reach and few more do (about
+// 64 ln(64 / (64 - top)) of an unordered row).  Elements at or above it are collected in LDS as
+// keys, order-preserving bits over the complement of the index, which are distinct and order by
+// value, then by the lower index; each is ranked by counting larger ones, so the order
+// of collection does not matter.  Where too many reach the threshold,
+//   * equal values (masked tokens at -infinity, say) are taken in index order, only as many
+//     as are missing, after the larger ones;
+//   * if the larger ones alone are too many (one group holds most large values), or the row holds
+//     a NaN or +infinity, the keys are taken one at a time, each the largest below the last.
 //
 // Rows longer than one workgroup holds, and calls with few rows, split each row; the parts'
 // (m, S, T) and keys go through the workspace and a second kernel joins them in part order.
@@ -23,7 +25,7 @@ namespace mnb {
 namespace {
 
 constexpr int kCap = 512;       // collected candidates
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // order-preserving bits: larger number, larger integer; every NaN above +infinity, both
 // zeros alike, nothing maps to 0 (the key of an absent element)
@@ -37,17 +39,44 @@ __device__ __forceinline__ float order_value(uint32_t u) {
 }
 __device__ __forceinline__ uint64_t make_key(uint32_t u, uint32_t index) { return (uint64_t)u << 32 | (uint32_t)~index; }
 
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+// lane ^ 1, lane ^ 2, mirrored in 8 lanes, rotated by 4 and 8 in 16
+constexpr int kQuad1 = 0xB1, kQuad2 = 0x4E, kMirror8 = 0x141, kRor4 = 0x124, kRor8 = 0x128;
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+// the maximum of each group of 4, 8 or 16 lanes, in all of them
+template <int N>
+__device__ __forceinline__ float group_max(float v) {
+  v = fmaxf(v, dpp<kQuad1>(v));
+  v = fmaxf(v, dpp<kQuad2>(v));
+  if constexpr (N == 8) v = fmaxf(v, dpp<kMirror8>(v));
+  if constexpr (N == 16) {
+    v = fmaxf(v, dpp<kRor4>(v));
+    v = fmaxf(v, dpp<kRor8>(v));
+  }
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = group_max<16>(v);
+  return fmaxf(fmaxf(lane_value(v, 0), lane_value(v, 16)), fmaxf(lane_value(v, 32), lane_value(v, 48)));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<kQuad1>(v);
+  v += dpp<kQuad2>(v);
+  v += dpp<kRor4>(v);
+  v += dpp<kRor8>(v);
+  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
 __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) {
     const uint64_t o = __shfl_xor((unsigned long long)v, d);
     v = o > v ? o : v;
   }
-  return v;
-}
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
   return v;
 }
 
@@ -57,6 +86,29 @@ template <int DT>
 __device__ __forceinline__ float piece_at(const Piece<DT> &q, int i) {
   if constexpr (DT == DT_F32) return __builtin_bit_cast(float, (uint32_t)q.v[i >> 2][i & 3]);
   else return to_f32<DT>((uint16_t)(q.v[0][i >> 1] >> (16 * (i & 1))));
+}
+
+// An empty use: what a later pass computes from the piece is computed again, not carried
+// over in registers (the converted values would halve the workgroups per CU).
+template <int DT>
+__device__ __forceinline__ void forget(Piece<DT> &q) {
+  asm volatile("" : "+v"(q.v[0]));
+  if constexpr (DT == DT_F32) asm volatile("" : "+v"(q.v[1]));
+}
+// its largest number (a NaN is passed over unless all are)
+template <int DT>
+__device__ __forceinline__ float piece_max(const Piece<DT> &q) {
+  if constexpr (DT == DT_F16) {
+    const u4_t v = q.v[0];
+    const h2_t a = __builtin_elementwise_max(as_h2(v[0]), as_h2(v[1])), b = __builtin_elementwise_max(as_h2(v[2]), as_h2(v[3]));
+    const h2_t c = __builtin_elementwise_max(a, b);
+    return fmaxf((float)c[0], (float)c[1]);
+  } else {
+    float m = fmaxf(piece_at<DT>(q, 0), piece_at<DT>(q, 1));
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) m = fmaxf(m, fmaxf(piece_at<DT>(q, i), piece_at<DT>(q, i + 1)));
+    return m;
+  }
 }
 
 // the row's results from (m, S, T)
@@ -77,88 +129,89 @@ __device__ __forceinline__ float token_logit(const LogprobsParams &p, int64_t ro
 }
 
 template <int DT, int WAVES, int E>
-__global__ __launch_bounds__(WAVES * 64) void part_kernel(LogprobsParams p) {
-  constexpr int THREADS = WAVES * 64;
+__global__ __launch_bounds__(WAVES * 64, DT == DT_F32 || WAVES < 8 ? 1 : 4) void part_kernel(LogprobsParams p) {
+  constexpr int THREADS = WAVES * 64, GROUP = THREADS / 64;
   typedef typename Elem<DT>::type T;
-  __shared__ uint64_t thread_key[THREADS];
   __shared__ uint64_t cand[kCap];
+  __shared__ float group[64];
+  __shared__ int larger[64];             // how many groups have a larger maximum
   __shared__ float red[WAVES][2];
   __shared__ uint64_t wave_key[WAVES];
-  __shared__ uint64_t threshold;
+  __shared__ int wave_count[WAVES];
   __shared__ int count;
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int64_t row = blockIdx.x / p.chunks;
   const int part = (int)(blockIdx.x - row * p.chunks);
   const int c0 = part * p.chunk, c1 = min(p.V, c0 + p.chunk);   // this part's elements
   const T *x = static_cast<const T *>(p.x) + row * p.ldl;
-  // pieces start at 16-byte boundaries: `skew` elements before c0 are not this part's
+  // pieces of 8 from the first 16-byte boundary; the up to 7 elements before it and the up to 7
+  // behind the last whole piece go one each to threads 0..15
   constexpr int kAlign = 16 / (int)sizeof(T);
-  const int skew = (int)(((uintptr_t)(x + c0) / sizeof(T)) % kAlign);
-  const int first = c0 - skew;
+  const int a0 = min(c1, c0 + (int)(-(uintptr_t)(x + c0) / sizeof(T) % kAlign));
+  const int a1 = a0 + (c1 - a0) / 8 * 8;
+  const int rounds = (a1 - a0 + THREADS * 8 - 1) / (THREADS * 8);   // pieces per thread: uniform
+  const int mine0 = a0 + t * 8;          // this thread's first element
 
   const float ninf = -__builtin_inff();
   Piece<DT> q[E];
-  auto present = [&](int j, int i) {
-    const int e = first + (j * THREADS + t) * 8 + i;
-    return e >= c0 && e < c1;
-  };
-#pragma unroll
+#pragma clang loop unroll(full)
   for (int j = 0; j < E; ++j) {
-    const int e = first + (j * THREADS + t) * 8;
-    if (e >= c0 && e + 8 <= c1) {
+    if (j >= rounds) continue;
+    const int e = mine0 + j * (THREADS * 8);
+    // absent elements are -infinity, which adds nothing to any sum
+    const uint32_t absent = DT == DT_F32 ? 0xff800000u : DT == DT_F16 ? 0xfc00fc00u : 0xff80ff80u;
 #pragma unroll
-      for (int h = 0; h < (DT == DT_F32 ? 2 : 1); ++h) q[j].v[h] = reinterpret_cast<const u4_t *>(x + e)[h];
-    } else {
-      // at a part's ends: absent elements are -infinity, which adds nothing to any sum
-      uint32_t w[DT == DT_F32 ? 8 : 4] = {};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        T v = from_f32<DT>(ninf);
-        if (e + i >= c0 && e + i < c1) v = x[e + i];
-        if constexpr (DT == DT_F32) w[i] = __builtin_bit_cast(uint32_t, v);
-        else w[i >> 1] |= (uint32_t)v << (16 * (i & 1));
-      }
-#pragma unroll
-      for (int h = 0; h < (DT == DT_F32 ? 2 : 1); ++h) q[j].v[h] = u4_t{w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]};
+    for (int h = 0; h < (DT == DT_F32 ? 2 : 1); ++h) {
+      q[j].v[h] = u4_t{absent, absent, absent, absent};
+      if (e < a1) q[j].v[h] = reinterpret_cast<const u4_t *>(x + e)[h];
     }
   }
+  const int edge_at = t < 8 ? c0 + t : a1 + t - 8;
+  const bool has_edge = t < 8 ? edge_at < a0 : t < 16 && edge_at < c1;
+  const float edge = has_edge ? to_f32<DT>(x[edge_at]) : ninf;
 
-  // the thread's largest key below `limit`
-  auto best_below = [&](uint64_t limit) {
-    uint64_t best = 0;
-#pragma unroll
-    for (int j = 0; j < E; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint64_t k = make_key(order_bits(piece_at<DT>(q[j], i)), (uint32_t)(first + (j * THREADS + t) * 8 + i));
-        if (present(j, i) && k < limit && k > best) best = k;
-      }
-    return best;
-  };
-  const uint64_t mine = best_below(~0ull);
-  const uint64_t wk = wave_max(mine);
-  if (lane == 0) wave_key[wave] = wk;
-  thread_key[t] = mine;
+  float mine = fmaxf(edge, ninf);        // (a NaN is passed over)
+#pragma clang loop unroll(full)
+  for (int j = 0; j < E; ++j) {
+    if (j >= rounds) continue;
+    mine = fmaxf(mine, piece_max<DT>(q[j]));
+  }
+  const float gm = group_max<GROUP>(mine);
+  if (lane % GROUP == 0) group[t / GROUP] = gm;
+  if (t < 64) larger[t] = 0;
   if (t == 0) count = 0;
   __syncthreads();
-  uint64_t top_key = 0;
-#pragma unroll
-  for (int i = 0; i < WAVES; ++i) top_key = wave_key[i] > top_key ? wave_key[i] : top_key;
-  const float m = order_value((uint32_t)(top_key >> 32));
+  const float g = group[lane];            // every wave holds the 64 group maxima
+  const float m = wave_max(g);
   // a part of -infinities: shift by 0, so that its terms are 0 and not NaN
   const float shift = m == ninf ? 0.f : m;
-
-  float S = 0.f, Tn = 0.f;
+  if (p.top > 0) {
+    int n = 0;
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    float s = 0.f, u = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float d = piece_at<DT>(q[j], i) - shift;
-      const float e = __builtin_amdgcn_exp2f(d * kLog2e);
-      s += e;
-      u += e * fmaxf(d, -1e4f);   // e is 0 there: 0, and not 0 times infinity
+    for (int i = 0; i < 64 / WAVES; ++i) {
+      const int o = wave * (64 / WAVES) + i;
+      const float v = lane_value(g, o);
+      n += v > g || (v == g && o < lane);
     }
+    atomicAdd(&larger[lane], n);
+  }
+
+  float S = 0.f, Tn = 0.f;                // Tn in units of log 2
+  auto add = [&](float v, float &s, float &u) {
+    const float d = (v - shift) * kLog2e;
+    const float e = __builtin_amdgcn_exp2f(d);
+    s += e;
+    u = fmaf(e, fmaxf(d, -1e4f), u);      // e is 0 there: 0, and not 0 times infinity
+  };
+  add(edge, S, Tn);
+#pragma clang loop unroll(full)
+  for (int j = 0; j < E; ++j) {
+    if (j >= rounds) continue;
+    float s = 0.f, u = 0.f;
+    forget<DT>(q[j]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) add(piece_at<DT>(q[j], i), s, u);
     S += s;
     Tn += u;
   }
@@ -168,19 +221,6 @@ __global__ __launch_bounds__(WAVES * 64) void part_kernel(LogprobsParams p) {
     red[wave][0] = S;
     red[wave][1] = Tn;
   }
-
-  if (p.top > 0 && wave == 0) {
-    // the group of lane l: threads l, l + 64, ...
-    uint64_t gk = 0;
-#pragma unroll
-    for (int i = 0; i < WAVES; ++i) gk = thread_key[i * 64 + lane] > gk ? thread_key[i * 64 + lane] : gk;
-    int larger = 0;
-    for (int i = 0; i < 64; ++i) {
-      const uint64_t o = __shfl((unsigned long long)gk, i);
-      larger += o > gk || (o == gk && i < lane);   // groups with nothing share key 0
-    }
-    if (larger == p.top - 1) threshold = gk;
-  }
   __syncthreads();
   S = Tn = 0.f;
 #pragma unroll
@@ -188,9 +228,16 @@ __global__ __launch_bounds__(WAVES * 64) void part_kernel(LogprobsParams p) {
     S += red[i][0];
     Tn += red[i][1];
   }
+  Tn *= kLn2;
 
   const int64_t slot = row * p.chunks + part;
   const float ls = logf(S);
+  if (t == 0) {
+    if (p.chunks > 1) *reinterpret_cast<f4_t *>(p.part + slot * 4) = f4_t{m, S, Tn, 0.f};
+    else write_row(p, row, m, S, Tn, token_logit<DT>(p, row));
+  }
+  if (p.top == 0) return;
+
   auto emit = [&](int rank, uint64_t k) {
     if (p.chunks > 1) p.keys[slot * p.top + rank] = k;
     else {
@@ -198,48 +245,96 @@ __global__ __launch_bounds__(WAVES * 64) void part_kernel(LogprobsParams p) {
       p.top_logprobs[row * p.top + rank] = (order_value((uint32_t)(k >> 32)) - m) - ls;
     }
   };
-  if (p.top > 0) {
-    const uint64_t thr = threshold;
-    if (mine >= thr && mine != 0) {
-#pragma unroll
-      for (int j = 0; j < E; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint64_t k = make_key(order_bits(piece_at<DT>(q[j], i)), (uint32_t)(first + (j * THREADS + t) * 8 + i));
-          if (present(j, i) && k >= thr) {
-            const int at = atomicAdd(&count, 1);
-            if (at < kCap) cand[at] = k;
-          }
-        }
-    }
-    __syncthreads();
-    const int n = count;
-    if (n <= kCap) {
-      for (int a = t; a < n; a += THREADS) {
-        const uint64_t k = cand[a];
-        int rank = 0;
-        for (int o = 0; o < n; ++o) rank += cand[o] > k;
-        if (rank < p.top) emit(rank, k);
+  // collects the elements above the threshold (and, with `ties`, those equal to it)
+  const float thr = lane_value(g, __builtin_ctzll(__ballot(larger[lane] == p.top - 1)));
+  auto collect = [&](bool ties) {
+    auto offer = [&](float v, int at) {
+      if (ties ? v >= thr : v > thr) {
+        const int n = atomicAdd(&count, 1);
+        if (n < kCap) cand[n] = make_key(order_bits(v), (uint32_t)at);
       }
+    };
+    if (has_edge) offer(edge, edge_at);
+#pragma clang loop unroll(full)
+    for (int j = 0; j < E; ++j) {
+      if (j >= rounds) continue;
+      forget<DT>(q[j]);
+      const int e = mine0 + j * (THREADS * 8);
+      if (e < a1 && piece_max<DT>(q[j]) >= thr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) offer(piece_at<DT>(q[j], i), e + i);
+      }
+    }
+  };
+  auto rank_all = [&](int n) {
+    for (int a = t; a < n; a += THREADS) {
+      const uint64_t k = cand[a];
+      int rank = 0;
+      for (int o = 0; o < n; ++o) rank += cand[o] > k;
+      if (rank < p.top) emit(rank, k);
+    }
+  };
+
+  int n = 0;
+  bool one_by_one = S != S;              // a NaN or +infinity in the row
+  if (!one_by_one) {
+    if (mine >= thr) collect(true);
+    __syncthreads();
+    n = count;
+    if (n <= kCap) {
+      rank_all(n);
       // a part with fewer elements than `top`: the rest of its slots are absent
       for (int a = n + t; a < p.top; a += THREADS) emit(a, 0);
-    } else {
-      uint64_t limit = ~0ull;
-      for (int rank = 0; rank < p.top; ++rank) {
-        const uint64_t b = wave_max(best_below(limit));
-        __syncthreads();
-        if (lane == 0) wave_key[wave] = b;
-        __syncthreads();
-        limit = 0;
-#pragma unroll
-        for (int i = 0; i < WAVES; ++i) limit = wave_key[i] > limit ? wave_key[i] : limit;
-        if (t == 0) emit(rank, limit);
-      }
+      return;
     }
+    __syncthreads();
+    if (t == 0) count = 0;
+    __syncthreads();
+    if (mine > thr) collect(false);
+    __syncthreads();
+    n = count;
+    one_by_one = n > kCap;
   }
-  if (t == 0) {
-    if (p.chunks > 1) *reinterpret_cast<f4_t *>(p.part + slot * 4) = f4_t{m, S, Tn, 0.f};
-    else write_row(p, row, m, S, Tn, token_logit<DT>(p, row));
+  // both rare forms read the logits again, one element per thread
+  if (!one_by_one) {
+    // all larger ones are in; equal ones in index order until `top` are
+    int need = p.top - n;                // at most 0 if the larger ones suffice
+    for (int e0 = c0; e0 < c1 && need > 0; e0 += THREADS) {
+      const int e = e0 + t;
+      const bool eq = e < c1 && to_f32<DT>(x[e]) == thr;
+      const uint64_t who = __ballot(eq);
+      if (lane == 0) wave_count[wave] = __popcll(who);
+      __syncthreads();
+      int at = __popcll(who & ((1ull << lane) - 1)), total = 0;
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) {
+        at += i < wave ? wave_count[i] : 0;
+        total += wave_count[i];
+      }
+      if (eq && at < need) cand[n + at] = make_key(order_bits(thr), (uint32_t)e);
+      const int took = min(total, need);
+      n += took;
+      need -= took;
+      __syncthreads();                   // wave_count may be written again, cand read
+    }
+    rank_all(n);
+    return;
+  }
+  uint64_t limit = ~0ull;
+  for (int rank = 0; rank < p.top; ++rank) {
+    uint64_t best = 0;
+    for (int e = c0 + t; e < c1; e += THREADS) {
+      const uint64_t k = make_key(order_bits(to_f32<DT>(x[e])), (uint32_t)e);
+      if (k < limit && k > best) best = k;
+    }
+    best = wave_max(best);
+    __syncthreads();
+    if (lane == 0) wave_key[wave] = best;
+    __syncthreads();
+    limit = 0;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) limit = wave_key[i] > limit ? wave_key[i] : limit;
+    if (t == 0) emit(rank, limit);
   }
 }
 
@@ -285,15 +380,19 @@ __global__ __launch_bounds__(256) void join_kernel(LogprobsParams p) {
   }
 }
 
-// Elements one workgroup can hold after an unaligned start (up to 7 elements before it).
-constexpr int held(int threads, int e) { return threads * e * 8 - 8; }
+// elements one workgroup holds in registers
+constexpr int held(int waves, int e) { return waves * 64 * e * 8; }
+constexpr int kSmall = held(4, 2), kMiddle = held(8, 4), kLarge = held(8, 12);
+static_assert(kLarge == held(16, 6), "both large forms hold the same part");
 
 template <int DT>
 hipError_t launch(const LogprobsParams &p, hipStream_t s) {
   const dim3 grid((uint32_t)((int64_t)p.M * p.chunks));
-  if (p.chunk <= held(256, 2)) hipLaunchKernelGGL((part_kernel<DT, 4, 2>), grid, dim3(256), 0, s, p);
-  else if (p.chunk <= held(1024, 2)) hipLaunchKernelGGL((part_kernel<DT, 16, 2>), grid, dim3(1024), 0, s, p);
-  else hipLaunchKernelGGL((part_kernel<DT, 16, 7>), grid, dim3(1024), 0, s, p);
+  if (p.chunk <= kSmall) hipLaunchKernelGGL((part_kernel<DT, 4, 2>), grid, dim3(256), 0, s, p);
+  else if (p.chunk <= kMiddle) hipLaunchKernelGGL((part_kernel<DT, 8, 4>), grid, dim3(512), 0, s, p);
+  // 32-bit rows take twice the registers: 6 pieces a thread instead of 12
+  else if constexpr (DT == DT_F32) hipLaunchKernelGGL((part_kernel<DT, 16, 6>), grid, dim3(1024), 0, s, p);
+  else hipLaunchKernelGGL((part_kernel<DT, 8, 12>), grid, dim3(512), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.chunks == 1) return e;
   hipLaunchKernelGGL((join_kernel<DT>), dim3((uint32_t)p.M), dim3(256), (uint32_t)(p.chunks * p.top * sizeof(uint64_t)), s, p);
@@ -302,14 +401,13 @@ hipError_t launch(const LogprobsParams &p, hipStream_t s) {
 
 }  // namespace
 
-// Parts of a row and their length (a multiple of 8): whole rows of up to 57336 elements when
-// the rows fill the chip, else parts short enough for about two workgroups per CU.
+// Parts of a row and their length: whole rows of up to 49152 elements when the rows fill the
+// chip, else parts short enough for about two workgroups per CU.
 int logprobs_chunks(int M, int V, int dtype, int *chunk) {
   (void)dtype;
-  const int sizes[] = {held(256, 2), held(1024, 2), held(1024, 7)};
+  const int sizes[] = {kSmall, kMiddle, kLarge};
   for (int i = 0; i < 3; ++i) {
     const int64_t parts = ((int64_t)V + sizes[i] - 1) / sizes[i];
-    // at most 64 parts, so that the joining kernel's keys fit LDS (64 x 32 x 8 bytes)
     if (i == 2 || (parts <= 32 && (parts == 1 || (int64_t)M * parts <= 4 * kCUs))) {
       *chunk = sizes[i];
       return (int)parts;
