@@ -58,16 +58,20 @@ __device__ __forceinline__ void unroll(F &&f) {
 }
 
 template <int DT, int FMT, int BM, int WM, int WN, int NF, int D, bool PRE>
-__global__ __launch_bounds__(WM * WN * 64, WM * WN * 64 == 512 ? 2 : 1) void gemm_kernel(MxMatmulParams p) {
+__global__ __launch_bounds__(WM * WN * 64, PRE ? 1 : 2) void gemm_kernel(MxMatmulParams p) {
   constexpr int WAVES = WM * WN, BN = WN * NF * 16, MF = BM / WM / 16;
   constexpr int SUB = FMT == MX_FP4 ? 2 : 1;      // instructions per step, operand pair
   constexpr int SLOTS = D + 1, SLOT = BM * 128;
   constexpr int XQ = BM / 8 / WAVES;              // X loads per wave and step (8 rows each)
   constexpr int WQ = SUB * NF;                    // weight loads per wave and step
   constexpr int WS = PRE ? SLOTS * SUB : SUB + 1; // weight register sets, one instruction's each
+  constexpr int GROUPS = SUB * MF, OPS = XQ + WQ + NF;   // X operands and loads of a step
   constexpr int U = !PRE && SUB == 2 ? 6 : 4;     // steps per unrolled loop body
   static_assert(U % SLOTS == 0 && U * SUB % WS == 0 && U * SUB % 4 == 0, "slots, sets and scale bytes are compile-time");
   static_assert(PRE || D == 1, "without PRE the weights run one step ahead");
+  // FP4 without PRE: the second instruction's weights go into the first one's set, so they are
+  // loaded in the second half of the step
+  static_assert(PRE || SUB == 1 || (XQ + NF) * GROUPS / OPS >= MF, "second-half weight loads");
   static_assert(XQ >= 1 && 8 * XQ * WAVES == BM, "X rows per wave");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[SLOTS * SLOT + kPanel * BM * 16];
   uint8_t *sxl = smem + SLOTS * SLOT;
@@ -112,27 +116,18 @@ __global__ __launch_bounds__(WM * WN * 64, WM * WN * 64 == 512 ? 2 : 1) void gem
     for (int f = 0; f < NF; ++f) acc[i][f] = f4_t{0.f, 0.f, 0.f, 0.f};
 
   u4_t w[WS][NF];
-  auto load_x = [&](int step, int slot) {
-    uint8_t *dst = smem + slot * SLOT + wave * XQ * 1024;
+  // Load q of a step's X.  Chunks past K in the last step hold the next row's bytes, or nothing:
+  // an offset past the descriptor's range reads nothing and puts zeros into LDS.
+  const int chunk0 = (lane & 7) ^ (lane >> 4), chunk1 = chunk0 ^ 4;   // this lane's source chunk, q even and odd
+  auto load_x = [&](int step, int slot, int q) {
     const uint32_t soff = (uint32_t)min(step, steps - 1) * 128;
-    if (tail && step >= steps - 1) {
-      // chunks past K hold the next row's bytes, or nothing: an offset past the descriptor's
-      // range reads nothing and puts zeros into LDS
-#pragma unroll
-      for (int q = 0; q < XQ; ++q) {
-        const int row = (wave * XQ + q) * 8 + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
-        dma16(xr, c < tail ? xvoff[q] : 0x7fffffffu, soff, dst + q * 1024);
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < XQ; ++q) dma16(xr, xvoff[q], soff, dst + q * 1024);
-    }
+    const int limit = step >= steps - 1 && tail ? tail : 8;
+    dma16(xr, ((q & 1) ? chunk1 : chunk0) < limit ? xvoff[q] : 0x7fffffffu, soff, smem + slot * SLOT + (wave * XQ + q) * 1024);
   };
   // operands of instruction s of a step into register set `set`
-  auto load_w = [&](int step, int s, int set) {
+  auto load_w = [&](int step, int s, int set, int f) {
     const uint8_t *src = wbase + (int64_t)min(min(step, steps - 1) * SUB + s, p.KS - 1) * 4096;
-#pragma unroll
-    for (int f = 0; f < NF; ++f) w[set][f] = *reinterpret_cast<const u4_t *>(src + f * 1024);
+    w[set][f] = *reinterpret_cast<const u4_t *>(src + f * 1024);
   };
   // this lane's chunk addresses in a slot: chunk b and chunk b + 4 of row r of operand 0
   const int row0 = wm * MF * 16 + r;
@@ -159,11 +154,9 @@ __global__ __launch_bounds__(WM * WN * 64, WM * WN * 64 == 512 ? 2 : 1) void gem
     const int chunks = min(kPanel, p.KB - c0);
     const int s0 = c0 * (4 / SUB), s1 = min(steps, s0 + chunks * (4 / SUB));   // steps of the panel
     uint32_t sw[NF], sw_next[NF];         // weight scales of this 512-k chunk and the next
-    auto load_sw = [&](int kb) {
+    auto load_sw = [&](int kb, int f) { sw_next[f] = sbase[(int64_t)min(kb, p.KB - 1) * 256 + f * 64]; };
 #pragma unroll
-      for (int f = 0; f < NF; ++f) sw_next[f] = sbase[(int64_t)min(kb, p.KB - 1) * 256 + f * 64];
-    };
-    load_sw(c0);
+    for (int f = 0; f < NF; ++f) load_sw(c0, f);
     lds_barrier();                        // the panel before has been read
     for (int q = wave; q < chunks * (BM / 64); q += WAVES) {
       const int c = q / (BM / 64), row = (q % (BM / 64)) * 64 + lane;
@@ -173,10 +166,13 @@ __global__ __launch_bounds__(WM * WN * 64, WM * WN * 64 == 512 ? 2 : 1) void gem
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       pin();
-      load_x(s0 + d, d);
+#pragma unroll
+      for (int q = 0; q < XQ; ++q) load_x(s0 + d, d, q);
       pin();
 #pragma unroll
-      for (int h = 0; h < SUB; ++h) load_w(s0 + d, h, (d * SUB + h) % WS);
+      for (int h = 0; h < SUB; ++h)
+#pragma unroll
+        for (int f = 0; f < NF; ++f) load_w(s0 + d, h, (d * SUB + h) % WS, f);
     }
     pin();
     const int left = (blocks & 15);
@@ -203,57 +199,46 @@ __global__ __launch_bounds__(WM * WN * 64, WM * WN * 64 == 512 ? 2 : 1) void gem
         constexpr int u = decltype(uc)::value;
         const int step = base + u;
         if (step >= s1) return;
-        // waits count the loads younger than the ones needed; more of them only wait longer
-        if constexpr (PRE) {
-          if (step + 1 < s1) {
-            wait_vmcnt<(D - 2) * (XQ + WQ) + WQ>();
-            lds_barrier();
-            const uint8_t *xs = smem + (u + 1) % SLOTS * SLOT, *sp = ss + (step + 1 - s0) * SUB / 4 * BM * 16;
-#pragma unroll
-            for (int h = 0; h < SUB; ++h)
-#pragma unroll
-              for (int i = 0; i < MF; ++i) read_x(fr[((u + 1) & 1) * SUB + h][i], i, h, xs, sp, (u + 1) * SUB + h);
-          }
-        } else {
-          wait_vmcnt<0>();
-          lds_barrier();
-        }
         constexpr bool next_chunk = u * SUB % 4 == 0;
+        // PRE: the next step's X; else this step's.  The count is of the loads younger than the
+        // ones needed; more of them only wait longer.
+        if constexpr (PRE) wait_vmcnt<(D - 2) * (XQ + WQ) + WQ>();
+        else wait_vmcnt<0>();
+        lds_barrier();
         if constexpr (next_chunk) {
 #pragma unroll
           for (int f = 0; f < NF; ++f) sw[f] = sw_next[f];
         }
-        pin();
-        load_x(step + D, (u + D) % SLOTS);
-        pin();
-        if constexpr (PRE) {
-#pragma unroll
-          for (int h = 0; h < SUB; ++h) load_w(step + D, h, ((u + D) * SUB + h) % WS);
-        }
-        if constexpr (next_chunk) load_sw(c0 + (step - s0) * SUB / 4 + 1);
-        pin();
-        if constexpr (PRE) {
-          unroll<0, SUB * MF>([&](auto jc) {
-            constexpr int h = decltype(jc)::value / MF, i = decltype(jc)::value % MF;
-            multiply(std::integral_constant<int, u * SUB + h>{}, i, fr[(u & 1) * SUB + h][i], sw);
-          });
-        } else {
-          const uint8_t *xs = smem + u % SLOTS * SLOT, *sp = ss + (step - s0) * SUB / 4 * BM * 16;
+        // the operands read during this step: the next step's, or AHEAD further on in this one
+        const int rstep = PRE ? min(step + 1, s1 - 1) : step;   // (past the last: read, not used)
+        constexpr int ru = PRE ? u + 1 : u;
+        const uint8_t *xs = smem + ru % SLOTS * SLOT, *sp = ss + (rstep - s0) * SUB / 4 * BM * 16;
+        if constexpr (!PRE) {
 #pragma unroll
           for (int j = 0; j < AHEAD; ++j) read_x(fr[0][j], j % MF, j / MF, xs, sp, u * SUB + j / MF);
-          unroll<0, SUB * MF>([&](auto jc) {
-            constexpr int j = decltype(jc)::value, h = j / MF, i = j % MF, n = j + AHEAD;
-            __builtin_amdgcn_sched_barrier(0);
-            // set (u SUB + h + SUB) mod WS: its last use was the instruction before this one
-            if constexpr (i == 0) load_w(step + 1, h, (u * SUB + h + SUB) % WS);
-            if constexpr (n < SUB * MF) read_x(fr[0][n % (AHEAD + 1)], n % MF, n / MF, xs, sp, u * SUB + n / MF);
-            multiply(std::integral_constant<int, u * SUB + h>{}, i, fr[0][j % (AHEAD + 1)], sw);
-            // the products stay between the reads around them (the compiler would sink them
-            // past the step's end, holding every operand of the step in registers)
+        }
+        // Loads, operand reads and products interleaved: a wave whose loads wait to be accepted
+        // issues nothing, so they go one at a time between the products.
+        unroll<0, GROUPS>([&](auto jc) {
+          constexpr int j = decltype(jc)::value, h = j / MF, i = j % MF, n = j + AHEAD;
+          pin();
+          unroll<j * OPS / GROUPS, (j + 1) * OPS / GROUPS>([&](auto oc) {
+            constexpr int o = decltype(oc)::value;
+            if constexpr (o < XQ) load_x(step + D, (u + D) % SLOTS, o);
+            else if constexpr (o < XQ + WQ) load_w(step + D, (o - XQ) / NF, ((u + D) * SUB + (o - XQ) / NF) % WS, (o - XQ) % NF);
+            else if constexpr (next_chunk) load_sw(c0 + (step - s0) * SUB / 4 + 1, o - XQ - WQ);
+          });
+          pin();
+          if constexpr (PRE) read_x(fr[(ru & 1) * SUB + h][i], i, h, xs, sp, ru * SUB + h);
+          else if constexpr (n < GROUPS) read_x(fr[0][n % (AHEAD + 1)], n % MF, n / MF, xs, sp, u * SUB + n / MF);
+          multiply(std::integral_constant<int, u * SUB + h>{}, i, fr[PRE ? (u & 1) * SUB + h : 0][PRE ? i : j % (AHEAD + 1)], sw);
+          // the products stay between the reads around them (the compiler would sink them
+          // past the step's end, holding every operand of the step in registers)
+          if constexpr (!PRE) {
 #pragma unroll
             for (int f = 0; f < NF; ++f) keep(acc[i][f]);
-          });
-        }
+          }
+        });
       });
     }
     wait_vmcnt<0>();   // loads past the last step land before their slots are reused
@@ -295,7 +280,7 @@ hipError_t launch_tile(const MxMatmulParams &p, hipStream_t s) {
 template <int DT, int FMT>
 hipError_t launch(const MxMatmulParams &p, hipStream_t s) {
   const int rows = mx_gemm_rows(p.M, p.N);
-  if (rows == 256) return launch_tile<DT, FMT, 256, 2, 4, 4, 1, false>(p, s);
+  if (rows == 256) return launch_tile<DT, FMT, 128, 1, 4, 4, 1, false>(p, s);
   if (rows == 128) return launch_tile<DT, FMT, 128, 1, 4, 2, 3, true>(p, s);
   return launch_tile<DT, FMT, 64, 1, 4, 2, 3, true>(p, s);
 }
