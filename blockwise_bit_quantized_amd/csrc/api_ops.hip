@@ -20,7 +20,7 @@ bool off16(int64_t bytes) { return (bytes & 15) != 0; }
 
 // bytes of an MX row and of its scales as they are read
 int64_t mx_row(int fmt, int K) { return fmt == MNB_MX_FP4 ? K / 2 : K; }
-int64_t scale_row(int K) { return cdiv(K, kMxScaleRow) * 16; }
+int64_t scale_row(int K) { return cdiv(K, kMxScaleK) * 16; }
 
 // [p, p + (rows - 1) ld + row): the bytes of a strided tensor
 struct Span {
@@ -103,8 +103,8 @@ int mnb_mx_packed_sizes(int N, int K, size_t *wq_bytes, size_t *sc_bytes) {
   const int st = check_matmul_sizes(0, N, K, MNB_MX_FP4);
   if (st) return st;
   const size_t ng = (size_t)cdiv(N, 64);
-  if (wq_bytes) *wq_bytes = ng * cdiv(K, kMxStep) * 2048;
-  if (sc_bytes) *sc_bytes = ng * cdiv(K, kMxScaleK) * 512;
+  if (wq_bytes) *wq_bytes = ng * cdiv(K, kMxStep) * 4096;
+  if (sc_bytes) *sc_bytes = ng * cdiv(K, kMxScaleK) * 1024;
   return MNB_OK;
 }
 

@@ -71,17 +71,15 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(MxDequantParams p,
   store8<DT>(static_cast<T *>(p.y) + (int64_t)row * p.ldy + 8 * c, v);
 }
 
-// weight row, within its group of 64, of lane 32 b + r of operand f
-__device__ __forceinline__ int packed_row(int r, int f) { return 32 * ((r >> 2) & 1) + 16 * f + 4 * (r >> 3) + (r & 3); }
-
 __global__ __launch_bounds__(kThreads) void pack_codes_kernel(MxPackParams p, int64_t chunks) {
   const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (id >= chunks) return;
-  const int lane = (int)(id & 63), f = (int)(id >> 6) & 1;
-  const int64_t gs = id >> 7;
+  const int lane = (int)(id & 63), f = (int)(id >> 6) & 3;
+  const int64_t gs = id >> 8;
   const int g = (int)(gs / p.KS), step = (int)(gs - (int64_t)g * p.KS);
-  const int64_t n = 64 * (int64_t)g + packed_row(lane & 31, f);
-  const int kb = step * 2 + (lane >> 5);
+  const int r = lane & 15, b = lane >> 4;
+  const int64_t n = 64 * (int64_t)g + 16 * (r >> 2) + 4 * f + (r & 3);
+  const int kb = step * 4 + b;
   u4_t w = {0, 0, 0, 0};
   if (n < p.N && kb < p.K / kBlock) w = *reinterpret_cast<const u4_t *>(p.codes + n * p.ldc + (int64_t)kb * 16);
   *reinterpret_cast<u4_t *>(p.wq + id * 16) = w;
@@ -90,14 +88,15 @@ __global__ __launch_bounds__(kThreads) void pack_codes_kernel(MxPackParams p, in
 __global__ __launch_bounds__(kThreads) void pack_scales_kernel(MxPackParams p, int64_t words) {
   const int64_t id = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (id >= words) return;
-  const int lane = (int)(id & 63), f = (int)(id >> 6) & 1;
-  const int64_t gk = id >> 7;
-  const int g = (int)(gk / p.KB), kq = (int)(gk - (int64_t)g * p.KB);
-  const int64_t n = 64 * (int64_t)g + packed_row(lane & 31, f);
+  const int lane = (int)(id & 63), f = (int)(id >> 6) & 3;
+  const int64_t gk = id >> 8;
+  const int g = (int)(gk / p.KB), kb512 = (int)(gk - (int64_t)g * p.KB);
+  const int r = lane & 15, b = lane >> 4;
+  const int64_t n = 64 * (int64_t)g + 16 * (r >> 2) + 4 * f + (r & 3);
   uint32_t w = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int kb = (kq * 4 + j) * 2 + (lane >> 5);
+    const int kb = (kb512 * 4 + j) * 4 + b;
     if (n < p.N && kb < p.K / kBlock) w |= (uint32_t)p.scales[n * p.lds + kb] << (8 * j);
   }
   reinterpret_cast<uint32_t *>(p.sc)[id] = w;
@@ -164,11 +163,11 @@ hipError_t launch_mx_dequantize(int dtype, int fmt, const MxDequantParams &p, hi
 }
 
 hipError_t launch_mx_pack(const MxPackParams &p, hipStream_t s) {
-  const int64_t chunks = (int64_t)p.NG * p.KS * 128, words = (int64_t)p.NG * p.KB * 128;
-  hipLaunchKernelGGL(pack_codes_kernel, dim3((uint32_t)((chunks + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, p, chunks);
+  const int64_t chunks = (int64_t)p.NG * p.KS * 256, words = (int64_t)p.NG * p.KB * 256;
+  hipLaunchKernelGGL(pack_codes_kernel, dim3((uint32_t)(chunks / kThreads)), dim3(kThreads), 0, s, p, chunks);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(pack_scales_kernel, dim3((uint32_t)((words + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, p, words);
+  hipLaunchKernelGGL(pack_scales_kernel, dim3((uint32_t)(words / kThreads)), dim3(kThreads), 0, s, p, words);
   return hipGetLastError();
 }
 

@@ -9,10 +9,9 @@ namespace mnb {
 enum { DT_F16 = 0, DT_BF16 = 1, DT_F32 = 2 };
 enum { MX_FP4 = 0, MX_FP8 = 1 };
 
-constexpr int kMxStep = 64;    // k of one matrix instruction (2 blocks)
+constexpr int kMxStep = 128;   // k of one matrix instruction (4 blocks)
 constexpr int kMxMaxK = 1 << 22;   // K limit of the product; its row distances stay below twice that
-constexpr int kMxScaleK = 256; // k of one weight scale dword per lane (4 steps, one byte each)
-constexpr int kMxScaleRow = 512; // k of 16 scale bytes: the pieces that X's scales are read in
+constexpr int kMxScaleK = 512; // k of one scale dword per lane (4 steps, one byte each)
 
 typedef float f4_t __attribute__((ext_vector_type(4)));
 typedef float f2_t __attribute__((ext_vector_type(2)));
@@ -139,11 +138,11 @@ struct MxDequantParams {
 };
 hipError_t launch_mx_dequantize(int dtype, int fmt, const MxDequantParams &p, hipStream_t s);
 
-// chunk (group of 64 rows, step of 64 k, operand f of two, lane): 16 bytes at
-// (((group * KS + step) * 2 + f) * 64 + lane) * 16.  Lane 32 b + r of operand f holds block b
-// of the step (32 k) of row 64 group + 32 ((r / 4) % 2) + 16 f + 4 (r / 8) + r % 4: a lane of the
-// product's result then holds 16 consecutive columns of each operand, 32 of both.  Scale dwords at
-// (((group * KB + k / 256) * 2 + f) * 64 + lane) * 4, byte j for step 4 (k / 256) + j.
+// chunk (group of 64 rows, step of 128 k, operand f, lane): 16 bytes at
+// (((group * KS + step) * 4 + f) * 64 + lane) * 16.  Lane 16 b + r of operand f holds block
+// b of the step (32 k) of row 64 group + 16 (r / 4) + 4 f + r % 4: a lane of the product's
+// result then holds 16 consecutive columns over the four operands.  Scale dwords at
+// (((group * KB + k / 512) * 4 + f) * 64 + lane) * 4, byte j for step 4 (k / 512) + j.
 struct MxPackParams {
   const uint8_t *codes, *scales;
   uint8_t *wq, *sc;
@@ -162,7 +161,7 @@ struct MxMatmulParams {
   float *part;                     // K split over workgroups: FP32 partial outputs [splits, M, N]
   int splits;
 };
-constexpr int kMxGemvMaxM = 32;
+constexpr int kMxGemvMaxM = 16;
 hipError_t launch_mx_gemv(int dtype, int fmt, const MxMatmulParams &p, hipStream_t s);
 hipError_t launch_mx_gemm(int dtype, int fmt, const MxMatmulParams &p, hipStream_t s);
 int mx_gemv_ksplit(int N, int K);                    // waves that share a weight row's K: 1, 2, 4 or 8

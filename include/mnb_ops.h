@@ -54,8 +54,8 @@ int mnb_mx_dequantize(const void *codes, int64_t ldc, const void *scales, int64_
 
 /*
  * Device layout of an FP4 weight [N, K] for mnb_mx_matmul (K % 32 == 0, K < 2^22):
- * rows in groups of 64, K in steps of 64; the 2 KiB of a (group, step) hold two matrix
- * operands of 32 rows, each 16 bytes (32 consecutive k of one row) for each of 64 lanes.
+ * rows in groups of 64, K in steps of 128; the 4 KiB of a (group, step) hold four matrix
+ * operands of 16 rows, each 16 bytes (32 consecutive k of one row) for each of 64 lanes.
  * mnb_mx_packed_sizes (host only) gives the two buffers' bytes.  Rows past N and k past K
  * are written as code 0 with scale byte 0.  scales: as above, or any row distance >= K/32.
  */
@@ -70,7 +70,7 @@ int mnb_mx_pack(const void *codes, int64_t ldc, const void *scales, int64_t lds,
  * own row of Y only, one of W its own column.  codes, scales, wq, sc and Y 16-byte aligned, as
  * are ldc and lds; bias 16-byte aligned.  Y must not overlap the inputs or the workspace.
  *
- * M <= 32 streams the weight once for all rows; more rows run as tiles of outputs.
+ * M <= 16 streams the weight once for all rows; more rows run as 128 x 128 output tiles.
  * workspace: at least mnb_mx_workspace_bytes(M, N, K, fmt) bytes, 16-byte aligned (NULL if that is 0).
  */
 size_t mnb_mx_workspace_bytes(int M, int N, int K, int fmt);

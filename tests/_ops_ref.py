@@ -74,18 +74,18 @@ def dequantize(codes, scales, fmt):
 
 def pack(codes, scales, N, K):
     """The device layout of include/mnb_ops.h: (wq bytes, sc bytes)."""
-    ng, ks, kb = -(-N // 64), -(-K // 64), -(-K // 256)
-    wq = np.zeros((ng, ks, 2, 64, 16), np.uint8)
-    sc = np.zeros((ng, kb, 2, 64, 4), np.uint8)
+    ng, ks, kb = -(-N // 64), -(-K // 128), -(-K // 512)
+    wq = np.zeros((ng, ks, 4, 64, 16), np.uint8)
+    sc = np.zeros((ng, kb, 4, 64, 4), np.uint8)
     for g in range(ng):
-        for f in range(2):
+        for f in range(4):
             for lane in range(64):
-                r, b = lane % 32, lane // 32
-                n = 64 * g + 32 * (r // 4 % 2) + 16 * f + 4 * (r // 8) + r % 4
+                r, b = lane % 16, lane // 16
+                n = 64 * g + 16 * (r // 4) + 4 * f + r % 4
                 if n >= N:
                     continue
                 for s in range(ks):
-                    k = s * 2 + b
+                    k = s * 4 + b
                     if k < K // 32:
                         wq[g, s, f, lane] = codes[n, k * 16:k * 16 + 16]
                         sc[g, s // 4, f, lane, s % 4] = scales[n, k]

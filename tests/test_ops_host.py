@@ -32,7 +32,7 @@ def test_every_declared_symbol_is_exported_and_bound():
 def test_packed_sizes_and_routes():
     for N, K in ((1, 32), (64, 128), (65, 160), (1000, 1056), (49152, 576)):
         st, wq, sc = mnb.mnb_mx_packed_sizes(N, K)
-        assert (st, wq, sc) == (OK, -(-N // 64) * -(-K // 64) * 2048, -(-N // 64) * -(-K // 256) * 512)
+        assert (st, wq, sc) == (OK, -(-N // 64) * -(-K // 128) * 4096, -(-N // 64) * -(-K // 512) * 1024)
     assert mnb.mnb_mx_packed_sizes(64, 40)[0] == UNSUPPORTED
     assert mnb.mnb_mx_packed_sizes(-1, 64)[0] == INVALID
     assert mnb.mnb_mx_packed_sizes(64, 1 << 25)[0] == UNSUPPORTED
@@ -42,8 +42,8 @@ def test_packed_sizes_and_routes():
         assert st == OK
         return text
     assert route(0, 64, 64, 0) == "noop" and route(4, 64, 0, 1) == "fill"
-    assert route(1, 8192, 2048, 1).startswith("mx_gemv_fp8") and route(32, 8192, 2048, 0).startswith("mx_gemv_fp4")
-    assert route(33, 8192, 2048, 0).startswith("mx_gemm_fp4")
+    assert route(1, 8192, 2048, 1).startswith("mx_gemv_fp8") and route(16, 8192, 2048, 0).startswith("mx_gemv_fp4")
+    assert route(17, 8192, 2048, 0).startswith("mx_gemm_fp4")
     assert mnb.mnb_mx_describe_route(1, 64, 64, 2)[0] == INVALID
     assert mnb.mnb_mx_workspace_bytes(1, 8192, 2048, 1) == 0
 
@@ -90,9 +90,9 @@ def test_matmul_validation():
     assert mm(b=P[4] + 16) == ALIAS
     # a last row of a strided X that ends inside Y
     assert mm(y=P[0] + 3 * 4096 + 16, ldc=4096) == ALIAS
-    need = mnb.mnb_mx_workspace_bytes(40, 64, 8192, 1)
+    need = mnb.mnb_mx_workspace_bytes(32, 64, 8192, 1)
     if need:
-        a = dict(M=40, K=8192, ldc=8192, lds=256)
+        a = dict(M=32, K=8192, ldc=8192, lds=256)
         assert mm(**a) == WORKSPACE and mm(ws=P[6], wsb=need - 1, **a) == WORKSPACE and mm(ws=P[4], wsb=need, **a) == ALIAS
 
 
@@ -178,11 +178,11 @@ def test_binding_refusals():
         mnb.mx_dequantize(mnb.MxTensor(codes[:1], scales[:1].clone(), mnb.MNB_MX_FP8))
     with pytest.raises(ValueError, match="MNB_MX_FP4"):
         mnb.mx_pack(q)
-    w = mnb.MxWeight(torch.zeros(2048, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8), 64, 64)
+    w = mnb.MxWeight(torch.zeros(4096, dtype=torch.uint8), torch.zeros(1024, dtype=torch.uint8), 64, 64)
     with pytest.raises(ValueError, match="on a GPU"):
         mnb.mx_matmul(q, w)
     with pytest.raises(ValueError, match="K="):
-        mnb.mx_matmul(q, mnb.MxWeight(torch.zeros(4096, dtype=torch.uint8), w.sc, 64, 96))
+        mnb.mx_matmul(q, mnb.MxWeight(w.wq, w.sc, 64, 96))
     with pytest.raises(ValueError, match="packed codes"):
         mnb.mx_matmul(q, mnb.MxWeight(w.wq[:-16], w.sc, 64, 64))
     with pytest.raises(ValueError, match="out must"):
