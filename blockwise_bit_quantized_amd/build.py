@@ -6,9 +6,11 @@
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +20,9 @@ LIB = os.path.join(PKG, "libmnb.so")
 # measurement helper for the benchmark (a streaming-read ceiling kernel), not the ABI
 CEILING_LIB = os.path.join(PKG, "libmnb_ceiling.so")
 CEILING_SOURCE = "ceiling.hip"
+# host side of the torch binding of include/mnb_ops.h (built where torch is installed)
+BINDING_LIB = os.path.join(PKG, "_mnb_ops" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+BINDING_SOURCE = "binding.cpp"
 OBJ = os.path.join(PKG, "_build")
 SOURCES = ["api.hip", "gemv.hip", "gemv_mfma.hip", "gemv_acc4.hip", "tproj.hip", "gemm.hip", "pack.hip",
            "api_ops.hip", "mx_quant.hip", "mx_gemv.hip", "mx_gemm.hip", "rmsnorm.hip", "logprobs.hip"]
@@ -57,8 +62,10 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
             print(err, flush=True)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(jobs, len(SOURCES))) as ex:
+    with ThreadPoolExecutor(max_workers=min(jobs, len(SOURCES) + 1)) as ex:
+        binding = ex.submit(_build_binding, verbose)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [hipcc, "--offload-arch=" + ARCH, "-mcode-object-version=5", "-shared", "-fPIC", *objs, "-o", tmp]
     if verbose:
@@ -70,6 +77,25 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
     os.replace(tmp, LIB)
     _build_ceiling(hipcc, verbose)
     return LIB
+
+
+def _build_binding(verbose: bool) -> None:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return                                   # the C ABI alone needs no torch
+    torch = os.path.join(list(spec.submodule_search_locations)[0])
+    inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
+    tmp = BINDING_LIB + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DUSE_ROCM", "-D__HIP_PLATFORM_AMD__=1",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-I" + os.path.join(ROOT, "include"),
+           os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s" % (BINDING_SOURCE, r.stderr))
+    os.replace(tmp, BINDING_LIB)
 
 
 def _build_ceiling(hipcc: str, verbose: bool) -> None:

@@ -4,9 +4,11 @@ output, and log probabilities over logits.
 
 The C calls keep their names (``mnb_mx_quantize`` ...) on plain integers; ``mx_quantize``,
 ``mx_dequantize``, ``mx_tensor``, ``mx_pack``, ``mx_matmul``, ``rmsnorm`` and ``logprobs``
-marshal torch tensors into them.  Everything here is forward only, like the rest of the
-package.  Scratch of a call comes from torch's allocator on the current stream, so calls
-on several streams, and graph captures, need no workspace of their own.
+marshal torch tensors into them; what they check and allocate is done in the native module
+_mnb_ops (csrc/binding.cpp), as a single-token call is bound by the host.  Everything here is
+forward only, like the rest of the package.  Scratch of a call comes from torch's allocator on
+the current stream, so calls on several streams, and graph captures, need no workspace of
+their own.
 """
 from __future__ import annotations
 
@@ -22,15 +24,15 @@ MNB_F16, MNB_BF16, MNB_F32 = 0, 1, 2
 MNB_MX_FP4, MNB_MX_FP8 = 0, 1
 MNB_LOGPROBS_MAX_TOP = 32
 
-_DTYPES = {torch.float16: MNB_F16, torch.bfloat16: MNB_BF16, torch.float32: MNB_F32} if torch else {}
 _OK = 0
 lib: Any = None
+_ext: Any = None
 _status_text: Any = None
 
 
 def _bind(library, status_text):
     """Called once by the package with its loaded library."""
-    global lib, _status_text
+    global lib, _ext, _status_text
     lib, _status_text = library, status_text
     P, I, L, S, F = C.c_void_p, C.c_int, C.c_int64, C.c_size_t, C.c_float
     sizes = C.POINTER(S)
@@ -48,6 +50,11 @@ def _bind(library, status_text):
             ("mnb_ops_version", I, [])):
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args
+    if torch is not None:
+        from . import _mnb_ops as _ext   # built with the library; there is no other path
+        _ext.bind(*(C.cast(getattr(lib, n), P).value for n in (
+            "mnb_mx_quantize", "mnb_mx_dequantize", "mnb_mx_matmul", "mnb_mx_workspace_bytes", "mnb_rmsnorm",
+            "mnb_logprobs", "mnb_logprobs_workspace_bytes", "mnb_status_string")))
 
 
 # ---------------------------------------------------------------------------------------
@@ -113,23 +120,16 @@ def _check(st: int):
         raise RuntimeError(_status_text(st))
 
 
-def _call(dev, f, *args):
-    """f(*args, stream) on the current stream of ``dev``, with ``dev`` current."""
-    i = dev.index
-    if i is None or dev.type != "cuda":
-        raise ValueError("tensors must be on a GPU, got %s" % dev)
-    if i == torch.cuda.current_device():
-        st = f(*args, _raw_stream(i))
-    else:
-        with torch.cuda.device(dev):
-            st = f(*args, _raw_stream(i))
-    if st != _OK:
-        raise RuntimeError(_status_text(st))
-
-
-def _raw_stream(index):
-    # the handle alone: building torch's Stream object costs as much as half a launch
-    return torch._C._cuda_getCurrentRawStream(index)
+def _run(f, t, *args):
+    """f(stream, t, *args) on the current stream of t's device, with that device current."""
+    i = t.get_device()
+    if i < 0:
+        return f(0, t, *args)            # refused there, after the other checks
+    # the stream's handle alone: building torch's Stream object costs as much as half a launch
+    if i == torch._C._cuda_getDevice():
+        return f(torch._C._cuda_getCurrentRawStream(i), t, *args)
+    with torch.cuda.device(i):
+        return f(torch._C._cuda_getCurrentRawStream(i), t, *args)
 
 
 def _ld(t, name):
@@ -145,33 +145,6 @@ def _ld(t, name):
     if ld < k:
         raise ValueError("the rows of %s must not overlap" % name)
     return ld
-
-
-def _beside(t, name, dtype, shape, dev):
-    """_ld of a tensor that has to match another's type, shape and device."""
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.device != dev:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
-    return _ld(t, name)
-
-
-def _float_type(t, name, f32=True):
-    code = _DTYPES.get(t.dtype)
-    if code is None or (code == MNB_F32 and not f32):
-        raise TypeError("%s must be float16%s, got %s" % (name, ", bfloat16 or float32" if f32 else " or bfloat16", t.dtype))
-    return code
-
-
-def _vector(t, name, dtype, n, dev):
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError("%s must be a contiguous [%d], got shape %s" % (name, n, tuple(t.shape)))
-    if t.device != dev:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
 
 
 def _blocks(K, name):
@@ -204,7 +177,10 @@ class MxTensor:
         rows, per_row = codes.shape
         K = per_row * 2 if fmt == MNB_MX_FP4 else per_row
         _blocks(K, "the last axis of an MX tensor")
-        _beside(scales, "MX scales", torch.uint8, (rows, K // 32), codes.device)
+        _ld(scales, "MX scales")
+        if scales.shape != (rows, K // 32) or scales.device != codes.device:
+            raise ValueError("MX scales must be [%d, %d] on %s, got %s on %s"
+                             % (rows, K // 32, codes.device, tuple(scales.shape), scales.device))
         need = _scale_row(K)
         # the row distance counts for one row too, as its scales are read in 16-byte pieces
         lds = scales.stride(0) if rows > 1 else need
@@ -214,21 +190,16 @@ class MxTensor:
                              "(mx_tensor lays them out so)" % need)
         self.codes, self.scales, self.fmt, self.rows, self.K, self.ldc, self.lds = codes, scales, fmt, rows, K, ldc, lds
 
-    @classmethod
-    def _new(cls, like, rows, K, fmt):
-        """Uninitialised, on the device of ``like``."""
-        _format(fmt)
-        q = object.__new__(cls)
-        ldc, lds = K // 2 if fmt == MNB_MX_FP4 else K, _scale_row(K)
-        s = like.new_empty((rows, lds), dtype=torch.uint8)
-        q.codes = like.new_empty((rows, ldc), dtype=torch.uint8)
-        q.scales = s if lds == K // 32 else s[:, :K // 32]
-        q.fmt, q.rows, q.K, q.ldc, q.lds = fmt, rows, K, ldc, lds
-        return q
-
     def __repr__(self):
         return "MxTensor([%d, %d], %s, %s)" % (self.rows, self.K, "FP4" if self.fmt == MNB_MX_FP4 else "FP8",
                                                self.codes.device)
+
+
+def _made(codes, scales, fmt, ldc, lds, rows, K):
+    """An MxTensor that a call here has just laid out."""
+    q = object.__new__(MxTensor)
+    q.codes, q.scales, q.fmt, q.rows, q.K, q.ldc, q.lds = codes, scales, fmt, rows, K, ldc, lds
+    return q
 
 
 def mx_tensor(codes, scales, fmt: int) -> MxTensor:
@@ -252,27 +223,13 @@ def mx_quantize(x, fmt: int = MNB_MX_FP4) -> MxTensor:
     """x [M, K] (fp16, bf16 or fp32, K a multiple of 32) to MX: one power-of-two scale for
     each 32 elements, 2^(floor(log2 max|x|) - 2 (FP4) or - 8 (FP8)), elements rounded to
     nearest even and clamped.  A block with an infinity or NaN stands for NaN throughout."""
-    code = _float_type(x, "x")
-    ldx = _ld(x, "x")
-    M, K = x.shape
-    _blocks(K, "the last axis of x")
-    q = MxTensor._new(x, M, K, fmt)
-    _call(x.device, lib.mnb_mx_quantize, x.data_ptr(), code, M, K, ldx, fmt, q.codes.data_ptr(), q.ldc,
-          q.scales.data_ptr(), q.lds)
-    return q
+    codes, scales, ldc, lds, rows, K = _run(_ext.quantize, x, fmt)
+    return _made(codes, scales, fmt, ldc, lds, rows, K)
 
 
 def mx_dequantize(q: MxTensor, dtype=None, out=None):
     """The values of an MX tensor in ``dtype`` (fp16 by default), each rounded once."""
-    dtype = dtype or torch.float16
-    M, K = q.rows, q.K
-    if out is None:
-        out, ldy = q.codes.new_empty((M, K), dtype=dtype), K
-    else:
-        ldy = _beside(out, "out", dtype, (M, K), q.codes.device)
-    _call(q.codes.device, lib.mnb_mx_dequantize, q.codes.data_ptr(), q.ldc, q.scales.data_ptr(), q.lds, q.fmt, M, K,
-          out.data_ptr(), _float_type(out, "out"), ldy)
-    return out
+    return _run(_ext.dequantize, q.codes, q.scales, q.fmt, q.rows, q.K, q.ldc, q.lds, dtype or torch.float16, out)
 
 
 class MxWeight:
@@ -296,36 +253,18 @@ def mx_pack(q: MxTensor) -> MxWeight:
     st, wqb, scb = mnb_mx_packed_sizes(q.rows, q.K)
     _check(st)
     w = MxWeight(q.codes.new_empty(wqb), q.codes.new_empty(scb), q.rows, q.K)
-    _call(q.codes.device, lib.mnb_mx_pack, q.codes.data_ptr(), q.ldc, q.scales.data_ptr(), q.lds, q.rows, q.K,
-          w.wq.data_ptr(), w.sc.data_ptr())
+    if not q.codes.is_cuda:
+        raise ValueError("tensors must be on a GPU, got %s" % q.codes.device)
+    _run(lambda stream, codes: _check(lib.mnb_mx_pack(codes.data_ptr(), q.ldc, q.scales.data_ptr(), q.lds, q.rows, q.K,
+                                                      w.wq.data_ptr(), w.sc.data_ptr(), stream)), q.codes)
     return w
 
 
 def mx_matmul(x: MxTensor, w: MxWeight, bias=None, dtype=None, out=None):
     """Y [M, N] = x . w^T (+ bias [N]) in ``dtype`` (fp16 by default, or bf16; the bias's type too),
     summed in 32 bits and rounded once; x FP8 or FP4 from mx_quantize, rmsnorm or mx_tensor."""
-    codes = x.codes
-    dev, M, K, N = codes.device, x.rows, x.K, w.N
-    dtype = dtype or torch.float16
-    code = _DTYPES.get(dtype)
-    if code is None or code == MNB_F32:
-        raise TypeError("the output must be float16 or bfloat16, got %s" % dtype)
-    if K != w.K:
-        raise ValueError("x has K=%d, weight has K=%d" % (K, w.K))
-    if w.wq.device != dev:
-        raise ValueError("the weight is on %s, expected %s" % (w.wq.device, dev))
-    if out is None:
-        out = codes.new_empty((M, N), dtype=dtype)
-    elif out.dtype != dtype or out.shape != (M, N) or not out.is_contiguous() or out.device != dev:
-        raise ValueError("out must be a contiguous %s [%d, %d] on %s" % (dtype, M, N, dev))
-    if bias is not None:
-        _vector(bias, "bias", dtype, N, dev)
-        bias = bias.data_ptr()
-    need = lib.mnb_mx_workspace_bytes(M, N, K, x.fmt)
-    ws = codes.new_empty(need) if need else None
-    _call(dev, lib.mnb_mx_matmul, codes.data_ptr(), x.ldc, x.scales.data_ptr(), x.lds, x.fmt, w.wq.data_ptr(),
-          w.sc.data_ptr(), bias, out.data_ptr(), code, M, N, K, ws.data_ptr() if need else None, need)
-    return out
+    return _run(_ext.matmul, x.codes, x.scales, x.fmt, x.rows, x.K, x.ldc, x.lds, w.wq, w.sc, w.N, w.K, bias,
+                dtype or torch.float16, out)
 
 
 class Normed(NamedTuple):
@@ -341,35 +280,8 @@ def rmsnorm(x, weight, eps: float = 1e-6, residual=None, fmt: int | None = None,
     and in x's type too with ``keep16`` (an adapter's projection wants it).  ``hidden`` (given a
     residual) receives h in x's type and may be ``residual`` or ``x`` itself; ``out`` receives y
     and may be ``x``.  Each output is rounded once from 32 bits."""
-    code = _float_type(x, "x", f32=False)
-    ldx = _ld(x, "x")
-    shape, dev, dtype = x.shape, x.device, x.dtype
-    M, K = shape
-    _vector(weight, "weight", dtype, K, dev)
-    rp = hp = yp = cp = sp = y = q = None
-    ldr = ldh = ldy = ldc = lds = 0
-    if residual is not None:
-        ldr = _beside(residual, "residual", dtype, shape, dev)
-        if hidden is None:
-            hidden, ldh = x.new_empty(shape), K
-        else:
-            ldh = _beside(hidden, "hidden", dtype, shape, dev)
-        rp, hp = residual.data_ptr(), hidden.data_ptr()
-    elif hidden is not None:
-        raise ValueError("hidden needs a residual")
-    if fmt is None or keep16 or out is not None:
-        if out is None:
-            y, ldy = x.new_empty(shape), K
-        else:
-            y, ldy = out, _beside(out, "out", dtype, shape, dev)
-        yp = y.data_ptr()
-    if fmt is not None:
-        _blocks(K, "the last axis of x")
-        q = MxTensor._new(x, M, K, fmt)
-        cp, ldc, sp, lds = q.codes.data_ptr(), q.ldc, q.scales.data_ptr(), q.lds
-    _call(dev, lib.mnb_rmsnorm, x.data_ptr(), ldx, rp, ldr, weight.data_ptr(), eps, code, M, K, hp, ldh, yp, ldy,
-          fmt or 0, cp, ldc, sp, lds)
-    return Normed(y, q, hidden)
+    y, h, codes, scales, ldc, lds, rows, K = _run(_ext.rmsnorm, x, weight, eps, residual, fmt, keep16, out, hidden)
+    return Normed(y, None if fmt is None else _made(codes, scales, fmt, ldc, lds, rows, K), h)
 
 
 class LogProbs(NamedTuple):
@@ -383,26 +295,4 @@ def logprobs(logits, tokens=None, top: int = 0) -> LogProbs:
     """For each row of logits [M, V] (fp16, bf16 or fp32): the log probability of tokens[m]
     (int64; 0 for a negative token, NaN for one past V), the entropy, and the ``top`` (at most 32)
     likeliest tokens in falling order, equal ones by the lower index."""
-    code = _float_type(logits, "logits")
-    ldl = _ld(logits, "logits")
-    M, V = logits.shape
-    dev = logits.device
-    if not 0 <= top <= min(MNB_LOGPROBS_MAX_TOP, V):
-        raise ValueError("top must be from 0 to %d, got %d" % (min(MNB_LOGPROBS_MAX_TOP, V), top))
-    if V == 0 and M > 0:
-        raise ValueError("logits have no columns")
-    tp = lp = lpp = tl = tlp = tt = ttp = ws = None
-    if tokens is not None:
-        _vector(tokens, "tokens", torch.int64, M, dev)
-        lp = logits.new_empty(M, dtype=torch.float32)
-        tp, lpp = tokens.data_ptr(), lp.data_ptr()
-    ent = logits.new_empty(M, dtype=torch.float32)
-    if top:
-        tl, tt = logits.new_empty((M, top), dtype=torch.float32), logits.new_empty((M, top), dtype=torch.int64)
-        tlp, ttp = tl.data_ptr(), tt.data_ptr()
-    need = lib.mnb_logprobs_workspace_bytes(M, V, code, top)
-    if need:
-        ws = logits.new_empty(need, dtype=torch.uint8)
-    _call(dev, lib.mnb_logprobs, logits.data_ptr(), code, M, V, ldl, tp, top, lpp, ent.data_ptr(), tlp, ttp,
-          ws.data_ptr() if need else None, need)
-    return LogProbs(lp, ent, tl, tt)
+    return LogProbs(*_run(_ext.logprobs, logits, tokens, top))
