@@ -408,7 +408,7 @@ int logprobs_chunks(int M, int V, int dtype, int *chunk) {
   const int sizes[] = {kSmall, kMiddle, kLarge};
   for (int i = 0; i < 3; ++i) {
     const int64_t parts = ((int64_t)V + sizes[i] - 1) / sizes[i];
-    if (i == 2 || (parts <= 32 && (parts == 1 || (int64_t)M * parts <= 4 * kCUs))) {
+    if (V <= kLarge ? parts == 1 : i == 2 || (parts <= 32 && (int64_t)M * parts <= 4 * kCUs)) {
       *chunk = sizes[i];
       return (int)parts;
     }
