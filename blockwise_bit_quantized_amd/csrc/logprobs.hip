@@ -80,6 +80,17 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
   return v;
 }
 
+// How many of n keys in LDS are larger than `k`, counted by 8 neighbouring lanes that share k; the
+// 8 lanes run it together.  (One lane alone waits for LDS once a key: 320 keys took 10 us.)
+__device__ __forceinline__ int count_larger(const uint64_t *keys, int n, uint64_t k, int lane) {
+  int c = 0;
+#pragma unroll 4
+  for (int o = lane & 7; o < n; o += 8) c += keys[o] > k;
+  c += __builtin_amdgcn_update_dpp(0, c, kQuad1, 0xf, 0xf, true);
+  c += __builtin_amdgcn_update_dpp(0, c, kQuad2, 0xf, 0xf, true);
+  return c + __builtin_amdgcn_update_dpp(0, c, kMirror8, 0xf, 0xf, true);
+}
+
 // one piece of 8 elements as loaded
 template <int DT> struct Piece { u4_t v[DT == DT_F32 ? 2 : 1]; };
 template <int DT>
@@ -197,9 +208,14 @@ __global__ __launch_bounds__(WAVES * 64, DT == DT_F32 || WAVES < 8 ? 1 : 4) void
     atomicAdd(&larger[lane], n);
   }
 
+  // Exponents are x log2(e) - fl(m log2(e)), one fused operation an element; the rounding of the
+  // constant, `off`, is the same in all of them and is taken out of the sums.  (Not for the wider
+  // types, whose m log2(e) may overflow.)
+  constexpr bool kFused = DT == DT_F16;
+  const float base = shift * kLog2e, off = kFused && base < 1e30f ? fmaf(shift, kLog2e, -base) : 0.f;
   float S = 0.f, Tn = 0.f;                // Tn in units of log 2
   auto add = [&](float v, float &s, float &u) {
-    const float d = (v - shift) * kLog2e;
+    const float d = kFused ? fmaf(v, kLog2e, -base) : (v - shift) * kLog2e;
     const float e = __builtin_amdgcn_exp2f(d);
     s += e;
     u = fmaf(e, fmaxf(d, -1e4f), u);      // e is 0 there: 0, and not 0 times infinity
@@ -227,6 +243,11 @@ __global__ __launch_bounds__(WAVES * 64, DT == DT_F32 || WAVES < 8 ? 1 : 4) void
   for (int i = 0; i < WAVES; ++i) {
     S += red[i][0];
     Tn += red[i][1];
+  }
+  if constexpr (kFused) {
+    const float f = __builtin_amdgcn_exp2f(-off);
+    Tn = (Tn - off * S) * f;
+    S *= f;
   }
   Tn *= kLn2;
 
@@ -267,11 +288,10 @@ __global__ __launch_bounds__(WAVES * 64, DT == DT_F32 || WAVES < 8 ? 1 : 4) void
     }
   };
   auto rank_all = [&](int n) {
-    for (int a = t; a < n; a += THREADS) {
+    for (int a = t / 8; a < n; a += THREADS / 8) {
       const uint64_t k = cand[a];
-      int rank = 0;
-      for (int o = 0; o < n; ++o) rank += cand[o] > k;
-      if (rank < p.top) emit(rank, k);
+      const int rank = count_larger(cand, n, k, lane);
+      if ((lane & 7) == 0 && rank < p.top) emit(rank, k);
     }
   };
 
@@ -338,15 +358,19 @@ __global__ __launch_bounds__(WAVES * 64, DT == DT_F32 || WAVES < 8 ? 1 : 4) void
   }
 }
 
-// joins the parts of a row: one workgroup of 256 threads per row
+// joins the parts of a row: one workgroup of 256 threads per row; LDS holds the row's parts and
+// keys, so that the loops over them wait for memory once
 template <int DT>
 __global__ __launch_bounds__(256) void join_kernel(LogprobsParams p) {
-  extern __shared__ uint64_t keys[];   // [chunks * top]
+  extern __shared__ uint64_t keys[];   // [chunks * top], then the parts
   const int t = threadIdx.x;
   const int64_t row = blockIdx.x;
-  const f4_t *part = reinterpret_cast<const f4_t *>(p.part) + row * p.chunks;
   const int n = p.chunks * p.top;
+  f4_t *part = reinterpret_cast<f4_t *>(keys + (n + 1) / 2 * 2);
+  for (int i = t; i < p.chunks; i += 256) part[i] = reinterpret_cast<const f4_t *>(p.part)[row * p.chunks + i];
   for (int i = t; i < n; i += 256) keys[i] = p.keys[row * n + i];
+  const float xt = t == 0 ? token_logit<DT>(p, row) : 0.f;
+  __syncthreads();
   // every thread joins the sums in part order, so all hold the same values
   float m = -__builtin_inff();
   bool nan = false;
@@ -366,14 +390,11 @@ __global__ __launch_bounds__(256) void join_kernel(LogprobsParams p) {
     if (f != 0.f) T += f * (v[2] + d * v[1]);   // (x - m_i) + (m_i - m)
   }
   const float ls = logf(S);
-  if (t == 0) write_row(p, row, m, S, T, token_logit<DT>(p, row));
-  __syncthreads();
-  for (int a = t; a < n; a += 256) {
+  if (t == 0) write_row(p, row, m, S, T, xt);
+  for (int a = t / 8; a < n; a += 32) {
     const uint64_t k = keys[a];
-    if (k == 0) continue;
-    int rank = 0;
-    for (int o = 0; o < n; ++o) rank += keys[o] > k;
-    if (rank < p.top) {
+    const int rank = count_larger(keys, n, k, t);
+    if ((t & 7) == 0 && k != 0 && rank < p.top) {
       p.top_tokens[row * p.top + rank] = (int64_t)(uint32_t)~(uint32_t)k;
       p.top_logprobs[row * p.top + rank] = (order_value((uint32_t)(k >> 32)) - m) - ls;
     }
@@ -390,12 +411,17 @@ hipError_t launch(const LogprobsParams &p, hipStream_t s) {
   const dim3 grid((uint32_t)((int64_t)p.M * p.chunks));
   if (p.chunk <= kSmall) hipLaunchKernelGGL((part_kernel<DT, 4, 2>), grid, dim3(256), 0, s, p);
   else if (p.chunk <= kMiddle) hipLaunchKernelGGL((part_kernel<DT, 8, 4>), grid, dim3(512), 0, s, p);
-  // 32-bit rows take twice the registers: 6 pieces a thread instead of 12
-  else if constexpr (DT == DT_F32) hipLaunchKernelGGL((part_kernel<DT, 16, 6>), grid, dim3(1024), 0, s, p);
-  else hipLaunchKernelGGL((part_kernel<DT, 8, 12>), grid, dim3(512), 0, s, p);
+  // 16 waves for one workgroup per CU (one row of 49152 fp16: 7.5 against 8.5 us); with more the 8
+  // waves' smaller workgroups overlap (1024 rows: 29.3 against 40.3).  32-bit rows take
+  // twice the registers: 6 pieces a thread always.
+  else if (DT == DT_F32 || (int64_t)p.M * p.chunks <= kCUs)
+    hipLaunchKernelGGL((part_kernel<DT, 16, 6>), grid, dim3(1024), 0, s, p);
+  else
+    hipLaunchKernelGGL((part_kernel<DT == DT_F32 ? DT_F16 : DT, 8, 12>), grid, dim3(512), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.chunks == 1) return e;
-  hipLaunchKernelGGL((join_kernel<DT>), dim3((uint32_t)p.M), dim3(256), (uint32_t)(p.chunks * p.top * sizeof(uint64_t)), s, p);
+  const uint32_t lds = (uint32_t)((p.chunks * p.top + 1) / 2 * 16 + p.chunks * 16);   // below 22 KiB
+  hipLaunchKernelGGL((join_kernel<DT>), dim3((uint32_t)p.M), dim3(256), lds, s, p);
   return hipGetLastError();
 }
 

@@ -88,7 +88,15 @@ __global__ __launch_bounds__(WAVES * 64) void norm_kernel(NormParams p) {
   const float r32 = (float)rstd;
 
   auto finish = [&](int c, float *v) {
-    if (p.hidden) store8<DT>(p.hidden + row * p.ldh + 8 * (int64_t)c, v);
+    if (p.hidden) {
+      uint16_t *to = p.hidden + row * p.ldh + 8 * (int64_t)c;
+      // with MX outputs the next call reads those and not the hidden rows: past the caches
+      // 8192 x 4096 takes 45.7 us, not 48.2 (with 16-bit outputs 57.8, not 55.1, so not there)
+      if constexpr (FMT >= 0)
+        __builtin_nontemporal_store(u4_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])},
+                                    reinterpret_cast<u4_t *>(to));
+      else store8<DT>(to, v);
+    }
     float w[8], h8[8];
     load8<DT>(p.w + 8 * (int64_t)c, w);
     uint32_t border = ~0u;
@@ -166,8 +174,13 @@ hipError_t launch(const NormParams &p, hipStream_t s) {
       return hipGetLastError();
     }
   }
+  // As few pieces a thread as give a workgroup the row, of 4 or 16 waves: with 4 pieces 8192 x 2560
+  // (FP4 out) took 45.1 us and 4096 x 8192 (16 bits) 55.1, with 2 and 1 they take 43.6 and 50.4;
+  // 16 waves for 4096 k took 67 where 4 take 48.
   if (p.K <= 2048) hipLaunchKernelGGL((norm_kernel<DT, FMT, 4, 1>), grid, dim3(256), 0, s, p);
-  else if (p.K <= 8192) hipLaunchKernelGGL((norm_kernel<DT, FMT, 4, 4>), grid, dim3(256), 0, s, p);
+  else if (p.K <= 4096) hipLaunchKernelGGL((norm_kernel<DT, FMT, 4, 2>), grid, dim3(256), 0, s, p);
+  else if (p.K <= 8192) hipLaunchKernelGGL((norm_kernel<DT, FMT, 16, 1>), grid, dim3(1024), 0, s, p);
+  else if (p.K <= 16384) hipLaunchKernelGGL((norm_kernel<DT, FMT, 16, 2>), grid, dim3(1024), 0, s, p);
   else hipLaunchKernelGGL((norm_kernel<DT, FMT, 16, 4>), grid, dim3(1024), 0, s, p);
   return hipGetLastError();
 }
