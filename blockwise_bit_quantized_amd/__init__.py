@@ -413,5 +413,5 @@ _ops._bind(lib, mnb_status_string)
 from .ops import (  # noqa: E402,F401
     MNB_BF16, MNB_F16, MNB_F32, MNB_LOGPROBS_MAX_TOP, MNB_MX_FP4, MNB_MX_FP8, LogProbs, MxTensor, MxWeight, Normed,
     logprobs, mnb_logprobs, mnb_logprobs_workspace_bytes, mnb_mx_dequantize, mnb_mx_describe_route, mnb_mx_matmul,
-    mnb_mx_pack, mnb_mx_packed_sizes, mnb_mx_quantize, mnb_mx_workspace_bytes, mnb_ops_version, mnb_rmsnorm,
+    mnb_mx_pack, mnb_mx_packed_sizes, mnb_mx_quantize, mnb_ops_version, mnb_rmsnorm,
     mx_dequantize, mx_matmul, mx_pack, mx_quantize, mx_tensor, rmsnorm)

@@ -125,12 +125,6 @@ int mnb_mx_pack(const void *codes, int64_t ldc, const void *scales, int64_t lds,
                                as_stream(stream)));
 }
 
-size_t mnb_mx_workspace_bytes(int M, int N, int K, int fmt) {
-  if (check_matmul_sizes(M, N, K, fmt) || M <= kMxGemvMaxM || N == 0 || K == 0) return 0;
-  const int splits = mx_gemm_splits(M, N, K, fmt);
-  return splits > 1 ? (size_t)splits * M * N * sizeof(float) : 0;
-}
-
 int mnb_mx_describe_route(int M, int N, int K, int fmt, char *buf, size_t buf_len) {
   const int st = check_matmul_sizes(M, N, K, fmt);
   if (st) return st;
@@ -139,13 +133,12 @@ int mnb_mx_describe_route(int M, int N, int K, int fmt, char *buf, size_t buf_le
   if (M == 0 || N == 0) snprintf(buf, buf_len, "noop");
   else if (K == 0) snprintf(buf, buf_len, "fill");
   else if (M <= kMxGemvMaxM) snprintf(buf, buf_len, "mx_gemv_%s ksplit=%d", name, mx_gemv_ksplit(N, K));
-  else snprintf(buf, buf_len, "mx_gemm_%s splits=%d", name, mx_gemm_splits(M, N, K, fmt));
+  else snprintf(buf, buf_len, "mx_gemm_%s tile=%dx%d", name, mx_gemm_rows(M, N) == 64 ? 64 : 128, mx_gemm_rows(M, N) == 256 ? 256 : 128);
   return MNB_OK;
 }
 
 int mnb_mx_matmul(const void *codes, int64_t ldc, const void *scales, int64_t lds, int fmt, const void *wq, const void *sc,
-                  const void *bias, void *Y, int dtype, int M, int N, int K, void *workspace, size_t ws_bytes,
-                  void *stream) {
+                  const void *bias, void *Y, int dtype, int M, int N, int K, void *stream) {
   int st = check_matmul_sizes(M, N, K, fmt);
   if (st) return st;
   if (bad_dtype(dtype, false)) return MNB_ERR_INVALID_ARG;
@@ -160,15 +153,12 @@ int mnb_mx_matmul(const void *codes, int64_t ldc, const void *scales, int64_t ld
   st = check_mx(fmt, K, codes, ldc, scales, lds);
   if (st) return st;
   if (ldc > 2 * kMxMaxK || lds > 2 * kMxMaxK) return MNB_ERR_UNSUPPORTED;
-  if (off16(wq) || off16(sc) || off16(workspace)) return MNB_ERR_MISALIGNED;
-  const size_t need = mnb_mx_workspace_bytes(M, N, K, fmt);
-  if (need && (!workspace || ws_bytes < need)) return MNB_ERR_WORKSPACE;
+  if (off16(wq) || off16(sc)) return MNB_ERR_MISALIGNED;
   size_t wqb = 0, scb = 0;
   mnb_mx_packed_sizes(N, K, &wqb, &scb);
   const Span x{codes, M, ldc, mx_row(fmt, K)}, e{scales, M, lds, scale_row(K)}, w{wq, 1, 0, (int64_t)wqb},
-      s{sc, 1, 0, (int64_t)scb}, ws{need ? workspace : nullptr, 1, 0, (int64_t)need};
-  if (overlap(y, x) || overlap(y, e) || overlap(y, w) || overlap(y, s) || overlap(y, ws)) return MNB_ERR_ALIAS;
-  if (overlap(ws, x) || overlap(ws, e) || overlap(ws, w) || overlap(ws, s) || overlap(ws, bi)) return MNB_ERR_ALIAS;
+      s{sc, 1, 0, (int64_t)scb};
+  if (overlap(y, x) || overlap(y, e) || overlap(y, w) || overlap(y, s)) return MNB_ERR_ALIAS;
   MxMatmulParams p{};
   p.codes = static_cast<const uint8_t *>(codes);
   p.scales = static_cast<const uint8_t *>(scales);
@@ -185,8 +175,6 @@ int mnb_mx_matmul(const void *codes, int64_t ldc, const void *scales, int64_t ld
   p.KS = (int)cdiv(K, kMxStep);
   p.KB = (int)cdiv(K, kMxScaleK);
   if (M <= kMxGemvMaxM) return status(launch_mx_gemv(dtype, fmt, p, as_stream(stream)));
-  p.splits = mx_gemm_splits(M, N, K, fmt);
-  p.part = static_cast<float *>(workspace);
   return status(launch_mx_gemm(dtype, fmt, p, as_stream(stream)));
 }
 

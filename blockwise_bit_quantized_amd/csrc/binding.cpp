@@ -26,7 +26,6 @@ struct {
   decltype(&mnb_mx_quantize) quantize;
   decltype(&mnb_mx_dequantize) dequantize;
   decltype(&mnb_mx_matmul) matmul;
-  decltype(&mnb_mx_workspace_bytes) matmul_ws;
   decltype(&mnb_rmsnorm) rmsnorm;
   decltype(&mnb_logprobs) logprobs;
   decltype(&mnb_logprobs_workspace_bytes) logprobs_ws;
@@ -199,10 +198,8 @@ PyObject *matmul(PyObject *const *a) {
          codes.device().str().c_str());
   if (bias.defined()) vector(bias, "bias", type, N, codes.device());
   on_gpu(codes);
-  const size_t need = c.matmul_ws(size(M), size(N), size(K), fmt);
-  const at::Tensor ws = need ? empty({(int64_t)need}, codes, at::kByte) : at::Tensor();
   check(c.matmul(data(codes), integer(a[6]), data(scales), integer(a[7]), fmt, data(wq), data(sc), data(bias), data(y), code, size(M),
-                 size(N), size(K), data(ws), need, pointer(a[0])));
+                 size(N), size(K), pointer(a[0])));
   return wrap(y);
 }
 
@@ -278,7 +275,7 @@ PyObject *logprobs(PyObject *const *a) {
 // bind(address, ...): the C functions in the order of `c`
 PyObject *bind(PyObject *const *a) {
   void **to = reinterpret_cast<void **>(&c);
-  for (int i = 0; i < 8; ++i) to[i] = pointer(a[i]);
+  for (int i = 0; i < 7; ++i) to[i] = pointer(a[i]);
   Py_RETURN_NONE;
 }
 
@@ -303,7 +300,7 @@ PyMethodDef method(const char *name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<F, N>)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef methods[] = {method<bind, 8>("bind"),
+PyMethodDef methods[] = {method<bind, 7>("bind"),
                          method<quantize, 3>("quantize"),
                          method<dequantize, 10>("dequantize"),
                          method<matmul, 15>("matmul"),

@@ -312,11 +312,6 @@ int mx_gemm_rows(int M, int N) {
   return mid >= kCUs / 2 ? 128 : 64;
 }
 
-int mx_gemm_splits(int M, int N, int K, int fmt) {
-  (void)M; (void)N; (void)K; (void)fmt;
-  return 1;
-}
-
 hipError_t launch_mx_gemm(int dtype, int fmt, const MxMatmulParams &p, hipStream_t s) {
   if (dtype == DT_F16) return fmt == MX_FP4 ? launch<DT_F16, MX_FP4>(p, s) : launch<DT_F16, MX_FP8>(p, s);
   return fmt == MX_FP4 ? launch<DT_BF16, MX_FP4>(p, s) : launch<DT_BF16, MX_FP8>(p, s);

@@ -158,15 +158,12 @@ struct MxMatmulParams {
   uint16_t *y;
   int64_t ldc, lds;
   int M, N, K, NG, KS, KB;
-  float *part;                     // K split over workgroups: FP32 partial outputs [splits, M, N]
-  int splits;
 };
-constexpr int kMxGemvMaxM = 16;
+constexpr int kMxGemvMaxM = 32;
 hipError_t launch_mx_gemv(int dtype, int fmt, const MxMatmulParams &p, hipStream_t s);
 hipError_t launch_mx_gemm(int dtype, int fmt, const MxMatmulParams &p, hipStream_t s);
-int mx_gemv_ksplit(int N, int K);                    // waves that share a weight row's K: 1, 2, 4 or 8
-int mx_gemm_rows(int M, int N);                      // rows of an output tile: 64, 128 or 256
-int mx_gemm_splits(int M, int N, int K, int fmt);    // K ranges per output tile
+int mx_gemv_ksplit(int N, int K);                    // waves that share a weight row's K: 1, 2 or 4
+int mx_gemm_rows(int M, int N);                      // 256 (two 128 x 256 tiles a CU), 128 or 64
 
 struct NormParams {
   const uint16_t *x, *res, *w;

@@ -41,8 +41,7 @@ def _bind(library, status_text):
             ("mnb_mx_dequantize", I, [P, L, P, L, I, I, I, P, I, L, P]),
             ("mnb_mx_packed_sizes", I, [I, I, sizes, sizes]),
             ("mnb_mx_pack", I, [P, L, P, L, I, I, P, P, P]),
-            ("mnb_mx_workspace_bytes", S, [I, I, I, I]),
-            ("mnb_mx_matmul", I, [P, L, P, L, I, P, P, P, P, I, I, I, I, P, S, P]),
+            ("mnb_mx_matmul", I, [P, L, P, L, I, P, P, P, P, I, I, I, I, P]),
             ("mnb_mx_describe_route", I, [I, I, I, I, C.c_char_p, S]),
             ("mnb_rmsnorm", I, [P, L, P, L, P, F, I, I, I, P, L, P, L, I, P, L, P, L, P]),
             ("mnb_logprobs_workspace_bytes", S, [I, I, I, I]),
@@ -53,7 +52,7 @@ def _bind(library, status_text):
     if torch is not None:
         from . import _mnb_ops as _ext   # built with the library; there is no other path
         _ext.bind(*(C.cast(getattr(lib, n), P).value for n in (
-            "mnb_mx_quantize", "mnb_mx_dequantize", "mnb_mx_matmul", "mnb_mx_workspace_bytes", "mnb_rmsnorm",
+            "mnb_mx_quantize", "mnb_mx_dequantize", "mnb_mx_matmul", "mnb_rmsnorm",
             "mnb_logprobs", "mnb_logprobs_workspace_bytes", "mnb_status_string")))
 
 
@@ -82,10 +81,6 @@ def mnb_mx_packed_sizes(N, K):
 
 def mnb_mx_pack(*args) -> int:
     return lib.mnb_mx_pack(*args)
-
-
-def mnb_mx_workspace_bytes(M, N, K, fmt) -> int:
-    return lib.mnb_mx_workspace_bytes(M, N, K, fmt)
 
 
 def mnb_mx_matmul(*args) -> int:

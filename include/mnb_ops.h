@@ -68,15 +68,13 @@ int mnb_mx_pack(const void *codes, int64_t ldc, const void *scales, int64_t lds,
  * by mnb_mx_pack; Y fp16 or bf16 [M, N] row-major, rounded once from FP32 accumulation; bias
  * [N] of Y's type or NULL.  K % 32 == 0, K < 2^22; ldc and lds at most 2^23.  A NaN scale or element of X reaches its
  * own row of Y only, one of W its own column.  codes, scales, wq, sc and Y 16-byte aligned, as
- * are ldc and lds; bias 16-byte aligned.  Y must not overlap the inputs or the workspace.
+ * are ldc and lds; bias 16-byte aligned.  Y must not overlap the inputs.
  *
- * M <= 16 streams the weight once for all rows; more rows run as 128 x 128 output tiles.
- * workspace: at least mnb_mx_workspace_bytes(M, N, K, fmt) bytes, 16-byte aligned (NULL if that is 0).
+ * M <= 32 streams the weight once for all rows; more rows run as tiles of 64 or 128 rows.
  */
-size_t mnb_mx_workspace_bytes(int M, int N, int K, int fmt);
 int mnb_mx_matmul(const void *codes, int64_t ldc, const void *scales, int64_t lds, int fmt,
                   const void *wq, const void *sc, const void *bias, void *Y, int dtype, int M,
-                  int N, int K, void *workspace, size_t ws_bytes, void *stream);
+                  int N, int K, void *stream);
 
 /* The kernels mnb_mx_matmul would launch, as text (host only), e.g. "mx_gemv_fp8 ...". */
 int mnb_mx_describe_route(int M, int N, int K, int fmt, char *buf, size_t buf_len);

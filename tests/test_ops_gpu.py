@@ -136,7 +136,7 @@ def test_pack_layout(N, K):
 # ------------------------------------------------------------------------------------------
 
 SHAPES = [(1, 1, 32), (1, 64, 128), (1, 896, 896), (1, 1000, 4096), (2, 65, 96), (5, 200, 576), (8, 1000, 640), (16, 130, 1056),
-          (16, 3000, 512), (17, 64, 32), (17, 65, 160), (33, 72, 576), (64, 320, 512), (100, 130, 1056), (128, 128, 2048),
+          (16, 3000, 512), (17, 64, 32), (17, 65, 160), (20, 3000, 512), (32, 1000, 1056), (33, 64, 32), (34, 65, 160), (33, 72, 576), (64, 320, 512), (100, 130, 1056), (128, 128, 2048),
           (129, 257, 320), (256, 512, 4096), (300, 1000, 800), (513, 136, 96)]
 
 
@@ -398,7 +398,7 @@ def check_logprobs(x, dt, tokens, top, got=None):
 
 @pytest.mark.parametrize("dtype", ["fp16", "bf16", "fp32"])
 @pytest.mark.parametrize("M,V,top", [(1, 1, 1), (3, 2, 2), (2, 31, 20), (5, 33, 32), (1, 500, 5), (4, 2041, 32), (3, 4088, 20),
-                                     (1, 4097, 8), (2, 16376, 3), (1, 49152, 5), (2, 50257, 20), (3, 57337, 32), (1, 262144, 32),
+                                     (1, 4097, 8), (2, 16376, 3), (1, 49152, 5), (2, 50257, 20), (3, 57337, 32), (2, 49153, 5), (1, 98305, 9), (2, 147456, 32), (1, 262144, 32),
                                      (300, 1000, 20), (260, 49152, 32), (1100, 2100, 1), (2, 131072, 0), (1, 1000003, 7)])
 def test_logprobs(dtype, M, V, top):
     r = rng(9, M, V, top)
@@ -489,6 +489,62 @@ def test_logprobs_extreme_sizes_of_numbers():
     x[2] = 6e4
     check_logprobs(dev(x).float(), None, np.array([9, 4999, 0]), 20)
     check_logprobs(dev(x).bfloat16(), None, np.array([9, 4999, 0]), 20)
+
+
+# ------------------------------------------------------------------------------------------
+# offsets past 32 bits, rows past one launch
+# ------------------------------------------------------------------------------------------
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^32 bytes and 2^31 elements: their last rows match the same rows alone."""
+    M, V = 45000, 49152
+    x = torch.zeros(M, V, dtype=torch.float16, device=DEV)
+    x[-3:] = dev(rng(18).standard_normal((3, V))).half()
+    tok = torch.arange(M, device=DEV)
+    got = mnb.logprobs(x, tok, 5)
+    check_logprobs(x[-3:].clone(), None, np.arange(M - 3, M), 5,
+                   mnb.LogProbs(got.logprob[-3:], got.entropy[-3:], got.top_logprobs[-3:], got.top_tokens[-3:]))
+    assert bool((got.top_tokens[0] == torch.arange(5, device=DEV)).all())
+    w = torch.ones(V, dtype=torch.float16, device=DEV)
+    for fmt in (FP4, FP8):
+        q = mnb.mx_quantize(x, fmt)
+        last = mnb.mx_quantize(x[-3:].clone(), fmt)
+        assert torch.equal(q.codes[-3:], last.codes) and torch.equal(q.scales[-3:], last.scales)
+        y = mnb.mx_dequantize(q)
+        assert torch.equal(y[-3:], mnb.mx_dequantize(last)) and not bool(y[:-3].any())
+        del q, y
+    n = mnb.rmsnorm(x, w, residual=x)
+    alone = mnb.rmsnorm(x[-3:].clone(), w, residual=x[-3:].clone())
+    assert torch.equal(n.y[-3:], alone.y) and torch.equal(n.hidden[-3:], alone.hidden)
+
+
+def test_product_offsets_past_32_bits():
+    """Y of more than 2^32 bytes, and X rows that lie megabytes apart."""
+    M, N, K = 45000, 49152, 64
+    r = rng(19)
+    (xq, xs), (wq, ws) = exact_operands(r, 64, N, K, FP8)
+    w = mnb.mx_pack(to_mx(wq, ws, FP4))
+    x64 = to_mx(xq, xs, FP8)
+    want = mnb.mx_matmul(x64, w)
+    rep = -(-M // 64)
+    x = mnb.mx_tensor(x64.codes.repeat(rep, 1)[:M], x64.scales.repeat(rep, 1)[:M], FP8)
+    y = mnb.mx_matmul(x, w)
+    assert torch.equal(y[:64], want) and torch.equal(y[M // 64 * 64:], want[:M % 64])
+    del y
+    apart = torch.zeros(300, (1 << 23) - 16, dtype=torch.uint8, device=DEV)
+    apart[:, :K] = x64.codes.repeat(5, 1)[:300]
+    x2 = mnb.mx_tensor(apart[:, :K], x64.scales.repeat(5, 1)[:300], FP8)
+    w2 = mnb.mx_pack(to_mx(wq[:200], ws[:200], FP4))
+    assert torch.equal(mnb.mx_matmul(x2, w2), want[:, :200].repeat(5, 1)[:300])
+
+
+def test_norm_rows_past_one_launch():
+    x = dev(rng(20).standard_normal((1, 32))).half().repeat((1 << 20) + 5, 1)
+    w = torch.ones(32, dtype=torch.float16, device=DEV)
+    n = mnb.rmsnorm(x, w, residual=x, fmt=FP8, keep16=True)
+    for t in (n.y, n.hidden, n.q.codes, n.q.scales):
+        assert bool((t == t[:1]).all())
 
 
 # ------------------------------------------------------------------------------------------

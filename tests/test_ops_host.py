@@ -23,7 +23,7 @@ P = [(i + 1) << 40 for i in range(12)]     # far apart, never dereferenced
 def test_every_declared_symbol_is_exported_and_bound():
     text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "mnb_ops.h")).read(), flags=re.S)
     names = sorted(set(re.findall(r"\b(mnb_[a-z_]+)\s*\(", text)))
-    assert len(names) == 11
+    assert len(names) == 10
     for n in names:
         assert hasattr(mnb.lib, n) and callable(getattr(mnb, n)), n
     assert mnb.mnb_ops_version() == 100
@@ -42,10 +42,10 @@ def test_packed_sizes_and_routes():
         assert st == OK
         return text
     assert route(0, 64, 64, 0) == "noop" and route(4, 64, 0, 1) == "fill"
-    assert route(1, 8192, 2048, 1).startswith("mx_gemv_fp8") and route(16, 8192, 2048, 0).startswith("mx_gemv_fp4")
-    assert route(17, 8192, 2048, 0).startswith("mx_gemm_fp4")
+    assert route(1, 8192, 2048, 1).startswith("mx_gemv_fp8") and route(32, 8192, 2048, 0).startswith("mx_gemv_fp4")
+    assert route(33, 8192, 2048, 0) == "mx_gemm_fp4 tile=64x128"
+    assert route(1024, 4096, 4096, 0).endswith("tile=128x128") and route(8192, 9728, 2560, 1).endswith("tile=128x256")
     assert mnb.mnb_mx_describe_route(1, 64, 64, 2)[0] == INVALID
-    assert mnb.mnb_mx_workspace_bytes(1, 8192, 2048, 1) == 0
 
 
 def quant(X=P[0], dt=0, M=4, K=64, ldx=64, fmt=1, c=P[1], ldc=64, s=P[2], lds=16):
@@ -74,8 +74,8 @@ def test_quantize_validation():
     assert g(None, 0, None, 0, 0, 64, None, None, None) == OK
 
 
-def mm(c=P[0], ldc=64, s=P[1], lds=16, fmt=1, wq=P[2], sc=P[3], b=None, y=P[4], dt=0, M=4, N=64, K=64, ws=None, wsb=0):
-    return mnb.mnb_mx_matmul(c, ldc, s, lds, fmt, wq, sc, b, y, dt, M, N, K, ws, wsb, None)
+def mm(c=P[0], ldc=64, s=P[1], lds=16, fmt=1, wq=P[2], sc=P[3], b=None, y=P[4], dt=0, M=4, N=64, K=64):
+    return mnb.mnb_mx_matmul(c, ldc, s, lds, fmt, wq, sc, b, y, dt, M, N, K, None)
 
 
 def test_matmul_validation():
@@ -90,10 +90,7 @@ def test_matmul_validation():
     assert mm(b=P[4] + 16) == ALIAS
     # a last row of a strided X that ends inside Y
     assert mm(y=P[0] + 3 * 4096 + 16, ldc=4096) == ALIAS
-    need = mnb.mnb_mx_workspace_bytes(32, 64, 8192, 1)
-    if need:
-        a = dict(M=32, K=8192, ldc=8192, lds=256)
-        assert mm(**a) == WORKSPACE and mm(ws=P[6], wsb=need - 1, **a) == WORKSPACE and mm(ws=P[4], wsb=need, **a) == ALIAS
+    assert mm(ldc=(1 << 23) + 16) == UNSUPPORTED and mm(lds=(1 << 23) + 16) == UNSUPPORTED
 
 
 def norm(x=P[0], ldx=64, r=P[1], ldr=64, w=P[2], eps=1e-6, dt=0, M=4, K=64, h=P[3], ldh=64, y=P[4], ldy=64, fmt=0, c=None,
@@ -132,9 +129,10 @@ def test_logprobs_validation():
     assert lp(x=P[0] + 1) == MISALIGNED and lp(x=P[0] + 2, dt=2) == MISALIGNED and lp(tok=P[1] + 4) == MISALIGNED
     assert lp(e=P[3] + 2) == MISALIGNED and lp(**dict(t, tt=P[5] + 4)) == MISALIGNED
     assert lp(o=P[0] + 64) == ALIAS and lp(e=P[2]) == ALIAS and lp(**dict(t, tt=P[1])) == ALIAS
-    need = mnb.mnb_logprobs_workspace_bytes(1, 49152, 0, 5)
+    assert mnb.mnb_logprobs_workspace_bytes(1, 49152, 0, 5) == 0     # one workgroup holds the row
+    need = mnb.mnb_logprobs_workspace_bytes(1, 100000, 0, 5)
     assert need > 0
-    a = dict(M=1, V=49152, ldl=49152)
+    a = dict(M=1, V=100000, ldl=100000)
     assert lp(**a, **t) == WORKSPACE and lp(ws=P[6], wsb=need - 1, **a, **t) == WORKSPACE
     assert lp(ws=P[0] + 16, wsb=need, **a, **t) == ALIAS and lp(ws=P[6] + 8, wsb=need, **a, **t) == MISALIGNED
     assert mnb.mnb_logprobs_workspace_bytes(0, 100, 0, 5) == 0 and mnb.mnb_logprobs_workspace_bytes(4, 100, 0, 40) == 0
