@@ -132,7 +132,8 @@ int mnb_mx_describe_route(int M, int N, int K, int fmt, char *buf, size_t buf_le
   const char *name = fmt == MNB_MX_FP4 ? "fp4" : "fp8";
   if (M == 0 || N == 0) snprintf(buf, buf_len, "noop");
   else if (K == 0) snprintf(buf, buf_len, "fill");
-  else if (M <= kMxGemvMaxM) snprintf(buf, buf_len, "mx_gemv_%s ksplit=%d", name, mx_gemv_ksplit(N, K));
+  else if (M <= kMxGemvMaxM) snprintf(buf, buf_len, "mx_gemv_%s operands=%d ksplit=%d", name,
+                                        mx_gemv_operands(fmt, M, N, K), mx_gemv_ksplit(fmt, M, N, K));
   else snprintf(buf, buf_len, "mx_gemm_%s tile=%dx%d", name, mx_gemm_rows(M, N) == 64 ? 64 : 128, mx_gemm_rows(M, N) == 256 ? 256 : 128);
   return MNB_OK;
 }
