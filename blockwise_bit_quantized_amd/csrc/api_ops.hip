@@ -134,7 +134,11 @@ int mnb_mx_describe_route(int M, int N, int K, int fmt, char *buf, size_t buf_le
   else if (K == 0) snprintf(buf, buf_len, "fill");
   else if (M <= kMxGemvMaxM) snprintf(buf, buf_len, "mx_gemv_%s operands=%d ksplit=%d", name,
                                         mx_gemv_operands(fmt, M, N, K), mx_gemv_ksplit(fmt, M, N, K));
-  else snprintf(buf, buf_len, "mx_gemm_%s tile=%dx%d", name, mx_gemm_rows(M, N) == 64 ? 64 : 128, mx_gemm_rows(M, N) == 256 ? 256 : 128);
+  else {
+    const int rows = mx_gemm_rows(fmt, M, N, K);
+    snprintf(buf, buf_len, "mx_gemm_%s tile=%dx%d%s", name, rows == 64 ? 64 : 128, rows == 256 ? 256 : 128,
+             mx_gemm_groups(fmt, M, N, K) == 2 ? " groups=2" : "");
+  }
   return MNB_OK;
 }
 

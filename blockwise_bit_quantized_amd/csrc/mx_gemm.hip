@@ -16,6 +16,13 @@
 //
 // With PRE the X operands of the next step are read into a second register set before the
 // current step's instructions are issued, so a single wave per SIMD does not wait for LDS.
+// With KG = 2 two groups of waves work on halves of K, each with its own ring and panel; the
+// second group's sums join the first's in LDS.
+//
+// Reached: 8192x9728x2560 167 us with FP8 X (2.4 PFLOP/s), 131 with FP4 (3.1); 4096^3 49 us
+// (2.8) and 35 (3.9).  The bare instructions on random data run at 4.25 and 4.5 PFLOP/s: the
+// clock falls to 1.5 - 1.9 GHz under them.  A 128 x 256 step of FP8 takes 2134 cycles for
+// 2048 of its instructions.
 #include "mx_mfma.h"
 
 namespace mnb {
@@ -57,8 +64,8 @@ __device__ __forceinline__ void unroll(F &&f) {
   }
 }
 
-template <int DT, int FMT, int BM, int WM, int WN, int NF, int D, bool PRE>
-__global__ __launch_bounds__(WM * WN * 64, PRE ? 1 : 2) void gemm_kernel(MxMatmulParams p) {
+template <int DT, int FMT, int BM, int WM, int WN, int NF, int D, bool PRE, int KG>
+__global__ __launch_bounds__(KG * WM * WN * 64, KG * (PRE ? 1 : 2)) void gemm_kernel(MxMatmulParams p) {
   constexpr int WAVES = WM * WN, BN = WN * NF * 16, MF = BM / WM / 16;
   constexpr int SUB = FMT == MX_FP4 ? 2 : 1;      // instructions per step, operand pair
   constexpr int SLOTS = D + 1, SLOT = BM * 128;
@@ -73,11 +80,13 @@ __global__ __launch_bounds__(WM * WN * 64, PRE ? 1 : 2) void gemm_kernel(MxMatmu
   // loaded in the second half of the step
   static_assert(PRE || SUB == 1 || (XQ + NF) * GROUPS / OPS >= MF, "second-half weight loads");
   static_assert(XQ >= 1 && 8 * XQ * WAVES == BM, "X rows per wave");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[SLOTS * SLOT + kPanel * BM * 16];
-  uint8_t *sxl = smem + SLOTS * SLOT;
+  constexpr int LDS = SLOTS * SLOT + kPanel * BM * 16;   // of one group of waves
+  __shared__ __attribute__((aligned(1024))) uint8_t smem_all[KG * LDS];
 
-  const int t = threadIdx.x, lane = t & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);   // uniform: addresses stay scalar
+  const int lane = threadIdx.x & 63;
+  const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // uniform: addresses stay scalar
+  const int wave = wave_all % WAVES, kg = wave_all / WAVES, t = wave * 64 + lane;
+  uint8_t *smem = smem_all + kg * LDS, *sxl = smem + SLOTS * SLOT;
   const int r = lane & 15, b = lane >> 4;
   const int wm = wave % WM, wn = wave / WM;
   // workgroup ids are dealt to the 8 XCDs by id modulo 8: each XCD takes a contiguous range of
@@ -150,9 +159,12 @@ __global__ __launch_bounds__(WM * WN * 64, PRE ? 1 : 2) void gemm_kernel(MxMatmu
   };
 
   // K in panels whose X scales fit LDS
-  for (int c0 = 0; c0 < p.KB; c0 += kPanel) {
-    const int chunks = min(kPanel, p.KB - c0);
-    const int s0 = c0 * (4 / SUB), s1 = min(steps, s0 + chunks * (4 / SUB));   // steps of the panel
+  const int share = (p.KB + KG - 1) / KG;   // 512-k chunks of a group; the last group may have fewer, or none
+  for (int panel = 0; panel < share; panel += kPanel) {
+    const int c0 = kg * share + panel, chunks = max(0, min(min(kPanel, share - panel), p.KB - c0));
+    const int s0 = c0 * (4 / SUB), s1 = max(s0, min(steps, s0 + chunks * (4 / SUB)));   // steps of the panel
+    // the groups meet at the same barriers: one with fewer steps only waits through the others'
+    const int s_end = KG == 1 ? s1 : s0 + min(kPanel, share - panel) * (4 / SUB);
     uint32_t sw[NF], sw_next[NF];         // weight scales of this 512-k chunk and the next
     auto load_sw = [&](int kb, int f) { sw_next[f] = sbase[(int64_t)min(kb, p.KB - 1) * 256 + f * 64]; };
 #pragma unroll
@@ -176,10 +188,13 @@ __global__ __launch_bounds__(WM * WN * 64, PRE ? 1 : 2) void gemm_kernel(MxMatmu
     }
     pin();
     const int left = (blocks & 15);
-    if (left && c0 + chunks == p.KB) {    // scale bytes past K may hold anything, a NaN among it
+    // does the last group end in this panel?  (the same answer in every group: there are barriers inside)
+    const int cl = (KG - 1) * share + panel;
+    const bool ends = cl < p.KB && min(min(kPanel, share - panel), p.KB - cl) == p.KB - cl;
+    if (left && ends) {   // scale bytes past K may hold anything, a NaN among it
       wait_vmcnt<0>();
       lds_barrier();
-      for (int id = t; id < BM * 16; id += WAVES * 64)
+      if (kg == KG - 1) for (int id = t; id < BM * 16; id += WAVES * 64)
         if ((id & 15) >= left) sxl[(chunks - 1) * BM * 16 + id] = 0;
       lds_barrier();
     }
@@ -194,23 +209,24 @@ __global__ __launch_bounds__(WM * WN * 64, PRE ? 1 : 2) void gemm_kernel(MxMatmu
 #pragma unroll
         for (int i = 0; i < MF; ++i) read_x(fr[h][i], i, h, smem, ss, h);
     }
-    for (int base = s0; base < s1; base += U) {
+    for (int base = s0; base < s_end; base += U) {
       unroll<0, U>([&](auto uc) {
         constexpr int u = decltype(uc)::value;
         const int step = base + u;
-        if (step >= s1) return;
+        if (step >= s_end) return;
         constexpr bool next_chunk = u * SUB % 4 == 0;
         // PRE: the next step's X; else this step's.  The count is of the loads younger than the
         // ones needed; more of them only wait longer.
         if constexpr (PRE) wait_vmcnt<(D - 2) * (XQ + WQ) + WQ>();
         else wait_vmcnt<0>();
         lds_barrier();
+        if (KG > 1 && step >= s1) return;
         if constexpr (next_chunk) {
 #pragma unroll
           for (int f = 0; f < NF; ++f) sw[f] = sw_next[f];
         }
         // the operands read during this step: the next step's, or AHEAD further on in this one
-        const int rstep = PRE ? min(step + 1, s1 - 1) : step;   // (past the last: read, not used)
+        const int rstep = PRE ? max(s0, min(step + 1, s1 - 1)) : step;   // (past the last: read, not used)
         constexpr int ru = PRE ? u + 1 : u;
         const uint8_t *xs = smem + ru % SLOTS * SLOT, *sp = ss + (rstep - s0) * SUB / 4 * BM * 16;
         if constexpr (!PRE) {
@@ -244,13 +260,32 @@ __global__ __launch_bounds__(WM * WN * 64, PRE ? 1 : 2) void gemm_kernel(MxMatmu
     wait_vmcnt<0>();   // loads past the last step land before their slots are reused
   }
 
+  if constexpr (KG == 2) {   // the second group's sums go through LDS to the first, which stores
+    static_assert(MF * NF * WAVES * 1024 <= LDS, "the sums fit");
+    lds_barrier();           // every wave has read the last step
+    f4_t *sums = reinterpret_cast<f4_t *>(smem_all + LDS) + wave * (MF * NF * 64) + lane;
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+        if (kg) sums[(i * NF + f) * 64] = acc[i][f];
+    lds_barrier();
+    if (!kg) {
+#pragma unroll
+      for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int f = 0; f < NF; ++f) acc[i][f] += sums[(i * NF + f) * 64];
+    }
+  }
+
   // A lane holds NF * 4 consecutive columns of each of its rows.  Through LDS they become whole
   // rows of the tile, 16 bytes a thread: stores straight from the registers put their pieces into
   // 16 lines each and ran at 3.9 TB/s, these at 6.3.  Chunks XOR-swizzled by the row.
   constexpr int CHUNKS = BN / 8;          // 16-byte chunks of an output row
-  static_assert(BM * BN * 2 <= (int)sizeof(smem), "the output tile fits");
+  static_assert(BM * BN * 2 <= LDS, "the output tile fits");
   const int nt = wn * NF * 16 - 16 * f0 + 16 * b + 4 * f0;   // this lane's first column within the tile
   if (p.N & 7) {                          // rows of other alignment
+    if (kg) return;
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
       const int64_t m = m0 + row0 + 16 * i;
@@ -264,6 +299,7 @@ __global__ __launch_bounds__(WM * WN * 64, PRE ? 1 : 2) void gemm_kernel(MxMatmu
     return;
   }
   lds_barrier();                          // every wave has read the last step
+  if (!kg) {
 #pragma unroll
   for (int e = 0; e < NF / 2; ++e) {      // two operands: 8 columns
     float bias[8] = {};
@@ -277,39 +313,58 @@ __global__ __launch_bounds__(WM * WN * 64, PRE ? 1 : 2) void gemm_kernel(MxMatmu
       store8<DT>(reinterpret_cast<uint16_t *>(smem + row * (BN * 2) + (((nt / 8 + e) ^ (row & (CHUNKS - 1))) << 4)), v);
     }
   }
+  }
   lds_barrier();
 #pragma unroll
-  for (int j = 0; j < BM * CHUNKS / (WAVES * 64); ++j) {
-    const int id = j * (WAVES * 64) + t, row = id / CHUNKS, c = id % CHUNKS;
+  for (int j = 0; j < BM * CHUNKS / (KG * WAVES * 64); ++j) {
+    const int id = (j * KG + kg) * (WAVES * 64) + t, row = id / CHUNKS, c = id % CHUNKS;
     if (row > last_row || n0 + 8 * c >= p.N) continue;
     *reinterpret_cast<u4_t *>(p.y + (m0 + row) * p.N + n0 + 8 * c) =
-        *reinterpret_cast<const u4_t *>(smem + row * (BN * 2) + ((c ^ (row & (CHUNKS - 1))) << 4));
+        *reinterpret_cast<const u4_t *>(smem_all + row * (BN * 2) + ((c ^ (row & (CHUNKS - 1))) << 4));
   }
 }
 
-template <int DT, int FMT, int BM, int WM, int WN, int NF, int D, bool PRE>
+template <int DT, int FMT, int BM, int WM, int WN, int NF, int D, bool PRE, int KG>
 hipError_t launch_tile(const MxMatmulParams &p, hipStream_t s) {
   const int64_t tiles = ((int64_t)p.M + BM - 1) / BM * (((int64_t)p.N + WN * NF * 16 - 1) / (WN * NF * 16));
-  hipLaunchKernelGGL((gemm_kernel<DT, FMT, BM, WM, WN, NF, D, PRE>), dim3((uint32_t)((tiles + 7) / 8 * 8)), dim3(WM * WN * 64),
+  hipLaunchKernelGGL((gemm_kernel<DT, FMT, BM, WM, WN, NF, D, PRE, KG>), dim3((uint32_t)((tiles + 7) / 8 * 8)), dim3(KG * WM * WN * 64),
                      0, s, p);
   return hipGetLastError();
 }
 
 template <int DT, int FMT>
 hipError_t launch(const MxMatmulParams &p, hipStream_t s) {
-  const int rows = mx_gemm_rows(p.M, p.N);
-  if (rows == 256) return launch_tile<DT, FMT, 128, 1, 4, 4, 1, false>(p, s);
-  if (rows == 128) return launch_tile<DT, FMT, 128, 1, 4, 2, 3, true>(p, s);
-  return launch_tile<DT, FMT, 64, 1, 4, 2, 3, true>(p, s);
+  const int rows = mx_gemm_rows(FMT, p.M, p.N, p.K);
+  if (rows == 256) return launch_tile<DT, FMT, 128, 1, 4, 4, 1, false, 1>(p, s);
+  if (rows == 128) return launch_tile<DT, FMT, 128, 1, 4, 2, 3, true, 1>(p, s);
+  if (mx_gemm_groups(FMT, p.M, p.N, p.K) == 2) return launch_tile<DT, FMT, 64, 1, 4, 2, 3, true, 2>(p, s);
+  return launch_tile<DT, FMT, 64, 1, 4, 2, 3, true, 1>(p, s);
 }
+
+bool long_k(int fmt, int K) { return (fmt == MX_FP4 ? K / 2 : K) >= 16 * 128; }   // 16 steps or more
 
 }  // namespace
 
-int mx_gemm_rows(int M, int N) {
-  const int64_t big = ((int64_t)M + 255) / 256 * (((int64_t)N + 255) / 256);
-  if (big >= kCUs) return 256;
-  const int64_t mid = ((int64_t)M + 127) / 128 * (((int64_t)N + 127) / 128);
-  return mid >= kCUs / 2 ? 128 : 64;
+// The tile with the least time for a whole grid: the rounds that 256 CUs need, times a tile's
+// time per step (FP8, 4096 k: 64 x 128 0.34 us alone on a CU, 128 x 128 0.56, 128 x 256 0.93,
+// two of them together 1.55; 64 x 128 without the second group of waves shares a CU and takes
+// less).  Measured with 64 x 128 / 128 x 128 / 128 x 256, us: 512x4096x4096 FP8 13.7 / 19.2 /
+// 28.2, 1024x4096x4096 23.7 / 20.2 / 28.8 and FP4 20.4 / 16.0 / 20.4, 2048x4096x4096 43 / 37 /
+// 31, 4096^3 83 / 71 / 49, 1500x2560x2560 18.5 / 14.5 / 20.3, 300x16384x1024 11.1 / 15.4 / 12.2.
+int mx_gemm_rows(int fmt, int M, int N, int K) {
+  const auto rounds = [&](int bm, int bn) { return (((int64_t)M + bm - 1) / bm * (((int64_t)N + bn - 1) / bn) + kCUs - 1) / kCUs; };
+  const int64_t r64 = rounds(64, 128), r128 = rounds(128, 128), r256 = rounds(128, 256);
+  const int64_t c64 = r64 * (long_k(fmt, K) ? 5 : 4), c128 = r128 * 9, c256 = r256 * (r256 > 1 ? 12 : 14);
+  return c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
+}
+
+// A CU draws about 60 GB/s however far ahead its loads run (7 steps ahead instead of 3: no
+// change), so a grid of few tiles is bound by its number of CUs.  A second group of waves with
+// the other half of K keeps more of them in flight: 64x2560x9728 FP8 28.5 -> 22.3 us,
+// 200x2560x4096 FP8 14.3 -> 12.2, FP4 9.9 -> 9.6; under 16 steps the join costs more than it
+// gives (64x8192x2048 FP4 6.1 -> 7.0).
+int mx_gemm_groups(int fmt, int M, int N, int K) {
+  return mx_gemm_rows(fmt, M, N, K) == 64 && long_k(fmt, K) ? 2 : 1;
 }
 
 hipError_t launch_mx_gemm(int dtype, int fmt, const MxMatmulParams &p, hipStream_t s) {

@@ -157,12 +157,13 @@ int mx_gemv_operands(int fmt, int M, int N, int K) {
   return rb;
 }
 
-// the smallest split that gives 8 waves per CU, but not more waves than 512-k parts
+// The smallest split that gives 8 waves per CU, as long as it shortens the longest wave's K:
+// three 512-k parts over four waves (16x1000x1056) take 3.1 us, over two 3.5.
 int mx_gemv_ksplit(int fmt, int M, int N, int K) {
   const int64_t units = ((int64_t)N + 63) / 64 * 4 / mx_gemv_operands(fmt, M, N, K);
   const int parts = (K + kMxScaleK - 1) / kMxScaleK;
   int s = 1;
-  while (s < kWaves && units * s < 8 * kCUs && 2 * s <= parts) s *= 2;
+  while (s < kWaves && units * s < 8 * kCUs && s < parts) s *= 2;
   return s;
 }
 

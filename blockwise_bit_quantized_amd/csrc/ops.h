@@ -164,7 +164,8 @@ hipError_t launch_mx_gemv(int dtype, int fmt, const MxMatmulParams &p, hipStream
 hipError_t launch_mx_gemm(int dtype, int fmt, const MxMatmulParams &p, hipStream_t s);
 int mx_gemv_operands(int fmt, int M, int N, int K);  // operands of 16 weight rows a wave: 1, 2 or 4
 int mx_gemv_ksplit(int fmt, int M, int N, int K);    // waves that share a weight row's K: 1, 2 or 4
-int mx_gemm_rows(int M, int N);                      // 256 (two 128 x 256 tiles a CU), 128 or 64
+int mx_gemm_groups(int fmt, int M, int N, int K);    // groups of waves that share a tile's K: 1 or 2
+int mx_gemm_rows(int fmt, int M, int N, int K);      // 256 (two 128 x 256 tiles a CU), 128 or 64
 
 struct NormParams {
   const uint16_t *x, *res, *w;
