@@ -17,6 +17,10 @@
 //   * if the larger ones alone are too many (one group holds most large values), or the row holds
 //     a NaN or +infinity, the keys are taken one at a time, each the largest below the last.
 //
+// Bound by memory and vector instructions together for many rows (1024 x 49152 fp16, top 20:
+// 101 MB in 27 us, 3.7 TB/s, while the instructions take 40 to 60% of the SIMDs' cycles), by
+// the chain of reductions for one row (49152: 7.0 us).
+//
 // Rows longer than one workgroup holds, and calls with few rows, split each row; the parts'
 // (m, S, T) and keys go through the workspace and a second kernel joins them in part order.
 #include "ops.h"

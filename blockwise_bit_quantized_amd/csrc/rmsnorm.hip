@@ -8,7 +8,8 @@
 // 7000, and the only ones whose code or block scale can differ).  All in 64 bits measured 52.7 us
 // at 8192 x 4096 (bfloat16, residual, FP8) against 48.2.
 //
-// Bound by memory: each input is read once and each output written once.  The aligned
+// Bound by memory (8192 x 4096: 236 MB in 45 us, 5.3 TB/s; 1 x 2048 2.9 us and 333 x 896 3.1,
+// latencies): each input is read once and each output written once.  The aligned
 // kernel keeps a row's h in registers between the sum of squares and the outputs (CH pieces
 // of 8 elements a thread); rows longer than that read the inputs a second time for the
 // pieces past it (from L2).  Rows of other alignment take the element-wise kernel.
