@@ -19,8 +19,8 @@
 // With KG = 2 two groups of waves work on halves of K, each with its own ring and panel; the
 // second group's sums join the first's in LDS.
 //
-// Reached: 8192x9728x2560 167 us with FP8 X (2.4 PFLOP/s), 131 with FP4 (3.1); 4096^3 49 us
-// (2.8) and 35 (3.9).  The bare instructions on random data run at 4.25 and 4.5 PFLOP/s: the
+// Reached: 8192x9728x2560 150 us with FP8 X (2.7 PFLOP/s), 107 with FP4 (3.8); 4096^3 49 us
+// (2.8) and 36 (3.8).  The bare instructions on random data run at 4.25 and 4.5 PFLOP/s: the
 // clock falls to 1.5 - 1.9 GHz under them.  A 128 x 256 step of FP8 takes 2134 cycles for
 // 2048 of its instructions.
 #include "mx_mfma.h"
