@@ -169,7 +169,7 @@ def test_matmul_exact_sums(M, N, K, fmt):
 
 @pytest.mark.parametrize("fmt", [FP4, FP8])
 @pytest.mark.parametrize("M,N,K", [(4097, 4100, 416), (2100, 9000, 1120), (4352, 4096, 8864), (1000, 2100, 8864), (40, 300, 17056),
-                                   (64, 260, 16800), (900, 4000, 4448), (1020, 4090, 2080), (100, 131, 2080), (333, 1000, 1568), (65, 2560, 9728),
+                                   (64, 260, 16800), (900, 4000, 4448), (900, 4032, 4448), (1020, 4090, 2080), (100, 131, 2080), (333, 1000, 1568), (65, 2560, 9728),
                                    (32, 8190, 2048), (32, 49100, 576), (21, 41000, 2112), (30, 65600, 576), (17, 131100, 1056), (24, 12300, 4128)])
 def test_matmul_exact_sums_large(M, N, K, fmt):
     """Tiles of every height, K past one panel of scales and ending inside a step; the reference is
