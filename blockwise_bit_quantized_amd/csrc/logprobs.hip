@@ -32,14 +32,16 @@ constexpr int kCap = 512;       // collected candidates
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // order-preserving bits: larger number, larger integer; every NaN above +infinity, both
-// zeros alike, nothing maps to 0 (the key of an absent element)
+// zeros alike.  Nothing maps to 0 (the key of an absent element), and a NaN is not the largest
+// integer: at index 0 its key would be all ones, which no search for a key below a limit finds.
+constexpr uint32_t kNanBits = 0xfffffffeu;
 __device__ __forceinline__ uint32_t order_bits(float f) {
   const uint32_t b = __builtin_bit_cast(uint32_t, f + 0.0f);   // -0 becomes +0
   const uint32_t u = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-  return f != f ? 0xffffffffu : u;
+  return f != f ? kNanBits : u;
 }
 __device__ __forceinline__ float order_value(uint32_t u) {
-  return __builtin_bit_cast(float, u & 0x80000000u ? u ^ 0x80000000u : ~u);   // 0xffffffff: a NaN
+  return __builtin_bit_cast(float, u & 0x80000000u ? u ^ 0x80000000u : ~u);   // kNanBits: a NaN
 }
 __device__ __forceinline__ uint64_t make_key(uint32_t u, uint32_t index) { return (uint64_t)u << 32 | (uint32_t)~index; }
 
