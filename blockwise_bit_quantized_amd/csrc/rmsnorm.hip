@@ -1,11 +1,12 @@
 // rmsnorm.hip -- y = h / sqrt(mean(h^2) + eps) * w, h = x + residual, with the new residual
 // stream h and y in 16 bits or MX as outputs, each rounded once from 32 bits.
 //
-// The sum of squares and the root are in 64 bits: bfloat16 rows may have squares past the
-// range of 32.  The products are in 32 bits, within 4 units of the last place of the exact y; an
-// MX output is nevertheless that of the exact y, as values so near a border of the
-// element grid that 4 units could cross it are computed again in 64 bits (one element in
-// 7000, and the only ones whose code or block scale can differ).  All in 64 bits measured 52.7 us
+// The sum of squares and the root are in 64 bits, of h before any rounding (32 bits may lose the
+// smaller of x and residual, and bfloat16 rows may have squares past their range).  The
+// products are in 32 bits, within 4 units of the last place of the exact y; an MX output is
+// nevertheless that of the exact y, as values so near a border of the element grid that 4
+// units could cross it are computed again in 64 bits from x and residual (one element in 7000, and
+// the only ones whose code or block scale can differ).  All in 64 bits measured 52.7 us
 // at 8192 x 4096 (bfloat16, residual, FP8) against 48.2.
 //
 // Bound by memory (8192 x 4096: 236 MB in 45 us, 5.3 TB/s; 1 x 2048 2.9 us and 333 x 896 3.1,
@@ -48,16 +49,19 @@ __device__ __forceinline__ float to_odd(double v) {
   return (float)__builtin_bit_cast(double, b);
 }
 
+// a piece of 8 elements of x and of the residual (-0 without one, which leaves x as it is)
 template <int DT>
-__device__ __forceinline__ void load_h(const NormParams &p, const uint16_t *x, const uint16_t *res, int64_t c, float *h) {
-  load8<DT>(x + 8 * c, h);
-  if (res) {
-    float r[8];
-    load8<DT>(res + 8 * c, r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] += r[i];
+struct Inputs {
+  u4_t x = {0, 0, 0, 0}, r = {0, 0, 0, 0};
+  __device__ __forceinline__ void load(const uint16_t *px, const uint16_t *pr, int64_t c) {
+    constexpr uint32_t zeros = 0x80008000u;
+    x = *reinterpret_cast<const u4_t *>(px + 8 * c);
+    r = pr ? *reinterpret_cast<const u4_t *>(pr + 8 * c) : u4_t{zeros, zeros, zeros, zeros};
   }
-}
+  __device__ __forceinline__ static float at(const u4_t &v, int i) { return to_f32<DT>((uint16_t)(v[i >> 1] >> (16 * (i & 1)))); }
+  __device__ __forceinline__ float h(int i) const { return at(x, i) + at(r, i); }
+  __device__ __forceinline__ double h64(int i) const { return (double)at(x, i) + (double)at(r, i); }
+};
 
 // K % 8 == 0, every row 16-byte aligned; with codes K % 32 == 0.  The piece loops run to a
 // multiple of THREADS so that the four lanes of a block meet in the exchanges.
@@ -67,52 +71,58 @@ __global__ __launch_bounds__(WAVES * 64) void norm_kernel(NormParams p) {
   const int64_t row = blockIdx.x;
   const int t = threadIdx.x, pieces = p.K / 8;
   const uint16_t *x = p.x + row * p.ldx, *res = p.res ? p.res + row * p.ldr : nullptr;
+  Inputs<DT> in[CH];
   float h[CH][8];
   double ss = 0.0;
 #pragma unroll
   for (int j = 0; j < CH; ++j) {
     const int c = j * THREADS + t;
-    if (c < pieces) {
-      load_h<DT>(p, x, res, c, h[j]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fma((double)h[j][i], (double)h[j][i], ss);
-    }
+    if (c < pieces) in[j].load(x, res, c);
   }
-  for (int c = CH * THREADS + t; c < pieces; c += THREADS) {
-    float v[8];
-    load_h<DT>(p, x, res, c, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fma((double)v[i], (double)v[i], ss);
+  for (int j = 0; j < CH; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double d = in[j].h64(i);
+      ss = fma(d, d, ss);
+      h[j][i] = in[j].h(i);
+    }
+  for (int c = CH * THREADS + t; c < pieces; c += THREADS) {
+    Inputs<DT> more;
+    more.load(x, res, c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fma(more.h64(i), more.h64(i), ss);
   }
   ss = block_sum<WAVES>(ss);
   const double rstd = 1.0 / sqrt(ss / p.K + (double)p.eps);
   const float r32 = (float)rstd;
 
-  auto finish = [&](int c, float *v) {
+  auto finish = [&](int c, const float *h8) {
+    float w[8], v[8];
+    load8<DT>(p.w + 8 * (int64_t)c, w);
+    uint32_t border = ~0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = h8[i] * r32 * w[i];
+      // every border (ties, powers of two) has at least 16 zero bits at its end
+      if constexpr (FMT >= 0) border = min(border, (__builtin_bit_cast(uint32_t, v[i]) + 4u) << 16);
+    }
+    if constexpr (FMT >= 0) {
+      if (border <= 8u << 16) {   // before hidden is stored, which may be in the place of x or residual
+        Inputs<DT> again;
+        again.load(x, res, c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_odd(again.h64(i) * rstd * (double)w[i]);
+      }
+    }
     if (p.hidden) {
       uint16_t *to = p.hidden + row * p.ldh + 8 * (int64_t)c;
       // with MX outputs the next call reads those and not the hidden rows: past the caches
       // 8192 x 4096 takes 45.7 us, not 48.2 (with 16-bit outputs 57.8, not 55.1, so not there)
       if constexpr (FMT >= 0)
-        __builtin_nontemporal_store(u4_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])},
+        __builtin_nontemporal_store(u4_t{pack2<DT>(h8[0], h8[1]), pack2<DT>(h8[2], h8[3]), pack2<DT>(h8[4], h8[5]), pack2<DT>(h8[6], h8[7])},
                                     reinterpret_cast<u4_t *>(to));
-      else store8<DT>(to, v);
-    }
-    float w[8], h8[8];
-    load8<DT>(p.w + 8 * (int64_t)c, w);
-    uint32_t border = ~0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      h8[i] = v[i];
-      v[i] = v[i] * r32 * w[i];
-      // every border (ties, powers of two) has at least 16 zero bits at its end
-      if constexpr (FMT >= 0) border = min(border, (__builtin_bit_cast(uint32_t, v[i]) + 4u) << 16);
-    }
-    if constexpr (FMT >= 0) {
-      if (border <= 8u << 16) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_odd((double)h8[i] * rstd * (double)w[i]);
-      }
+      else store8<DT>(to, h8);
     }
     if (p.y) store8<DT>(p.y + row * p.ldy + 8 * (int64_t)c, v);
     if constexpr (FMT >= 0) {
@@ -138,8 +148,11 @@ __global__ __launch_bounds__(WAVES * 64) void norm_kernel(NormParams p) {
     if (c < pieces) finish(c, h[j]);
   }
   for (int c = CH * THREADS + t; c < pieces; c += THREADS) {
+    Inputs<DT> more;
+    more.load(x, res, c);
     float v[8];
-    load_h<DT>(p, x, res, c, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = more.h(i);
     finish(c, v);
   }
 }
@@ -151,8 +164,8 @@ __global__ __launch_bounds__(256) void norm_any_kernel(NormParams p) {
   const uint16_t *x = p.x + row * p.ldx, *res = p.res ? p.res + row * p.ldr : nullptr;
   double ss = 0.0;
   for (int k = threadIdx.x; k < p.K; k += 256) {
-    const float h = to_f32<DT>(x[k]) + (res ? to_f32<DT>(res[k]) : 0.f);
-    ss = fma((double)h, (double)h, ss);
+    const double h = (double)to_f32<DT>(x[k]) + (res ? (double)to_f32<DT>(res[k]) : 0.0);
+    ss = fma(h, h, ss);
   }
   ss = block_sum<4>(ss);
   const float r32 = (float)(1.0 / sqrt(ss / p.K + (double)p.eps));

@@ -1,0 +1,116 @@
+"""The norm's MX codes against those of the norm in 64 bits, bit for bit, on rows whose outputs lie at
+the borders of the element grid (ties, powers of two), where 32 bits alone take the wrong side.
+
+Rows that lie at borders by construction have a mean square of exactly 1 (eps 0), so that y = h w: the
+fillers below complete the sum of squares with powers of two.  32 bits lose the residuals that put them
+to one side of it."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import _ops_ref as ref
+from _util import ensure_lib
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+mnb = ensure_lib()
+DEV = torch.device("cuda:0")
+FP4, FP8 = mnb.MNB_MX_FP4, mnb.MNB_MX_FP8
+DT = {"fp16": torch.float16, "bf16": torch.bfloat16}
+# numbers below 2, whose block has its largest magnitude in [1, 2): elements are x / 2^-2 (FP4) or
+# x / 2^-8 (FP8).  Ties that go up and ties that go down.
+TIES = {FP4: [0.625, 1.25, 0.875, 0.4375, 0.1875], FP8: [1.0625, 1.3125, 1.1875, 1.4375, 0.59375]}
+TOP = 1.5
+
+
+def rng(*seed):
+    return np.random.default_rng([20261207, *seed])
+
+
+def dev(a, dt):
+    return torch.from_numpy(np.asarray(a, np.float64)).to(dt).to(DEV)
+
+
+def same_codes(q, want, fmt, where=""):
+    v, s = ref.quantize(want, fmt)
+    assert np.array_equal(q.scales.cpu().numpy(), s), where
+    got, codes = q.codes.cpu().numpy(), ref.element_codes(v, fmt)
+    assert np.array_equal(got, codes), (where, int((got != codes).sum()))
+
+
+def block_of(ties, top):
+    """32 numbers whose squares sum to 32 exactly: the ties, the largest, powers of two (but 2^-4, FP4's tie)."""
+    b = [*ties, top]
+    for v in [top, *(2.0 ** -e for e in range(12) if e != 4)]:
+        while v * v <= 32 - np.square(b).sum():
+            b.append(v)
+    assert np.square(b).sum() == 32 and len(b) <= 32
+    return np.array(b + [0.0] * (32 - len(b)))
+
+
+def unit_row(fmt, K, r):
+    """A row of mean square 1 with ties in every block: (numbers, mask of the ties)."""
+    x = np.concatenate([block_of(TIES[fmt], TOP) for _ in range(K // 32)])
+    tie = np.isin(x, TIES[fmt])
+    for b in range(K // 32):
+        at = r.permutation(32) + 32 * b
+        x[32 * b:32 * b + 32], tie[32 * b:32 * b + 32] = x[at], tie[at]
+    return x * r.choice([-1.0, 1.0], K), tie
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("fmt", [FP4, FP8])
+def test_random_rows_have_the_codes_of_the_64_bit_norm(dtype, fmt):
+    for M, K in ((2000, 1024), (300, 4096), (40, 8192), (20, 36000), (1, 65536)):
+        r = rng(1, fmt, M, K)
+        x, res = dev(r.standard_normal((M, K)), DT[dtype]), dev(r.standard_normal((M, K)), DT[dtype])
+        w = dev(1 + 0.2 * r.standard_normal(K), DT[dtype])
+        X, R, W = (t.double().cpu().numpy() for t in (x, res, w))
+        h = X + R
+        want = h / np.sqrt((h * h).mean(-1, keepdims=True) + 1e-6) * W
+        n = mnb.rmsnorm(x, w, 1e-6, residual=res, fmt=fmt)
+        same_codes(n.q, want, fmt, (M, K))
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("fmt", [FP4, FP8])
+@pytest.mark.parametrize("K", [64, 2048, 4096, 8192, 40000])
+def test_sums_past_32_bits_at_ties(dtype, fmt, K):
+    """x at a tie, a residual too small for the 32-bit sum: y lies beside the tie by the residual's sign.
+    The residuals' signs cancel in the sum of squares to second order (2^-48)."""
+    r = rng(2, fmt, K)
+    x, tie = unit_row(fmt, K, r)
+    res = np.where(tie, 2.0 ** -24 * 2.0 ** np.floor(np.log2(np.abs(x) + (x == 0))), 0.0)
+    if dtype == "fp16":
+        res = np.where(tie, 2.0 ** -24, 0.0)                         # its smallest number
+    sign = np.ones(K)
+    for v in np.unique(np.abs(x[tie])):                              # half of each tie's up, half down
+        at = np.flatnonzero(tie & (np.abs(x) == v))
+        sign[at] = np.where(np.arange(len(at)) % 2 == 0, 1.0, -1.0) * np.sign(x[at])
+    h = x + res * sign
+    assert abs((h * h).mean() - 1) < 2.0 ** -44
+    X, R = dev(np.stack([x, x]), DT[dtype]), dev(np.stack([res * sign, -res * sign]), DT[dtype])
+    hh = np.stack([h, x - res * sign])
+    n = mnb.rmsnorm(X, torch.ones(K, dtype=DT[dtype], device=DEV), 0.0, residual=R, fmt=fmt)
+    same_codes(n.q, hh / np.sqrt((hh * hh).mean(-1, keepdims=True)), fmt)
+    held = R.clone()                                                 # in place: the inputs are overwritten
+    m = mnb.rmsnorm(X, torch.ones(K, dtype=DT[dtype], device=DEV), 0.0, residual=held, hidden=held, fmt=fmt)
+    assert torch.equal(m.q.codes, n.q.codes) and torch.equal(m.q.scales, n.q.scales) and torch.equal(held, n.hidden)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("fmt", [FP4, FP8])
+@pytest.mark.parametrize("K", [64, 2048, 40000])
+def test_the_norm_is_that_of_the_unrounded_sum(dtype, fmt, K):
+    """The largest numbers carry a residual that a 32-bit sum loses, so the norm lies 2^-24 or so beside 1 and
+    every tie to its side."""
+    r = rng(3, fmt, K)
+    x, tie = unit_row(fmt, K, r)
+    big = np.abs(x) == TOP
+    res = np.where(big, np.sign(x) * 2.0 ** -24, 0.0)
+    h = np.stack([x + res, x - res])
+    X, R = dev(np.stack([x, x]), DT[dtype]), dev(np.stack([res, -res]), DT[dtype])
+    n = mnb.rmsnorm(X, torch.ones(K, dtype=DT[dtype], device=DEV), 0.0, residual=R, fmt=fmt)
+    same_codes(n.q, h / np.sqrt((h * h).mean(-1, keepdims=True)), fmt)
