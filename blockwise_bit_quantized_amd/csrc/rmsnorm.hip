@@ -6,7 +6,8 @@
 // products are in 32 bits, within 4 units of the last place of the exact y; an MX output is
 // nevertheless that of the exact y, as values so near a border of the element grid that 4
 // units could cross it are computed again in 64 bits from x and residual (one element in 7000, and
-// the only ones whose code or block scale can differ).  All in 64 bits measured 52.7 us
+// the only ones whose code or block scale can differ).  So are rows whose norm 32 bits do not hold,
+// whatever their outputs.  All in 64 bits measured 52.7 us
 // at 8192 x 4096 (bfloat16, residual, FP8) against 48.2.
 //
 // Bound by memory (8192 x 4096: 236 MB in 45 us, 5.3 TB/s; 1 x 2048 2.9 us and 333 x 896 3.1,
@@ -63,6 +64,10 @@ struct Inputs {
   __device__ __forceinline__ double h64(int i) const { return (double)at(x, i) + (double)at(r, i); }
 };
 
+// Is the root's inverse so far from 1 that 32 bits do not hold it, or h, in full?  (bfloat16 rows of subnormals with a
+// small eps, or near the largest number; a NaN too.)
+__device__ __forceinline__ bool far_norm(double rstd) { return !(rstd >= 0x1p-100 && rstd <= 0x1p100); }
+
 // K % 8 == 0, every row 16-byte aligned; with codes K % 32 == 0.  The piece loops run to a
 // multiple of THREADS so that the four lanes of a block meet in the exchanges.
 template <int DT, int FMT, int WAVES, int CH>
@@ -96,6 +101,7 @@ __global__ __launch_bounds__(WAVES * 64) void norm_kernel(NormParams p) {
   ss = block_sum<WAVES>(ss);
   const double rstd = 1.0 / sqrt(ss / p.K + (double)p.eps);
   const float r32 = (float)rstd;
+  const bool far = far_norm(rstd);
 
   auto finish = [&](int c, const float *h8) {
     float w[8], v[8];
@@ -107,13 +113,11 @@ __global__ __launch_bounds__(WAVES * 64) void norm_kernel(NormParams p) {
       // every border (ties, powers of two) has at least 16 zero bits at its end
       if constexpr (FMT >= 0) border = min(border, (__builtin_bit_cast(uint32_t, v[i]) + 4u) << 16);
     }
-    if constexpr (FMT >= 0) {
-      if (border <= 8u << 16) {   // before hidden is stored, which may be in the place of x or residual
-        Inputs<DT> again;
-        again.load(x, res, c);
+    if (far || (FMT >= 0 && border <= 8u << 16)) {   // before hidden is stored, which may be in the place of x or residual
+      Inputs<DT> again;
+      again.load(x, res, c);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_odd(again.h64(i) * rstd * (double)w[i]);
-      }
+      for (int i = 0; i < 8; ++i) v[i] = to_odd(again.h64(i) * rstd * (double)w[i]);
     }
     if (p.hidden) {
       uint16_t *to = p.hidden + row * p.ldh + 8 * (int64_t)c;
@@ -168,11 +172,13 @@ __global__ __launch_bounds__(256) void norm_any_kernel(NormParams p) {
     ss = fma(h, h, ss);
   }
   ss = block_sum<4>(ss);
-  const float r32 = (float)(1.0 / sqrt(ss / p.K + (double)p.eps));
+  const double rstd = 1.0 / sqrt(ss / p.K + (double)p.eps);
+  const float r32 = (float)rstd;
+  const bool far = far_norm(rstd);
   for (int k = threadIdx.x; k < p.K; k += 256) {
-    const float h = to_f32<DT>(x[k]) + (res ? to_f32<DT>(res[k]) : 0.f);
+    const float a = to_f32<DT>(x[k]), b = res ? to_f32<DT>(res[k]) : 0.f, h = a + b, w = to_f32<DT>(p.w[k]);
     if (p.hidden) p.hidden[row * p.ldh + k] = from_f32<DT>(h);
-    p.y[row * p.ldy + k] = from_f32<DT>(h * r32 * to_f32<DT>(p.w[k]));
+    p.y[row * p.ldy + k] = from_f32<DT>(far ? to_odd(((double)a + (double)b) * rstd * (double)w) : h * r32 * w);
   }
 }
 

@@ -114,3 +114,43 @@ def test_the_norm_is_that_of_the_unrounded_sum(dtype, fmt, K):
     X, R = dev(np.stack([x, x]), DT[dtype]), dev(np.stack([res, -res]), DT[dtype])
     n = mnb.rmsnorm(X, torch.ones(K, dtype=DT[dtype], device=DEV), 0.0, residual=R, fmt=fmt)
     same_codes(n.q, h / np.sqrt((h * h).mean(-1, keepdims=True)), fmt)
+
+
+def within_half_a_step(got, want, dt, K):
+    """One rounding of `dt` beside the 32-bit steps (the sum of squares and the root are in 64 bits): 2^-21."""
+    top, least = torch.finfo(dt).max, torch.finfo(dt).smallest_normal * torch.finfo(dt).eps
+    g = got.double().cpu().numpy()
+    over = np.abs(want) >= top * (1 + torch.finfo(dt).eps / 4)
+    assert (np.abs(g[over]) == np.inf).all() and (np.sign(g[over]) == np.sign(want[over])).all()
+    err = np.abs(g[~over] - want[~over])
+    assert (err <= np.abs(want[~over]) * (torch.finfo(dt).eps / 2 + 2.0 ** -21) + least / 2).all(), err.max()
+
+
+@pytest.mark.parametrize("K", [64, 577, 2048, 4096, 8192, 9000, 40000])
+def test_rows_whose_norm_is_near_the_ends_of_32_bits(K):
+    """bfloat16 rows of subnormals with eps 0 (the root's inverse is past 32 bits), rows near the largest number (it
+    is subnormal), and sums past the largest 32-bit number: y is of order 1 in all of them."""
+    r = rng(4, K)
+    dt = torch.bfloat16
+    x = np.stack([r.integers(1, 9, K) * 2.0 ** -133 * r.choice([-1.0, 1.0], K),
+                  r.uniform(0.5, 1, K) * 3.3e38 * r.choice([-1.0, 1.0], K),
+                  r.uniform(0.5, 1, K) * 2e38,
+                  r.standard_normal(K) * 1e-36,
+                  r.standard_normal(K) * 2.0 ** 100,
+                  r.standard_normal(K)])
+    res = np.stack([r.integers(1, 9, K) * 2.0 ** -133, np.zeros(K), r.uniform(0.5, 1, K) * 2.5e38, np.zeros(K),
+                    r.standard_normal(K) * 2.0 ** 100, r.standard_normal(K)])
+    X, R, W = dev(x, dt), dev(res, dt), dev(1 + 0.2 * r.standard_normal(K), dt)
+    x, res, w = (t.double().cpu().numpy() for t in (X, R, W))
+    for residual in (None, R):
+        h = x if residual is None else x + res
+        want = h / np.sqrt((h * h).mean(-1, keepdims=True)) * w
+        n = mnb.rmsnorm(X, W, 0.0, residual=residual)
+        within_half_a_step(n.y, want, dt, K)
+        if residual is not None:
+            within_half_a_step(n.hidden, h, dt, K)
+        if K % 32 == 0:
+            for fmt in (FP4, FP8):
+                n = mnb.rmsnorm(X, W, 0.0, residual=residual, fmt=fmt, keep16=True)
+                within_half_a_step(n.y, want, dt, K)
+                same_codes(n.q, want, fmt, K)
