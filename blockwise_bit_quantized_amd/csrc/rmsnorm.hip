@@ -7,7 +7,8 @@
 // nevertheless that of the exact y, as values so near a border of the element grid that 4
 // units could cross it are computed again in 64 bits from x and residual (one element in 7000, and
 // the only ones whose code or block scale can differ).  So are rows whose norm 32 bits do not hold,
-// whatever their outputs.  All in 64 bits measured 52.7 us
+// whatever their outputs, and blocks below 2^-100.  (Two limits of 32 bits stay: a y past their range counts as
+// infinite, and an element 2^126 times smaller than its row's norm keeps their absolute precision.)  All in 64 bits measured 52.7 us
 // at 8192 x 4096 (bfloat16, residual, FP8) against 48.2.
 //
 // Bound by memory (8192 x 4096: 236 MB in 45 us, 5.3 TB/s; 1 x 2048 2.9 us and 333 x 896 3.1,
@@ -41,13 +42,15 @@ __device__ __forceinline__ double block_sum(double v) {
   return v;
 }
 
-// To 32 bits, inexact values to the neighbour with an odd last bit: a later rounding to fewer
-// bits then gives what one rounding of v would (rounding to nearest first would turn values
-// next to an element's border into ties).
+// To 32 bits, inexact values to the neighbour with an odd last bit, among subnormals too: a later
+// rounding to fewer bits then gives what one rounding of v would (rounding to nearest first
+// would turn values next to an element's border into ties).
 __device__ __forceinline__ float to_odd(double v) {
-  uint2 b = __builtin_bit_cast(uint2, v);          // 29 of the 52 fraction bits go, all in the low word
-  b.x = (b.x & 0xe0000000u) | ((b.x & 0x1fffffffu) ? 0x20000000u : 0u);
-  return (float)__builtin_bit_cast(double, b);
+  const float f = (float)v;
+  const double g = f;
+  const uint32_t b = __builtin_bit_cast(uint32_t, f);
+  if (g == v || __builtin_isinf(f)) return f;
+  return __builtin_bit_cast(float, (fabs(g) > fabs(v) ? b - 1 : b) | 1u);
 }
 
 // a piece of 8 elements of x and of the residual (-0 without one, which leaves x as it is)
@@ -70,8 +73,9 @@ __device__ __forceinline__ bool far_norm(double rstd) { return !(rstd >= 0x1p-10
 
 // K % 8 == 0, every row 16-byte aligned; with codes K % 32 == 0.  The piece loops run to a
 // multiple of THREADS so that the four lanes of a block meet in the exchanges.
+// 8 waves a SIMD, so that two rows of 16 waves share a CU (500 x 16384, FP8: 16.0 us, 17.0 with 7 waves).
 template <int DT, int FMT, int WAVES, int CH>
-__global__ __launch_bounds__(WAVES * 64) void norm_kernel(NormParams p) {
+__global__ __launch_bounds__(WAVES * 64, CH <= 2 ? 8 : 4) void norm_kernel(NormParams p) {
   constexpr int THREADS = WAVES * 64;
   const int64_t row = blockIdx.x;
   const int t = threadIdx.x, pieces = p.K / 8;
@@ -113,11 +117,24 @@ __global__ __launch_bounds__(WAVES * 64) void norm_kernel(NormParams p) {
       // every border (ties, powers of two) has at least 16 zero bits at its end
       if constexpr (FMT >= 0) border = min(border, (__builtin_bit_cast(uint32_t, v[i]) + 4u) << 16);
     }
-    if (far || (FMT >= 0 && border <= 8u << 16)) {   // before hidden is stored, which may be in the place of x or residual
+    uint32_t amax = 0;            // the largest magnitude: of the thread, then of the block's four
+    const auto largest = [&] {
+      amax = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = max(amax, __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu);
+    };
+    bool repeat = far;
+    if constexpr (FMT >= 0) {
+      largest();
+      // below 2^-100 the block may be one whose borders end in fewer zeros, or whose v are subnormal
+      repeat = repeat || border <= 8u << 16 || amax - 1 < ((127u - 100) << 23) - 1;
+    }
+    if (repeat) {   // before hidden is stored, which may be in the place of x or residual
       Inputs<DT> again;
       again.load(x, res, c);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = to_odd(again.h64(i) * rstd * (double)w[i]);
+      if constexpr (FMT >= 0) largest();
     }
     if (p.hidden) {
       uint16_t *to = p.hidden + row * p.ldh + 8 * (int64_t)c;
@@ -130,9 +147,6 @@ __global__ __launch_bounds__(WAVES * 64) void norm_kernel(NormParams p) {
     }
     if (p.y) store8<DT>(p.y + row * p.ldy + 8 * (int64_t)c, v);
     if constexpr (FMT >= 0) {
-      uint32_t amax = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = max(amax, __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu);
       amax = max(amax, (uint32_t)__shfl_xor((int)amax, 1));
       amax = max(amax, (uint32_t)__shfl_xor((int)amax, 2));
       const uint32_t e = mx_scale<FMT>(amax);

@@ -154,3 +154,30 @@ def test_rows_whose_norm_is_near_the_ends_of_32_bits(K):
                 n = mnb.rmsnorm(X, W, 0.0, residual=residual, fmt=fmt, keep16=True)
                 within_half_a_step(n.y, want, dt, K)
                 same_codes(n.q, want, fmt, K)
+
+
+# 32 whole numbers whose squares sum to 32 * 128^2
+IN_128THS = np.array([192, 191, 191, 160, 160, 150, 150, 150, 150, 131, 131, 131, 131, 131, 131, 129, 129, 129, 127, 125, 125, 125, 125, 113, 113, 80, 65, 65, 33, 13, 7, 7])
+
+
+@pytest.mark.parametrize("fmt", [FP4, FP8])
+@pytest.mark.parametrize("K", [64, 2048, 40000])
+def test_outputs_among_the_smallest_numbers(fmt, K):
+    """Weights of 2^-130 and less: the block's scale is the smallest, FP8's ties odd multiples of 2^-137, and 32
+    bits hold y in steps of 2^-149.  Residuals that such steps lose put y beside the tie."""
+    r = rng(5, fmt, K)
+    x = np.tile(IN_128THS / 128, K // 32)                # mean square 1, half of them odd
+    res = np.where(x > 0, 2.0 ** -22, 0.0)
+    sign = np.ones(K)
+    for v in np.unique(x):
+        at = np.flatnonzero(x == v)
+        sign[at] = np.where(np.arange(len(at)) % 2 == 0, 1.0, -1.0)
+    h = np.stack([x + res * sign, x - res * sign])
+    X, R = dev(np.stack([x, x]), torch.bfloat16), dev(np.stack([res * sign, -res * sign]), torch.bfloat16)
+    for e in (-125, -127, -128, -129, -130, -131, -132, -133):
+        W = dev(np.full(K, 2.0 ** e), torch.bfloat16)
+        want = h / np.sqrt((h * h).mean(-1, keepdims=True)) * 2.0 ** e
+        n = mnb.rmsnorm(X, W, 0.0, residual=R, fmt=fmt, keep16=True)
+        same_codes(n.q, want, fmt, e)
+        y = n.y.double().cpu().numpy()
+        assert (np.abs(y - want) <= np.abs(want) * 2.0 ** -8 + 2.0 ** -134).all()
