@@ -14,10 +14,11 @@
 // (FP8 X) and 138 against 128 (FP4 X): the part clocks down to 1.5 - 1.9 GHz under this load, and
 // that shape moves twice the accumulator bytes per operation.
 //
-// Precision.  With FP4 on both sides the sum of an instruction is as exact as 32 bits; with FP8 the
-// adder keeps about 12 bits below the sum of the magnitudes where the scales of its blocks
-// differ by many octaves (2^-12.6 of it was the largest error found over scales of 2^-8 to
-// 2^8), and about 24 where they are alike.
+// Precision, in units of the sum of the terms' magnitudes.  With FP4 on both sides the sums are as
+// exact as 32 bits (2^-23.4 at most over scales of 2^-8 to 2^8, K up to 9728).  With FP8 the adder
+// aligns its terms to the largest and keeps fewer bits: 2^-17.9 at K = 96, 2^-20.6 at 2016 and 2^-21.8 at 9696 with
+// scales alike, 2^-16.9, 2^-17.6 and 2^-19.2 with scales of 2^-8 to 2^8, 2^-12.6 the largest found on any data.
+// It is the instruction's own; the 16-bit formats would hold FP8 values, at half the rate.
 #pragma once
 
 #include <type_traits>

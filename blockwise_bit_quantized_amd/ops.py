@@ -257,7 +257,9 @@ def mx_pack(q: MxTensor) -> MxWeight:
 
 def mx_matmul(x: MxTensor, w: MxWeight, bias=None, dtype=None, out=None):
     """Y [M, N] = x . w^T (+ bias [N]) in ``dtype`` (fp16 by default, or bf16; the bias's type too),
-    summed in 32 bits and rounded once; x FP8 or FP4 from mx_quantize, rmsnorm or mx_tensor."""
+    rounded once; x FP8 or FP4 from mx_quantize, rmsnorm or mx_tensor.  FP4 x is summed as exactly as
+    32 bits allow; with FP8 x the matrix instruction keeps fewer bits (an error of at most 2^-12 of
+    the sum of |x| |w|, 2^-16 to 2^-22 in measurements)."""
     return _run(_ext.matmul, x.codes, x.scales, x.fmt, x.rows, x.K, x.ldc, x.lds, w.wq, w.sc, w.N, w.K, bias,
                 dtype or torch.float16, out)
 

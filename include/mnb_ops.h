@@ -65,8 +65,15 @@ int mnb_mx_pack(const void *codes, int64_t ldc, const void *scales, int64_t lds,
 
 /*
  * Y[M,N] = X . W^T (+ bias), X an MX tensor [M, K] (fmt FP8 or FP4), W an FP4 weight packed
- * by mnb_mx_pack; Y fp16 or bf16 [M, N] row-major, rounded once from FP32 accumulation; bias
- * [N] of Y's type or NULL.  K % 32 == 0, K < 2^22; ldc and lds at most 2^23.  A NaN scale or element of X reaches its
+ * by mnb_mx_pack; Y fp16 or bf16 [M, N] row-major, rounded once from the matrix instructions' 32-bit
+ * sums; bias [N] of Y's type or NULL.  How exact these sums are depends on X's format (the
+ * MX specification leaves it open), in units of sum_k |x| |w| of the result:
+ *   FP4 X  as a sum in 32 bits: at most (K / 128 + 1) 2^-23;
+ *   FP8 X  fewer bits, as the instruction aligns its terms to the largest: at most 2^-12, measured
+ *          2^-16 to 2^-22 (the smaller the longer K) over scales of 2^-8 to 2^8.  Of Y's own size that
+ *          is about 2^-17 on random data, where 3 to 8% of fp16 results are a neighbour of what a
+ *          32-bit sum would give; results that nearly cancel have no more than that.
+ * K % 32 == 0, K < 2^22; ldc and lds at most 2^23.  A NaN scale or element of X reaches its
  * own row of Y only, one of W its own column.  codes, scales, wq, sc and Y 16-byte aligned, as
  * are ldc and lds; bias 16-byte aligned.  Y must not overlap the inputs.
  *
