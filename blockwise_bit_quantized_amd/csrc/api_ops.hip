@@ -48,12 +48,12 @@ bool bad_ld(int64_t ld, int64_t least) { return ld < least || ld > (1ll << 40); 
 int check_matmul_sizes(int M, int N, int K, int fmt) {
   if (M < 0 || N < 0 || K < 0) return MNB_ERR_INVALID_ARG;
   if (fmt != MNB_MX_FP4 && fmt != MNB_MX_FP8) return MNB_ERR_INVALID_ARG;
-  // 32-bit offsets from a tile's first row reach its 256 rows of X
+  // 32-bit offsets from a tile's first row reach its 128 rows of X
   if (K % kBlock || K >= kMxMaxK) return MNB_ERR_UNSUPPORTED;
   // a launch has fewer than 2^32 threads: 256 per (row group, step) of the packer and at most
-  // 512 per range and tile of 64 x 128 outputs of the product
+  // 512 per tile of 64 x 128 outputs of the product, whose count is rounded up to a multiple of 8
   if (cdiv(N, 64) * cdiv(K, kMxStep) >= 1 << 24) return MNB_ERR_UNSUPPORTED;
-  if (cdiv(M, 64) * cdiv(N, 128) >= 1 << 19) return MNB_ERR_UNSUPPORTED;
+  if (cdiv(M, 64) * cdiv(N, 128) > (1 << 23) - 8) return MNB_ERR_UNSUPPORTED;
   return MNB_OK;
 }
 

@@ -53,7 +53,8 @@ int mnb_mx_dequantize(const void *codes, int64_t ldc, const void *scales, int64_
                       int M, int K, void *Y, int dtype, int64_t ldy, void *stream);
 
 /*
- * Device layout of an FP4 weight [N, K] for mnb_mx_matmul (K % 32 == 0, K < 2^22):
+ * Device layout of an FP4 weight [N, K] for mnb_mx_matmul (K % 32 == 0, K < 2^22,
+ * ceil(N / 64) ceil(K / 128) < 2^24, else MNB_ERR_UNSUPPORTED):
  * rows in groups of 64, K in steps of 128; the 4 KiB of a (group, step) hold four matrix
  * operands of 16 rows, each 16 bytes (32 consecutive k of one row) for each of 64 lanes.
  * mnb_mx_packed_sizes (host only) gives the two buffers' bytes.  Rows past N and k past K
@@ -73,9 +74,10 @@ int mnb_mx_pack(const void *codes, int64_t ldc, const void *scales, int64_t lds,
  *          2^-16 to 2^-22 (the smaller the longer K) over scales of 2^-8 to 2^8.  Of Y's own size that
  *          is about 2^-17 on random data, where 3 to 8% of fp16 results are a neighbour of what a
  *          32-bit sum would give; results that nearly cancel have no more than that.
- * K % 32 == 0, K < 2^22; ldc and lds at most 2^23.  A NaN scale or element of X reaches its
- * own row of Y only, one of W its own column.  codes, scales, wq, sc and Y 16-byte aligned, as
- * are ldc and lds; bias 16-byte aligned.  Y must not overlap the inputs.
+ * W's sizes as for mnb_mx_pack, ceil(M / 64) ceil(N / 128) <= 2^23 - 8, ldc and lds at most 2^23, else
+ * MNB_ERR_UNSUPPORTED.  A NaN scale or element of X reaches its own row of Y only, one of W its
+ * own column.  codes, scales, wq, sc and Y 16-byte aligned, as are ldc and lds; bias 16-byte
+ * aligned.  Y must not overlap the inputs.
  *
  * M <= 32 streams the weight once for all rows; more rows run as tiles of 64 or 128 rows.
  */
