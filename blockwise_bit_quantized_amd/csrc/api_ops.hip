@@ -250,9 +250,6 @@ static int check_logprobs(int M, int V, int dtype, int top) {
   if (M < 0 || V < 0 || bad_dtype(dtype, true) || top < 0) return MNB_ERR_INVALID_ARG;
   if (top > MNB_LOGPROBS_MAX_TOP || V > (1 << 22)) return MNB_ERR_UNSUPPORTED;
   if (M > 0 && V > 0 && top > V) return MNB_ERR_INVALID_ARG;
-  int chunk = 0;
-  // a launch has fewer than 2^32 threads, up to 1024 per part of a row
-  if (V > 0 && (int64_t)M * logprobs_chunks(M, V, dtype, &chunk) >= 1 << 22) return MNB_ERR_UNSUPPORTED;
   return MNB_OK;
 }
 
@@ -301,7 +298,29 @@ int mnb_logprobs(const void *logits, int dtype, int M, int V, int64_t ldl, const
   p.chunks = logprobs_chunks(M, V, dtype, &p.chunk);
   p.part = static_cast<float *>(workspace);
   p.keys = reinterpret_cast<uint64_t *>(static_cast<char *>(workspace) + (need ? (size_t)M * p.chunks * 16 : 0));
-  return status(launch_logprobs(dtype, p, as_stream(stream)));
+  // a launch has fewer than 2^32 threads, up to 1024 per part of a row
+  const int rows = ((1 << 22) - 1) / p.chunks;
+  for (int64_t m0 = 0; m0 < M; m0 += rows) {
+    LogprobsParams q = p;
+    q.M = (int)(M - m0 < rows ? M - m0 : rows);
+    q.x = static_cast<const char *>(logits) + m0 * ldl * sz;
+    if (tokens) {
+      q.tokens += m0;
+      q.logprob += m0;
+    }
+    if (entropy) q.entropy += m0;
+    if (top) {
+      q.top_logprobs += m0 * top;
+      q.top_tokens += m0 * top;
+    }
+    if (need) {
+      q.part += m0 * p.chunks * 4;
+      q.keys += m0 * p.chunks * top;
+    }
+    const hipError_t err = launch_logprobs(dtype, q, as_stream(stream));
+    if (err != hipSuccess) return MNB_ERR_HIP;
+  }
+  return MNB_OK;
 }
 
 }  // extern "C"

@@ -33,3 +33,17 @@ def test_product_of_more_than_2_to_32_outputs(fmt):
         part = y[at:at + 16384]
         full = part[:len(part) // 64 * 64].view(-1, 64, N)
         assert bool((full == want).all()) and torch.equal(part[len(full) * 64:], want[:len(part) % 64]), at
+
+
+@pytest.mark.parametrize("M,V,top", [((1 << 22) + 5, 8, 3), ((1 << 22) - 1, 5, 5), (9 << 20, 3, 0)])
+def test_logprobs_of_more_than_2_to_22_rows(M, V, top):
+    """1000 rows repeat, and so do their results."""
+    r = np.random.default_rng([20261210, M])
+    x = torch.from_numpy(r.standard_normal((1000, V))).to(DEV).half()
+    tok = torch.from_numpy(r.integers(0, V, 1000)).to(DEV)
+    want = mnb.logprobs(x, tok, top)
+    rep = -(-M // 1000)
+    got = mnb.logprobs(x.repeat(rep, 1)[:M], tok.repeat(rep)[:M], top)
+    for a, b in zip(got, want):
+        if b is not None:
+            assert a.shape[0] == M and torch.equal(a, b.repeat(rep, *[1] * (b.dim() - 1))[:M])
