@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -80,15 +81,25 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
 
 
 def _build_binding(verbose: bool) -> None:
+    """The torch module.  Where its tools are not there the library stands alone: MatMulNBits and the C ABI
+    need nothing else, and the torch calls of the operators raise an ImportError."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
-        return                                   # the C ABI alone needs no torch
-    torch = os.path.join(list(spec.submodule_search_locations)[0])
+    torch = os.path.join(list(spec.submodule_search_locations)[0]) if spec else ""
     inc, lib = os.path.join(torch, "include"), os.path.join(torch, "lib")
+    python = sysconfig.get_paths()["include"]
+    missing = ["torch"] if spec is None else [
+        what for what, there in (("g++", shutil.which("g++")),
+                                 ("torch's headers", os.path.exists(os.path.join(inc, "ATen", "ATen.h"))),
+                                 ("Python's headers", os.path.exists(os.path.join(python, "Python.h")))) if not there]
+    if missing:
+        if os.path.exists(BINDING_LIB):          # of an earlier build: not of this library
+            os.remove(BINDING_LIB)
+        print("_mnb_ops is not built: no %s" % " and no ".join(missing), file=sys.stderr, flush=True)
+        return
     tmp = BINDING_LIB + ".tmp%d" % os.getpid()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DUSE_ROCM", "-D__HIP_PLATFORM_AMD__=1",
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
-           "-isystem", sysconfig.get_paths()["include"], "-I" + os.path.join(ROOT, "include"),
+           "-isystem", python, "-I" + os.path.join(ROOT, "include"),
            os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)

@@ -30,6 +30,17 @@ _ext: Any = None
 _status_text: Any = None
 
 
+class _NotBuilt:
+    """In the place of a native module that could not be imported: every use of it says why."""
+
+    def __init__(self, cause):
+        self._cause = cause
+
+    def __getattr__(self, name):
+        raise ImportError("the torch calls of the operators need the module _mnb_ops, built for this Python and torch: "
+                          "run `python blockwise_bit_quantized_amd/build.py` (%s)" % self._cause) from self._cause
+
+
 def _bind(library, status_text):
     """Called once by the package with its loaded library."""
     global lib, _ext, _status_text
@@ -50,7 +61,11 @@ def _bind(library, status_text):
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args
     if torch is not None:
-        from . import _mnb_ops as _ext   # built with the library; there is no other path
+        try:
+            from . import _mnb_ops as _ext   # built with the library; there is no other path
+        except ImportError as e:             # MatMulNBits and the C calls do not need it
+            _ext = _NotBuilt(e)
+            return
         _ext.bind(*(C.cast(getattr(lib, n), P).value for n in (
             "mnb_mx_quantize", "mnb_mx_dequantize", "mnb_mx_matmul", "mnb_rmsnorm",
             "mnb_logprobs", "mnb_logprobs_workspace_bytes", "mnb_status_string")))
