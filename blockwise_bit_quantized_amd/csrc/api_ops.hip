@@ -22,16 +22,29 @@ bool off16(int64_t bytes) { return (bytes & 15) != 0; }
 int64_t mx_row(int fmt, int K) { return fmt == MNB_MX_FP4 ? K / 2 : K; }
 int64_t scale_row(int K) { return cdiv(K, kMxScaleK) * 16; }
 
-// [p, p + (rows - 1) ld + row): the bytes of a strided tensor
+// rows of `row` bytes, `ld` apart
 struct Span {
   const void *p;
   int64_t rows, ld, row;
 };
+uintptr_t end_of(const Span &s) {
+  uintptr_t d, e;
+  if (__builtin_mul_overflow((uintptr_t)(s.rows - 1), (uintptr_t)s.ld, &d) || __builtin_add_overflow(d, (uintptr_t)s.row, &d) ||
+      __builtin_add_overflow((uintptr_t)s.p, d, &e))
+    return UINTPTR_MAX;
+  return e;
+}
+// Do they share a byte?  Rows between each other's rows (columns of one buffer) do not; where the row
+// distances differ, whole ranges count.
 bool overlap(const Span &a, const Span &b) {
   if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.row <= 0 || b.row <= 0) return false;
   const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-  const uintptr_t a1 = a0 + (uintptr_t)((a.rows - 1) * a.ld + a.row), b1 = b0 + (uintptr_t)((b.rows - 1) * b.ld + b.row);
-  return a0 < b1 && b0 < a1;
+  if (a0 >= end_of(b) || b0 >= end_of(a)) return false;
+  const int64_t ld = a.rows > 1 ? a.ld : b.ld;
+  if (ld <= 0 || (a.rows > 1 && b.rows > 1 && a.ld != b.ld) || (a.rows == 1 && b.rows == 1)) return true;
+  // b's columns, counted from a's
+  const int64_t d = b0 >= a0 ? (int64_t)((b0 - a0) % (uintptr_t)ld) : (int64_t)((ld - (int64_t)((a0 - b0) % (uintptr_t)ld)) % ld);
+  return d < a.row || d + b.row > ld;
 }
 bool same(const Span &a, const Span &b) { return a.p == b.p && (a.ld == b.ld || a.rows == 1) && a.row == b.row; }
 
@@ -42,7 +55,7 @@ int check_mx(int fmt, int K, const void *codes, int64_t ldc, const void *scales,
   return MNB_OK;
 }
 
-// sizes that every call here takes: a row distance times the row count stays far below 2^63
+// a row distance in elements: any real one is far below 2^40
 bool bad_ld(int64_t ld, int64_t least) { return ld < least || ld > (1ll << 40); }
 
 int check_matmul_sizes(int M, int N, int K, int fmt) {

@@ -10,6 +10,8 @@
  *    `dtype` is MNB_F16, MNB_BF16 or MNB_F32;
  *  - rows may be strided: `ld...` arguments are distances between rows, in elements of the
  *    tensor, or in bytes for codes and scales;
+ *  - an output shares no byte with an input or another output (MNB_ERR_ALIAS), but where said; rows
+ *    between each other's rows, as column ranges of one buffer with one row distance, share none;
  *  - workspaces of these calls need no initialisation and hold nothing between calls.
  * M, N, K, V == 0 (no rows or no columns): nothing is enqueued, MNB_OK, except K == 0 of
  * mnb_mx_matmul, which fills Y with the bias or zeros.
@@ -98,7 +100,7 @@ int mnb_mx_describe_route(int M, int N, int K, int fmt, char *buf, size_t buf_le
  *           so are the other tensors then)
  * dtype fp16 or bf16 for X, residual, weight [K], hidden and Y; weight contiguous.  hidden may be
  * residual or X itself, and Y may be X (same address and row distance); any other overlap
- * of an output with an input or another output is refused (MNB_ERR_ALIAS).
+ * is refused.
  * Any K and any element alignment without codes.
  */
 int mnb_rmsnorm(const void *X, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
