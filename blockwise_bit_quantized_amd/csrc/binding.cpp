@@ -59,6 +59,11 @@ int64_t integer(PyObject *o) {
   if (v == -1 && PyErr_Occurred()) throw Raised();
   return v;
 }
+bool truth(PyObject *o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised();
+  return v != 0;
+}
 void *pointer(PyObject *o) {
   void *p = PyLong_AsVoidPtr(o);
   if (!p && PyErr_Occurred()) throw Raised();
@@ -222,10 +227,10 @@ PyObject *rmsnorm(PyObject *const *a) {
   } else if (hidden.defined()) {
     fail(PyExc_ValueError, "hidden needs a residual");
   }
-  const bool mx = a[5] != Py_None;
+  const bool mx = a[5] != Py_None, keep16 = !mx || truth(a[6]);
   if (mx) blocks(K, "x");
   if (y.defined()) ldy = row_distance_beside(y, "out", type, M, K, x.device());
-  else if (!mx || PyObject_IsTrue(a[6])) y = empty({M, ldy = K}, x, type);
+  else if (keep16) y = empty({M, ldy = K}, x, type);
   at::Tensor codes, scales;
   int64_t ldc = 0, lds = 0;
   int fmt = 0;
