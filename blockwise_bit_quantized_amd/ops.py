@@ -132,7 +132,10 @@ def _check(st: int):
 
 def _run(f, t, *args):
     """f(stream, t, *args) on the current stream of t's device, with that device current."""
-    i = t.get_device()
+    try:
+        i = t.get_device()
+    except AttributeError:
+        i = -1
     if i < 0:
         return f(0, t, *args)            # refused there, after the other checks
     # the stream's handle alone: building torch's Stream object costs as much as half a launch

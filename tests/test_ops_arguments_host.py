@@ -17,3 +17,12 @@ def test_an_error_in_keep16_is_passed_on():
     x, w = torch.zeros(4, 64, dtype=torch.float16), torch.ones(64, dtype=torch.float16)
     with pytest.raises(ZeroDivisionError, match="of the caller"):
         mnb.rmsnorm(x, w, fmt=mnb.MNB_MX_FP8, keep16=Odd())
+
+
+@pytest.mark.parametrize("bad", [None, 3, np.zeros((4, 64), np.float16), [[1.0]]])
+def test_what_is_no_tensor_is_a_type_error(bad):
+    x, w = torch.zeros(4, 64, dtype=torch.float16), torch.ones(64, dtype=torch.float16)
+    for call in (lambda: mnb.mx_quantize(bad), lambda: mnb.rmsnorm(bad, w), lambda: mnb.logprobs(bad),
+                 lambda: mnb.rmsnorm(x, bad), lambda: mnb.logprobs(x, bad if bad is not None else 7)):
+        with pytest.raises(TypeError, match="tensor"):
+            call()
