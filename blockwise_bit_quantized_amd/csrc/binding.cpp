@@ -133,6 +133,11 @@ void check(int status) {
   if (status != MNB_OK) fail(PyExc_RuntimeError, "%s", c.status_string(status));
 }
 
+// a caller's tensor that the call wrote into: its version tells a graph that saved it
+void written(const at::Tensor &t) {
+  if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 at::Tensor empty(at::IntArrayRef shape, const at::Tensor &like, at::ScalarType type) {
   return at::empty(shape, like.options().dtype(type));
 }
@@ -178,6 +183,7 @@ PyObject *dequantize(PyObject *const *a) {
   on_gpu(codes);
   check(c.dequantize(data(codes), integer(a[6]), data(scales), integer(a[7]), fmt, size(M), size(K), data(y), type_code(type), ldy,
                      pointer(a[0])));
+  if (a[9] != Py_None) written(y);
   return wrap(y);
 }
 
@@ -205,6 +211,7 @@ PyObject *matmul(PyObject *const *a) {
   on_gpu(codes);
   check(c.matmul(data(codes), integer(a[6]), data(scales), integer(a[7]), fmt, data(wq), data(sc), data(bias), data(y), code, size(M),
                  size(N), size(K), pointer(a[0])));
+  if (a[14] != Py_None) written(y);
   return wrap(y);
 }
 
@@ -245,6 +252,8 @@ PyObject *rmsnorm(PyObject *const *a) {
   on_gpu(x);
   check(c.rmsnorm(data(x), ldx, data(residual), ldr, data(weight), (float)eps, code, size(M), size(K), data(hidden), ldh, data(y), ldy,
                   fmt, data(codes), ldc, data(scales), lds, pointer(a[0])));
+  if (a[7] != Py_None) written(y);
+  if (a[8] != Py_None) written(hidden);
   return Py_BuildValue("NNNNLLLL", wrap(y), wrap(hidden), wrap(codes), wrap(scales), (long long)ldc, (long long)lds, (long long)M,
                        (long long)K);
 }
