@@ -18,11 +18,14 @@
 //     a NaN or +infinity, the keys are taken one at a time, each the largest below the last.
 //
 // Bound by memory and vector instructions together for many rows (1024 x 49152 fp16, top 20:
-// 101 MB in 27 us, 3.7 TB/s, while the instructions take 40 to 60% of the SIMDs' cycles), by
-// the chain of reductions for one row (49152: 7.0 us).
+// 101 MB in 27 to 28.5 us, 3.6 TB/s, while the instructions take 40 to 60% of the SIMDs' cycles; bfloat16
+// 30.5, fp32 55.7), by the chain of reductions for one row (49152: 7.2 us, bfloat16 8.5, fp32 8.1).
 //
-// Rows longer than one workgroup holds, and calls with few rows, split each row; the parts'
-// (m, S, T) and keys go through the workspace and a second kernel joins them in part order.
+// Rows longer than one workgroup holds are split; the parts' (m, S, T) and keys go through the
+// workspace and a second kernel joins them in part order (one row of 50257 8.6 us, of 131072 10.6, of 262144
+// 10.2; 1024 rows of 131072 fp16 65, fp32 137).  A last part with elements in fewer threads than
+// give `top` groups has no threshold and takes its keys one at a time: 1024 rows of 50257, whose
+// last parts hold 1105, take 110 us for top 20 (fp32 333).
 #include "ops.h"
 
 namespace mnb {
@@ -378,14 +381,9 @@ __global__ __launch_bounds__(THREADS) void join_kernel(LogprobsParams p) {
   const float xt = t == 0 ? token_logit<DT>(p, row) : 0.f;
   __syncthreads();
   // every thread joins the sums in part order, so all hold the same values
+  // (a part's maximum passes a NaN over; its S is NaN then, and so is the row's)
   float m = -__builtin_inff();
-  bool nan = false;
-  for (int i = 0; i < p.chunks; ++i) {
-    const float mi = part[i][0];
-    nan = nan || mi != mi;
-    m = fmaxf(m, mi);
-  }
-  if (nan) m = __builtin_nanf("");
+  for (int i = 0; i < p.chunks; ++i) m = fmaxf(m, part[i][0]);
   float S = 0.f, T = 0.f;
   for (int i = 0; i < p.chunks; ++i) {
     const f4_t v = part[i];
@@ -407,7 +405,10 @@ __global__ __launch_bounds__(THREADS) void join_kernel(LogprobsParams p) {
   }
 }
 
-// elements one workgroup holds in registers
+// Elements one workgroup holds in registers.  With 12 pieces a thread of the 8-wave form three workgroups
+// share a CU; 14 or 16 pieces leave two, and everything is slower but what then fits (us, 12 / 14 / 16
+// pieces, fp16, top 20: 1024x32000 20.9 / 23.4 / 23.5, 1024x49152 28.4 / 32.0 / 32.5, 1024x131072 64 / 81 / 70,
+// 1024x50257 110 / 34 / 34).
 constexpr int held(int waves, int e) { return waves * 64 * e * 8; }
 constexpr int kSmall = held(4, 2), kMiddle = held(8, 4), kLarge = held(8, 12);
 static_assert(kLarge == held(16, 6), "both large forms hold the same part");
@@ -426,7 +427,7 @@ hipError_t launch(const LogprobsParams &p, hipStream_t s) {
     hipLaunchKernelGGL((part_kernel<DT == DT_F32 ? DT_F16 : DT, 8, 12>), grid, dim3(512), 0, s, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.chunks == 1) return e;
-  const uint32_t lds = (uint32_t)((p.chunks * p.top + 1) / 2 * 16 + p.chunks * 16);   // below 22 KiB
+  const uint32_t lds = (uint32_t)((p.chunks * p.top + 1) / 2 * 16 + p.chunks * 16);   // 22.8 KiB at most: 86 parts of 32
   // 16 waves where there are many keys to rank (16 parts of 20: 8.1 us with 4)
   if (p.chunks * p.top > 128) hipLaunchKernelGGL((join_kernel<DT, 1024>), dim3((uint32_t)p.M), dim3(1024), lds, s, p);
   else hipLaunchKernelGGL((join_kernel<DT, 256>), dim3((uint32_t)p.M), dim3(256), lds, s, p);
@@ -435,8 +436,10 @@ hipError_t launch(const LogprobsParams &p, hipStream_t s) {
 
 }  // namespace
 
-// Parts of a row and their length: whole rows of up to 49152 elements when the rows fill the
-// chip, else parts short enough for about two workgroups per CU.
+// Parts of a row and their length: whole rows of up to kLarge elements, however few (us, whole / in
+// parts and joined, fp16: 1x8000 4.3 / 6.3, 1x20000 5.8 / 7.2, 1x32000 6.1 / 7.4, 1x49152 7.2 / 8.7, 32x20000
+// 7.1 / 10.2, 32x49152 9.1 / 11.7, 256x49152 11.6 / 15.9; only 1x49152 bfloat16 goes 8.5 / 8.3), longer rows in
+// parts of kLarge when they fill the chip, else in parts short enough for up to four workgroups per CU.
 int logprobs_chunks(int M, int V, int dtype, int *chunk) {
   (void)dtype;
   const int sizes[] = {kSmall, kMiddle, kLarge};

@@ -9,7 +9,12 @@
 // first took 6.2 us where this takes 5.5 (8x49152x576).  KSPLIT waves of a workgroup share a
 // row's K when the rows alone give too few waves to keep the memory busy; their partial sums
 // meet in LDS in a fixed order.  Two X operands for 17 to 32 rows take 5.9 us at
-// 32x8192x2048 and 16.1 at 32x49152x2048, the tiled kernel 7.5 and 21.4.
+// 32x8192x2048 and 16.1 at 32x49152x2048, the tiled kernel 7.5 and 21.4.  With FP4 X:
+// 1x49152x2048 9.8 us, 8x49152x576 5.3, 32x8192x2048 5.7, 32x49152x2048 14.4, 24x16384x4096 10.3.
+//
+// Farthest from the weight's bytes are long K and few columns (1x2560x9728 6.4 us with FP8 X, 32x2560x9728
+// 13.5, FP4 9.2, for 2.9): N gives 160 workgroups of at most four waves that share a K, and a wave issues a
+// 512-k part's loads when it has multiplied the part before.
 #include "mx_mfma.h"
 
 namespace mnb {

@@ -15,9 +15,7 @@ constexpr int kMxScaleK = 512; // k of one scale dword per lane (4 steps, one by
 
 typedef float f4_t __attribute__((ext_vector_type(4)));
 typedef float f2_t __attribute__((ext_vector_type(2)));
-typedef int i4_t __attribute__((ext_vector_type(4)));
 typedef int i8_t __attribute__((ext_vector_type(8)));
-typedef short s2_t __attribute__((ext_vector_type(2)));
 
 // ---- 16-bit and 32-bit values -------------------------------------------------------------
 

@@ -7,15 +7,17 @@
 // nevertheless that of the exact y, as values so near a border of the element grid that 4
 // units could cross it are computed again in 64 bits from x and residual (one element in 7000, and
 // the only ones whose code or block scale can differ).  So are rows whose norm 32 bits do not hold,
-// whatever their outputs, and blocks below 2^-100.  (Two limits of 32 bits stay: a y past their range counts as
-// infinite, and an element 2^126 times smaller than its row's norm keeps their absolute precision.)  All in 64 bits measured 52.7 us
-// at 8192 x 4096 (bfloat16, residual, FP8) against 48.2.
+// whatever their outputs, and blocks below 2^-100.  (Two limits of 32 bits stay: a y past their
+// range counts as infinite, and an element 2^126 times smaller than its row's norm keeps their
+// absolute precision.)  All in 64 bits measured 55.7 us at 8192 x 4096 (bfloat16, residual,
+// FP8) against 45.8, in fp16 59.0 against 44.8.
 //
-// Bound by memory (8192 x 4096: 236 MB in 45 us, 5.3 TB/s; 1 x 2048 2.9 us and 333 x 896 3.1,
-// latencies): each input is read once and each output written once.  The aligned
+// Bound by memory (8192 x 4096, bfloat16, residual, FP8: 236 MB in 45.5 us, 5.2 TB/s; 1 x 2048 2.8 us and
+// 333 x 896 3.1, latencies): each input is read once and each output written once.  The aligned
 // kernel keeps a row's h in registers between the sum of squares and the outputs (CH pieces
 // of 8 elements a thread); rows longer than that read the inputs a second time for the
-// pieces past it (from L2).  Rows of other alignment take the element-wise kernel.
+// pieces past it (from L2).  Rows of other alignment take the element-wise kernel, whose accesses of
+// 2 bytes bound it (4096 x 4095 with a residual, 16 bits: 134 MB in 56.8 us, 2.4 TB/s).
 #include "ops.h"
 
 namespace mnb {
@@ -139,7 +141,7 @@ __global__ __launch_bounds__(WAVES * 64, CH <= 2 ? 8 : 4) void norm_kernel(NormP
     if (p.hidden) {
       uint16_t *to = p.hidden + row * p.ldh + 8 * (int64_t)c;
       // with MX outputs the next call reads those and not the hidden rows: past the caches
-      // 8192 x 4096 takes 45.7 us, not 48.2 (with 16-bit outputs 57.8, not 55.1, so not there)
+      // 8192 x 4096 takes 45.8 us, not 49.3 (4096 x 8192 with 16-bit outputs 51.4, not 49.9, so not there)
       if constexpr (FMT >= 0)
         __builtin_nontemporal_store(u4_t{pack2<DT>(h8[0], h8[1]), pack2<DT>(h8[2], h8[3]), pack2<DT>(h8[4], h8[5]), pack2<DT>(h8[6], h8[7])},
                                     reinterpret_cast<u4_t *>(to));
@@ -208,9 +210,9 @@ hipError_t launch(const NormParams &p, hipStream_t s) {
       return hipGetLastError();
     }
   }
-  // As few pieces a thread as give a workgroup the row, of 4 or 16 waves: with 4 pieces 8192 x 2560
-  // (FP4 out) took 45.1 us and 4096 x 8192 (16 bits) 55.1, with 2 and 1 they take 43.6 and 50.4;
-  // 16 waves for 4096 k took 67 where 4 take 48.
+  // As few pieces a thread as give a workgroup the row, of 4 or 16 waves: with 4 pieces in 4 waves 8192 x 2560
+  // (FP4 out, the kernel alone) takes 41.7 us, 8192 x 4096 (FP8) 53.0 and 4096 x 8192 (16 bits) 51.4, so
+  // 30.3, 45.8 and 49.9; 16 waves for 2560 and 4096 k take 61.2 and 70.4.
   if (p.K <= 2048) hipLaunchKernelGGL((norm_kernel<DT, FMT, 4, 1>), grid, dim3(256), 0, s, p);
   else if (p.K <= 4096) hipLaunchKernelGGL((norm_kernel<DT, FMT, 4, 2>), grid, dim3(256), 0, s, p);
   else if (p.K <= 8192) hipLaunchKernelGGL((norm_kernel<DT, FMT, 16, 1>), grid, dim3(1024), 0, s, p);
