@@ -64,3 +64,23 @@ def test_sums_that_cancel(M, N, K, fmt, spread):
     bound = size * ((total / 128 + 1) * 2.0 ** -23 if fmt == FP4 else 2.0 ** -12) + np.abs(want) * 2.0 ** -8
     assert (np.abs(got - want) <= bound).all(), (np.abs(got - want) / bound).max()
     assert (got == got[:1]).all()
+
+
+@pytest.mark.parametrize("fmt", [FP4, FP8])
+@pytest.mark.parametrize("M", [1, 40])
+def test_scales_at_the_ends_of_their_range(fmt, M):
+    """Scale bytes from 0 (2^-127) to 254 (2^127) whose products lie inside 32 bits, each over a whole row and mixed in
+    one.  The bounds above; results below the smallest normal number may be flushed."""
+    r = np.random.default_rng([20261211, fmt, M])
+    K, N = 256, 72
+    pairs = [(0, 254), (254, 0), (0, 250), (1, 250), (127, 0), (0, 127), (127, 1), (3, 127), (20, 110), (0, 0), (64, 64), (240, 100), (253, 1), (200, 54)]
+    mixed = np.array([0, 254, 127, 1, 250, 3, 200, 60])
+    rows = [(np.full(K // 32, a), np.full(K // 32, b)) for a, b in pairs] + [(mixed, 254 - mixed)]
+    for xs, ws in rows:
+        xq, wq = ref.round_elements(r.uniform(-6, 6, (M, K)), fmt), ref.FP4[r.integers(0, 16, (N, K))]
+        xs, ws = np.tile(xs, (M, 1)), np.tile(ws, (N, 1))
+        each = np.ldexp(1.0, xs[:1] + ws[:1] - 254).repeat(32, 1)       # both scales of a term: in range where either alone is not
+        want, size = (xq * each) @ wq.T, (np.abs(xq) * each) @ np.abs(wq).T
+        got = mnb.mx_matmul(to_mx(xq, xs, fmt), mnb.mx_pack(to_mx(wq, ws, FP4)), dtype=torch.bfloat16).double().cpu().numpy()
+        bound = size * ((K / 128 + 1) * 2.0 ** -23 if fmt == FP4 else 2.0 ** -12) + np.abs(want) * 2.0 ** -8 + 2.0 ** -126
+        assert (np.abs(got - want) <= bound).all(), (xs[0, 0], ws[0, 0], (np.abs(got - want) / bound).max())
