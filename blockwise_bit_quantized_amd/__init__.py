@@ -415,3 +415,12 @@ from .ops import (  # noqa: E402,F401
     logprobs, mnb_logprobs, mnb_logprobs_workspace_bytes, mnb_mx_dequantize, mnb_mx_describe_route, mnb_mx_matmul,
     mnb_mx_pack, mnb_mx_packed_sizes, mnb_mx_quantize, mnb_ops_version, mnb_rmsnorm,
     mx_dequantize, mx_matmul, mx_pack, mx_quantize, mx_tensor, rmsnorm)
+
+# The operators of a decoding step (include/mnb_decode.h)
+from . import decode as _decode  # noqa: E402
+
+_decode._bind(lib)
+from .decode import (  # noqa: E402,F401
+    KvCache, kv_append, kv_attention, kv_cache, kv_read, mnb_decode_version, mnb_kv_append, mnb_kv_attention,
+    mnb_kv_attention_workspace_bytes, mnb_kv_cache, mnb_kv_describe_route, mnb_kv_page_bytes, mnb_kv_read, mnb_kv_rows,
+    mnb_sample, rope_table, sample)

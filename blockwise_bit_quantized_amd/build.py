@@ -26,7 +26,8 @@ BINDING_LIB = os.path.join(PKG, "_mnb_ops" + (sysconfig.get_config_var("EXT_SUFF
 BINDING_SOURCE = "binding.cpp"
 OBJ = os.path.join(PKG, "_build")
 SOURCES = ["api.hip", "gemv.hip", "gemv_mfma.hip", "gemv_acc4.hip", "tproj.hip", "gemm.hip", "pack.hip",
-           "api_ops.hip", "mx_quant.hip", "mx_gemv.hip", "mx_gemm.hip", "rmsnorm.hip", "logprobs.hip"]
+           "api_ops.hip", "mx_quant.hip", "mx_gemv.hip", "mx_gemm.hip", "rmsnorm.hip", "logprobs.hip",
+           "api_decode.hip", "kv_append.hip", "kv_attention.hip", "sample.hip"]
 ARCH = os.environ.get("MNB_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

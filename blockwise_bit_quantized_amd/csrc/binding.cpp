@@ -1,10 +1,10 @@
-// binding.cpp -- the host side of the torch binding of include/mnb_ops.h (module _mnb_ops): checks
-// of arguments, output and scratch allocation, and the C call, in one native call.
+// binding.cpp -- the host side of the torch binding of include/mnb_ops.h and include/mnb_decode.h (module
+// _mnb_ops): checks of arguments, output and scratch allocation, and the C call, in one native call.
 //
 // A single-token call is bound by the host: a launch takes about 3.2 us, and the same
 // steps in Python (attribute reads, allocations, ctypes) took 4 to 10 us on top of it where
 // these take 2 to 3.  The module holds no state but the addresses of the C functions, which
-// `bind` receives once; every function takes the stream handle first.  Forward only.
+// `bind` and `bind_decode` receive once; every function takes the stream handle first.  Forward only.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -14,11 +14,12 @@
 #include <torch/csrc/DynamicTypes.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <string>
 
-#include "mnb_ops.h"
+#include "mnb_decode.h"
 
 namespace {
 
@@ -31,6 +32,13 @@ struct {
   decltype(&mnb_logprobs_workspace_bytes) logprobs_ws;
   decltype(&mnb_status_string) status_string;
 } c;
+struct {
+  decltype(&mnb_kv_append) append;
+  decltype(&mnb_kv_read) read;
+  decltype(&mnb_kv_attention) attention;
+  decltype(&mnb_kv_attention_workspace_bytes) attention_ws;
+  decltype(&mnb_sample) sample;
+} d;
 
 // A Python exception on its way out of a check.
 struct Raised {};
@@ -286,10 +294,227 @@ PyObject *logprobs(PyObject *const *a) {
   return Py_BuildValue("NNNN", wrap(lp), wrap(ent), wrap(tl), wrap(tt));
 }
 
+// ---- include/mnb_decode.h -----------------------------------------------------------------------
+
+// cache: a[0..3] data, kv_heads, head_dim, page_size (its data checked where the cache was made)
+struct Cache {
+  at::Tensor data;
+  mnb_kv_cache c{};
+  explicit Cache(PyObject *const *a) : data(tensor(a[0], "the cache's data")) {
+    if (data.scalar_type() != at::kByte) fail(PyExc_TypeError, "the cache's data must be uint8");
+    const int64_t stride = row_distance(data, "the cache's data");
+    c.data = data.data_ptr();
+    c.pages = size(data.size(0));
+    c.kv_heads = size(integer(a[1]));
+    c.head_dim = size(integer(a[2]));
+    c.page_size = size(integer(a[3]));
+    c.page_stride = stride;
+  }
+};
+// rows: a[0..2] pages, lengths, starts or None
+struct Rows {
+  at::Tensor pages, lengths, starts;
+  mnb_kv_rows r{};
+  Rows(PyObject *const *a, int64_t rows, at::Device dev)
+      : pages(tensor(a[0], "pages")), lengths(tensor(a[1], "lengths")), starts(maybe_tensor(a[2], "starts")) {
+    if (pages.scalar_type() != at::kInt) fail(PyExc_TypeError, "pages must be int32, got %s", at::toString(pages.scalar_type()));
+    r.ldp = row_distance(pages, "pages");
+    if (pages.device() != dev)
+      fail(PyExc_ValueError, "pages is on %s, expected %s", pages.device().str().c_str(), dev.str().c_str());
+    const int64_t batch = pages.size(0);
+    vector(lengths, "lengths", at::kInt, batch, dev);
+    if (starts.defined()) vector(starts, "starts", at::kInt, batch + 1, dev);
+    else if (rows != batch)
+      fail(PyExc_ValueError, "without starts every sequence has one row: %lld rows, %lld sequences", (long long)rows, (long long)batch);
+    r.pages = static_cast<const int32_t *>(data(pages));
+    r.lengths = static_cast<const int32_t *>(data(lengths));
+    r.starts = static_cast<const int32_t *>(data(starts));
+    r.batch = size(batch);
+    r.width = size(pages.size(1));
+    r.rows = size(rows);
+  }
+};
+
+// The row distance of [rows, heads, head_dim] whose heads lie side by side.
+int64_t heads_distance(const at::Tensor &t, const char *name, int64_t rows, int64_t heads, int64_t D) {
+  if (t.dim() != 3 || (rows >= 0 && t.size(0) != rows) || (heads >= 0 && t.size(1) != heads) || t.size(2) != D)
+    fail(PyExc_ValueError, "%s has shape %s, expected [%s, %s, %lld]", name, shape_of(t).c_str(), rows < 0 ? "rows" : std::to_string(rows).c_str(),
+         heads < 0 ? "heads" : std::to_string(heads).c_str(), (long long)D);
+  const int64_t n = t.size(0), h = t.size(1);
+  if (t.stride(2) != 1 || (h > 1 && t.stride(1) != D)) fail(PyExc_ValueError, "the heads of %s must lie side by side", name);
+  if (n <= 1) return h * D ? h * D : 1;
+  if (t.stride(0) < h * D) fail(PyExc_ValueError, "the rows of %s must not overlap", name);
+  return t.stride(0);
+}
+int64_t heads_beside(const at::Tensor &t, const char *name, at::ScalarType type, int64_t rows, int64_t heads, int64_t D, at::Device dev) {
+  if (t.scalar_type() != type)
+    fail(PyExc_TypeError, "%s must be %s, got %s", name, at::toString(type), at::toString(t.scalar_type()));
+  if (t.device() != dev)
+    fail(PyExc_ValueError, "%s is on %s, expected %s", name, t.device().str().c_str(), dev.str().c_str());
+  return heads_distance(t, name, rows, heads, D);
+}
+
+// kv_append(stream, k, q or None, v, cache x 4, pages, lengths, starts, table, q_weight, k_weight, eps, interleaved, out) -> q
+PyObject *kv_append(PyObject *const *a) {
+  const at::Tensor k = tensor(a[1], "k"), q = maybe_tensor(a[2], "q"), v = tensor(a[3], "v"), table = maybe_tensor(a[11], "rope"),
+                   qw = maybe_tensor(a[12], "q_weight"), kw = maybe_tensor(a[13], "k_weight");
+  at::Tensor y = maybe_tensor(a[16], "out");
+  const Cache cache(a + 4);
+  const int D = cache.c.head_dim;
+  const int code = float_type(k, "k", false);
+  const at::ScalarType type = k.scalar_type();
+  const at::Device dev = k.device();
+  const int64_t ldk = heads_distance(k, "k", -1, cache.c.kv_heads, D), rows = k.size(0);
+  const int64_t ldv = heads_beside(v, "v", type, rows, cache.c.kv_heads, D, dev);
+  int64_t ldq = 0, ldo = 0, heads = 0;
+  if (q.defined()) {
+    ldq = heads_beside(q, "q", type, rows, -1, D, dev);
+    heads = q.size(1);
+    if (y.defined()) ldo = heads_beside(y, "out", type, rows, heads, D, dev);
+    else {
+      y = empty({rows, heads, D}, q, type);
+      ldo = heads * D;
+    }
+  } else if (y.defined()) {
+    fail(PyExc_ValueError, "out needs q");
+  }
+  if (cache.data.device() != dev)
+    fail(PyExc_ValueError, "the cache is on %s, expected %s", cache.data.device().str().c_str(), dev.str().c_str());
+  const Rows r(a + 8, rows, dev);
+  int64_t rot = 0, table_rows = 0;
+  if (table.defined()) {
+    if (table.scalar_type() != at::kFloat) fail(PyExc_TypeError, "rope must be float32, got %s", at::toString(table.scalar_type()));
+    if (table.dim() != 2 || !table.is_contiguous() || table.device() != dev)
+      fail(PyExc_ValueError, "rope must be a contiguous [positions, rotated elements] on %s", dev.str().c_str());
+    table_rows = table.size(0);
+    rot = table.size(1);
+    if (rot % 16 || rot > D) fail(PyExc_ValueError, "rope must have a multiple of 16 and at most %d columns, got %lld", D, (long long)rot);
+  }
+  if (qw.defined()) vector(qw, "q_weight", type, D, dev);
+  if (kw.defined()) vector(kw, "k_weight", type, D, dev);
+  const double eps = PyFloat_AsDouble(a[14]);
+  if (eps == -1.0 && PyErr_Occurred()) throw Raised();
+  const bool interleaved = truth(a[15]);
+  on_gpu(k);
+  check(d.append(&cache.c, &r.r, data(q), ldq, size(heads), data(k), ldk, data(v), ldv, code, static_cast<const float *>(data(table)),
+                 size(table_rows), size(rot), interleaved, data(qw), data(kw), (float)eps, data(y), ldo, pointer(a[0])));
+  written(cache.data);
+  if (a[16] != Py_None) written(y);
+  return wrap(y);
+}
+
+// kv_read(stream, data, kv_heads, head_dim, page_size, pages, lengths, starts, rows, dtype, k or None, v or None) -> (k, v)
+PyObject *kv_read(PyObject *const *a) {
+  const Cache cache(a + 1);
+  const at::Device dev = cache.data.device();
+  const int64_t rows = integer(a[8]), heads = cache.c.kv_heads, D = cache.c.head_dim;
+  if (rows < 0) fail(PyExc_ValueError, "rows must not be negative, got %lld", (long long)rows);
+  if (!THPDtype_Check(a[9])) fail(PyExc_TypeError, "dtype must be a torch dtype");
+  const at::ScalarType type = reinterpret_cast<THPDtype *>(a[9])->scalar_type;
+  if (type_code(type) < 0) fail(PyExc_TypeError, "the output must be float16, bfloat16 or float32");
+  const Rows r(a + 5, rows, dev);
+  at::Tensor out[2] = {maybe_tensor(a[10], "out"), maybe_tensor(a[11], "out")};
+  int64_t ld[2];
+  for (int i = 0; i < 2; ++i) {
+    if (out[i].defined()) ld[i] = heads_beside(out[i], "out", type, rows, heads, D, dev);
+    else {
+      out[i] = empty({rows, heads, D}, cache.data, type);
+      ld[i] = heads * D ? heads * D : 1;
+    }
+  }
+  on_gpu(cache.data);
+  check(d.read(&cache.c, &r.r, data(out[0]), ld[0], data(out[1]), ld[1], type_code(type), pointer(a[0])));
+  for (int i = 0; i < 2; ++i)
+    if (a[10 + i] != Py_None) written(out[i]);
+  return Py_BuildValue("NN", wrap(out[0]), wrap(out[1]));
+}
+
+// kv_attention(stream, q, cache x 4, pages, lengths, starts, scale or None, window, out) -> y
+PyObject *kv_attention(PyObject *const *a) {
+  const at::Tensor q = tensor(a[1], "q");
+  at::Tensor y = maybe_tensor(a[11], "out"), ws;
+  const Cache cache(a + 2);
+  const int D = cache.c.head_dim;
+  const int code = float_type(q, "q", false);
+  const at::Device dev = q.device();
+  const int64_t ldq = heads_distance(q, "q", -1, -1, D), rows = q.size(0), heads = q.size(1);
+  if (cache.data.device() != dev)
+    fail(PyExc_ValueError, "the cache is on %s, expected %s", cache.data.device().str().c_str(), dev.str().c_str());
+  if (cache.c.kv_heads == 0 || heads % cache.c.kv_heads)
+    fail(PyExc_ValueError, "%lld query heads are no multiple of %d key/value heads", (long long)heads, cache.c.kv_heads);
+  const Rows r(a + 6, rows, dev);
+  double scale = 1.0 / std::sqrt((double)D);
+  if (a[9] != Py_None) {
+    scale = PyFloat_AsDouble(a[9]);
+    if (scale == -1.0 && PyErr_Occurred()) throw Raised();
+  }
+  const int64_t window = integer(a[10]);
+  if (window < 0) fail(PyExc_ValueError, "window must not be negative, got %lld", (long long)window);
+  int64_t ldy = heads * D;
+  if (y.defined()) ldy = heads_beside(y, "out", q.scalar_type(), rows, heads, D, dev);
+  else y = empty({rows, heads, D}, q, q.scalar_type());
+  on_gpu(q);
+  const int w = window > INT32_MAX ? INT32_MAX : (int)window;
+  const size_t need = d.attention_ws(&cache.c, &r.r, size(heads), w);
+  if (need) ws = empty({(int64_t)need}, q, at::kByte);
+  check(d.attention(&cache.c, &r.r, data(q), ldq, size(heads), code, (float)scale, w, data(y), ldy, data(ws), need, pointer(a[0])));
+  if (a[11] != Py_None) written(y);
+  return wrap(y);
+}
+
+// a parameter of sampling: a tensor [M], or a number for all rows
+struct Parameter {
+  at::Tensor t;
+  double number = 0;
+  Parameter(PyObject *o, const char *name, at::ScalarType type, int64_t M, at::Device dev) {
+    if (THPVariable_Check(o)) {
+      t = THPVariable_Unpack(o);
+      vector(t, name, type, M, dev);
+      return;
+    }
+    if (type == at::kInt) {
+      const int64_t v = integer(o);
+      number = (double)(v > INT32_MAX ? INT32_MAX : v < 0 ? 0 : v);
+    } else {
+      number = PyFloat_AsDouble(o);
+      if (number == -1.0 && PyErr_Occurred()) throw Raised();
+    }
+  }
+};
+
+// sample(stream, logits, u, temperature, top_k, top_p, min_p, out) -> tokens
+PyObject *sample(PyObject *const *a) {
+  const at::Tensor x = tensor(a[1], "logits"), u = tensor(a[2], "u");
+  at::Tensor y = maybe_tensor(a[7], "out");
+  const int code = float_type(x, "logits", true);
+  const int64_t ldl = row_distance(x, "logits"), M = x.size(0), V = x.size(1);
+  const at::Device dev = x.device();
+  vector(u, "u", at::kFloat, M, dev);
+  const Parameter temperature(a[3], "temperature", at::kFloat, M, dev), top_k(a[4], "top_k", at::kInt, M, dev),
+      top_p(a[5], "top_p", at::kFloat, M, dev), min_p(a[6], "min_p", at::kFloat, M, dev);
+  if (V == 0 && M > 0) fail(PyExc_ValueError, "logits have no columns");
+  if (y.defined()) vector(y, "out", at::kLong, M, dev);
+  else y = empty({M}, x, at::kLong);
+  on_gpu(x);
+  check(d.sample(data(x), code, size(M), size(V), ldl, static_cast<const float *>(data(u)), static_cast<const float *>(data(temperature.t)),
+                 (float)temperature.number, static_cast<const int32_t *>(data(top_k.t)), (int)top_k.number,
+                 static_cast<const float *>(data(top_p.t)), (float)top_p.number, static_cast<const float *>(data(min_p.t)),
+                 (float)min_p.number, static_cast<int64_t *>(data(y)), pointer(a[0])));
+  if (a[7] != Py_None) written(y);
+  return wrap(y);
+}
+
 // bind(address, ...): the C functions in the order of `c`
 PyObject *bind(PyObject *const *a) {
   void **to = reinterpret_cast<void **>(&c);
   for (int i = 0; i < 7; ++i) to[i] = pointer(a[i]);
+  Py_RETURN_NONE;
+}
+
+// bind_decode(address, ...): in the order of `d`
+PyObject *bind_decode(PyObject *const *a) {
+  void **to = reinterpret_cast<void **>(&d);
+  for (int i = 0; i < 5; ++i) to[i] = pointer(a[i]);
   Py_RETURN_NONE;
 }
 
@@ -320,6 +545,11 @@ PyMethodDef methods[] = {method<bind, 7>("bind"),
                          method<matmul, 15>("matmul"),
                          method<rmsnorm, 9>("rmsnorm"),
                          method<logprobs, 4>("logprobs"),
+                         method<bind_decode, 5>("bind_decode"),
+                         method<kv_append, 17>("kv_append"),
+                         method<kv_read, 12>("kv_read"),
+                         method<kv_attention, 12>("kv_attention"),
+                         method<sample, 8>("sample"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mnb_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,563 @@
+// kv_attention.hip -- attention over the paged FP4 cache, for rows that are few for each sequence.
+//
+// y = softmax(scale q K^T) V over the tokens a row sees.  A tile is 16 rows: the query heads that
+// share a key/value head, of one token or of several.  A wave takes 32 tokens a step:
+//   S^T [32 tokens x 16 rows] = K Q^T, two matrix instructions of 16 x 16 x 32 for each 32 elements.  The
+//     sum over the head may run in any order that K and Q share, so lane (g, r) takes a fourth of
+//     token r's row in one load.
+//   p = 2^(S' - base), base the largest score seen, raised only when a score passes it by 2^8: scores
+//     within that cost no exchange between lanes and no rescaling.  The sums are FP32.
+//   O^T [D x 16 rows] += V^T P^T: the lane that holds the scores of 8 tokens holds the same 8 tokens'
+//     probabilities as the instruction's operand, and the cache's value layout gives the lane the
+//     same elements of these 8 tokens, so neither passes through LDS.
+// FP4 codes become 16-bit numbers by the conversion instruction that applies the block's scale.
+//
+// Items (sequence, tile of rows, head) are cut in steps of 32 tokens, laid end to end and shared out evenly, so
+// a long sequence among short ones does not keep one workgroup; a workgroup's first and last item
+// may be parts, which a second kernel joins in their order.
+#include <type_traits>
+
+#include "decode.h"
+
+namespace mnb {
+namespace {
+
+constexpr int kStep = 32;      // tokens of a wave's step
+constexpr int kWaves = 4;
+
+typedef __bf16 b8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 hh_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bb_t __attribute__((ext_vector_type(2)));
+
+template <int DT>
+__device__ __forceinline__ f4_t mfma16(u4_t a, u4_t b, f4_t c) {
+  if constexpr (DT == DT_F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8_t, a), __builtin_bit_cast(h8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8_t, a), __builtin_bit_cast(b8_t, b), c, 0, 0, 0);
+}
+// byte B of w as two 16-bit numbers, times the power of two in the exponent field of `s`
+template <int DT, int B>
+__device__ __forceinline__ uint32_t expand2(uint32_t w, uint32_t s) {
+  const float f = __builtin_bit_cast(float, s);
+  if constexpr (DT == DT_F16) return __builtin_bit_cast(uint32_t, (hh_t)__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, f, B));
+  else return __builtin_bit_cast(uint32_t, (bb_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, B));
+}
+template <int DT>
+__device__ __forceinline__ u4_t expand8(uint32_t w, uint32_t s) {
+  return u4_t{expand2<DT, 0>(w, s), expand2<DT, 1>(w, s), expand2<DT, 2>(w, s), expand2<DT, 3>(w, s)};
+}
+// scale byte I of w in the exponent field (the conversion reads nothing else of it)
+template <int I>
+__device__ __forceinline__ uint32_t scale_of(uint32_t w) {
+  return I < 3 ? w << (23 - 8 * I) : w >> 1;
+}
+
+// The value operand's parts: 16 lanes share 128, 64 or 32 elements, 8, 4 or 2 each; lane r of part k has the
+// elements d0 + 8 word + (first nibble) + j of unit `word`.
+template <int D> struct Parts {
+  static constexpr int n8 = D / 128, n4 = D % 128 / 64, n2 = D % 64 / 32, count = n8 + n4 + n2, tiles = D / 16;
+  static constexpr int nib(int k) { return k < n8 ? 8 : k < n8 + n4 ? 4 : 2; }
+  static constexpr int d0(int k) { return k < n8 ? 128 * k : k < n8 + n4 ? 128 * n8 : 128 * n8 + 64 * n4; }
+  static constexpr int tile0(int k) { return d0(k) / 16; }
+  __device__ static __forceinline__ int word(int k, int r) { return d0(k) / 8 + (nib(k) == 8 ? r : nib(k) == 4 ? r & 7 : r & 3); }
+  __device__ static __forceinline__ int shift(int k, int r) { return nib(k) == 8 ? 0 : nib(k) == 4 ? 16 * (r >> 3) : 8 * (r >> 2); }
+  // first of the elements that row r of the tiles of part k holds (r = 4 g + i in a result)
+  __device__ static __forceinline__ int first(int k, int r) { return 8 * word(k, r) + shift(k, r) / 4; }
+};
+
+// largest of the four lanes of a row
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+template <int DT, int D>
+struct Tile {
+  typedef Parts<D> P;
+  static constexpr int KS = D / 32;                       // matrix instructions along the head
+  static constexpr float kOff = DT == DT_F16 ? 6.f : 0.f; // fp16 keeps small probabilities by 2^6
+  static constexpr uint32_t kFar = DT == DT_F16 ? 141 : 253;   // first scale whose values may pass q's type
+  u4_t q[KS];
+  f4_t o[P::tiles];
+  float base, sum;         // base: what scores are taken against; the sum of this lane's probabilities
+  int pos, lo;             // the row sees tokens lo .. pos
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < P::tiles; ++j) o[j] = f4_t{0.f, 0.f, 0.f, 0.f};
+    base = -__builtin_inff();
+    sum = 0.f;
+  }
+
+  // O^T += V^T P^T for 32 tokens; with `only`, rows that do not see the token keep theirs
+  template <bool ONLY>
+  __device__ __forceinline__ void values(const u4_t *va, const u4_t *vb, const uint32_t *sa, const uint32_t *sb, u4_t prob, int r,
+                                         bool sees) {
+#pragma unroll
+    for (int k = 0; k < P::count; ++k) {
+      const int sh = P::shift(k, r);
+      uint32_t a[4], b[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        a[t] = P::nib(k) == 8 ? va[k][t] : va[k][t] >> sh;
+        b[t] = P::nib(k) == 8 ? vb[k][t] : vb[k][t] >> sh;
+      }
+      auto pair = [&](auto byte) {
+        constexpr int B = decltype(byte)::value;
+        const uint32_t a0 = expand2<DT, B>(a[0], scale_of<0>(sa[k])), a1 = expand2<DT, B>(a[1], scale_of<1>(sa[k]));
+        const uint32_t a2 = expand2<DT, B>(a[2], scale_of<2>(sa[k])), a3 = expand2<DT, B>(a[3], scale_of<3>(sa[k]));
+        const uint32_t b0 = expand2<DT, B>(b[0], scale_of<0>(sb[k])), b1 = expand2<DT, B>(b[1], scale_of<1>(sb[k]));
+        const uint32_t b2 = expand2<DT, B>(b[2], scale_of<2>(sb[k])), b3 = expand2<DT, B>(b[3], scale_of<3>(sb[k]));
+        constexpr uint32_t L = 0x05040100u, H = 0x07060302u;
+        const u4_t lo4 = {__builtin_amdgcn_perm(a1, a0, L), __builtin_amdgcn_perm(a3, a2, L), __builtin_amdgcn_perm(b1, b0, L),
+                          __builtin_amdgcn_perm(b3, b2, L)};
+        const u4_t hi4 = {__builtin_amdgcn_perm(a1, a0, H), __builtin_amdgcn_perm(a3, a2, H), __builtin_amdgcn_perm(b1, b0, H),
+                          __builtin_amdgcn_perm(b3, b2, H)};
+        f4_t &x = o[P::tile0(k) + 2 * B], &y = o[P::tile0(k) + 2 * B + 1];
+        if constexpr (ONLY) {
+          const f4_t zero = {0.f, 0.f, 0.f, 0.f};
+          const f4_t dx = mfma16<DT>(lo4, prob, zero), dy = mfma16<DT>(hi4, prob, zero);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] += sees ? dx[i] : 0.f;
+            y[i] += sees ? dy[i] : 0.f;
+          }
+        } else {
+          x = mfma16<DT>(lo4, prob, x);
+          y = mfma16<DT>(hi4, prob, y);
+        }
+      };
+      pair(std::integral_constant<int, 0>());
+      if (P::nib(k) >= 4) pair(std::integral_constant<int, 1>());
+      if (P::nib(k) == 8) {
+        pair(std::integral_constant<int, 2>());
+        pair(std::integral_constant<int, 3>());
+      }
+    }
+  }
+
+  // 32 tokens from t0 (a multiple of 32) in the heads at ha and hb (16 tokens each, already offset to the
+  // first of them in their pages)
+  template <bool EDGE>
+  __device__ __forceinline__ void step(const uint8_t *ha, const uint8_t *hb, int ia, int ib, int S, float scale, int t0, int g, int r,
+                                       int tile_lo, int tile_hi) {
+    // keys
+    f4_t s[2];
+    const uint8_t *const head[2] = {ha, hb};
+    const int in[2] = {ia, ib};                          // token of the page
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int tok = in[h] + r;
+      uint32_t w[KS];
+      const uint32_t *src = reinterpret_cast<const uint32_t *>(head[h] + (int64_t)tok * (D / 2) + g * (D / 8));
+#pragma unroll
+      for (int i = 0; i < KS; ++i) w[i] = src[i];
+      const uint8_t *sc = head[h] + kv_key_scales(S, D) + (int64_t)tok * (D / 32);
+      s[h] = f4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        const uint32_t e = sc[(g * (D / 4) + 8 * i) / 32];
+        s[h] = mfma16<DT>(expand8<DT>(w[i], e << 23), q[i], s[h]);
+      }
+    }
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = s[i >> 2][i & 3] * scale;
+    if constexpr (EDGE) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
+        if (tok < lo || tok > pos) t[i] = -__builtin_inff();
+      }
+    }
+    float most = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+    if (__any(most > base + (kOff + 8.f))) {
+      const float now = fmaxf(base, row_max(most) - kOff);
+      const float f = now == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(base - now);
+      base = now;
+      sum *= f;
+#pragma unroll
+      for (int j = 0; j < P::tiles; ++j) o[j] *= f;
+    }
+    const float from = base == -__builtin_inff() ? 0.f : base;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      t[i] = __builtin_amdgcn_exp2f(t[i] - from);
+      sum += t[i];
+    }
+    const u4_t prob = {pack2<DT>(t[0], t[1]), pack2<DT>(t[2], t[3]), pack2<DT>(t[4], t[5]), pack2<DT>(t[6], t[7])};
+    // values
+    u4_t va[P::count], vb[P::count];
+    uint32_t sa[P::count], sb[P::count];
+#pragma unroll
+    for (int k = 0; k < P::count; ++k) {
+      const int word = P::word(k, r), ua = (ia >> 2) + g, ub = (ib >> 2) + g;
+      va[k] = *reinterpret_cast<const u4_t *>(ha + kv_value_codes(S, D) + ((int64_t)ua * (D / 8) + word) * 16);
+      vb[k] = *reinterpret_cast<const u4_t *>(hb + kv_value_codes(S, D) + ((int64_t)ub * (D / 8) + word) * 16);
+      sa[k] = *reinterpret_cast<const uint32_t *>(ha + kv_value_scales(S, D) + ((int64_t)ua * (D / 32) + word / 4) * 4);
+      sb[k] = *reinterpret_cast<const uint32_t *>(hb + kv_value_scales(S, D) + ((int64_t)ub * (D / 32) + word / 4) * 4);
+    }
+    if constexpr (!EDGE) {
+      values<false>(va, vb, sa, sb, prob, r, true);
+      return;
+    }
+    // Tokens that no row sees may hold anything: their scales become 0.  Of the others, one whose values
+    // are no numbers of q's type must not reach a row that does not see it (0 times infinity): such tokens go
+    // one at a time, into the rows that do.
+    uint32_t far = 0, keep_a = 0, keep_b = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int a = t0 + 4 * g + i, b = a + 16;
+      if (a >= tile_lo && a <= tile_hi) keep_a |= 0xffu << (8 * i);
+      if (b >= tile_lo && b <= tile_hi) keep_b |= 0xffu << (8 * i);
+    }
+    uint32_t na[P::count], nb[P::count];                 // without the far ones
+#pragma unroll
+    for (int k = 0; k < P::count; ++k) {
+      sa[k] &= keep_a;
+      sb[k] &= keep_b;
+      uint32_t fa = 0, fb = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if ((sa[k] >> (8 * i) & 255) >= kFar) fa |= 0xffu << (8 * i);
+        if ((sb[k] >> (8 * i) & 255) >= kFar) fb |= 0xffu << (8 * i);
+      }
+      na[k] = sa[k] & ~fa;
+      nb[k] = sb[k] & ~fb;
+      far |= fa | fb;
+    }
+    values<false>(va, vb, na, nb, prob, r, true);
+    if (__any(far != 0)) {
+      for (int x = 0; x < 32; ++x) {                     // token t0 + x: lanes of group (x & 15) / 4, place x & 3
+        const bool mine = (x & 15) >> 2 == g;
+        const uint32_t byte = mine ? 0xffu << (8 * (x & 3)) : 0;
+        uint32_t oa[P::count], ob[P::count];
+#pragma unroll
+        for (int k = 0; k < P::count; ++k) {
+          oa[k] = x < 16 ? sa[k] & ~na[k] & byte : 0;
+          ob[k] = x < 16 ? 0 : sb[k] & ~nb[k] & byte;
+        }
+        uint32_t any = 0;
+#pragma unroll
+        for (int k = 0; k < P::count; ++k) any |= oa[k] | ob[k];
+        if (!__any(any != 0)) continue;
+        // probabilities of this token alone
+        const uint32_t half = 0xffffu << (16 * (x & 1));
+        u4_t one = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (mine && w == (x >> 4) * 2 + ((x & 3) >> 1)) one[w] = prob[w] & half;
+        values<true>(va, vb, oa, ob, one, r, t0 + x >= lo && t0 + x <= pos);
+      }
+    }
+  }
+};
+
+// How a sequence's work is cut: its tiles of 16 rows, and the tokens that any of its rows sees.
+struct Cut {
+  KvSeq seq;
+  int tiles, from, steps;      // from: a multiple of kStep
+  bool beyond;                 // more tokens than the pages hold: its rows become NaN
+};
+__device__ __forceinline__ Cut cut_of(const KvAttnParams &p, int b) {
+  Cut c;
+  c.seq = kv_seq(p.rows, b);
+  c.tiles = (int)(((int64_t)c.seq.n * p.G + 15) / 16);
+  const int lo = p.window ? max(0, c.seq.first() - p.window + 1) : 0;
+  c.from = lo / kStep * kStep;
+  c.beyond = c.seq.len > p.rows.width << p.cache.shift;
+  // a row that sees nothing is written too
+  c.steps = c.beyond ? 1 : max(1, (c.seq.len - c.from + kStep - 1) / kStep);
+  return c;
+}
+__device__ __forceinline__ int64_t cost_of(const KvAttnParams &p, int b) {
+  if (b >= p.rows.batch) return 0;
+  const Cut c = cut_of(p, b);
+  return (int64_t)c.tiles * p.cache.heads * (p.whole ? 1 : c.steps);
+}
+
+// sums over the workgroup: inclusive over its threads, and of all
+template <int WAVES>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t &total) {
+  __shared__ int64_t part[WAVES];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t o = __shfl_up((long long)v, d);
+    if (lane >= d) v += o;
+  }
+  __syncthreads();
+  if (lane == 63) part[wave] = v;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i) {
+    if (i < wave) v += part[i];
+    total += part[i];
+  }
+  return v;
+}
+// the sequence that holds place `at` of the work, and the place where it begins
+template <int WAVES>
+__device__ __forceinline__ int find_work(const KvAttnParams &p, int64_t at, int64_t &begin) {
+  __shared__ int found;
+  __shared__ int64_t found_begin;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < p.rows.batch; b0 += WAVES * 64) {
+    int64_t total;
+    const int64_t mine = cost_of(p, b0 + threadIdx.x), end = block_scan<WAVES>(mine, total) + before;
+    if (at < before + total) {
+      if (at >= end - mine && at < end) {
+        found = b0 + threadIdx.x;
+        found_begin = end - mine;
+      }
+      break;
+    }
+    before += total;
+  }
+  __syncthreads();
+  begin = found_begin;
+  const int b = found;
+  __syncthreads();
+  return b;
+}
+template <int WAVES>
+__device__ __forceinline__ int64_t whole_work(const KvAttnParams &p) {
+  int64_t sum = 0, total;
+  for (int b0 = 0; b0 < p.rows.batch; b0 += WAVES * 64) {
+    block_scan<WAVES>(cost_of(p, b0 + threadIdx.x), total);
+    sum += total;
+  }
+  return sum;
+}
+// steps of a workgroup
+__device__ __forceinline__ int64_t share_of(const KvAttnParams &p, int64_t total) {
+  if (p.whole) return 1;
+  const int64_t s = (total + p.workgroups - 1) / p.workgroups;
+  return s < 2 * kWaves ? 2 * kWaves : s;
+}
+
+template <int DT, int D>
+__global__ __launch_bounds__(kWaves * 64) void rows_kernel(KvAttnParams p) {
+  typedef Parts<D> P;
+  constexpr int kRow = D + 4;                            // FP32 of a row in LDS, off the bank period
+  __shared__ float acc[kWaves][16][kRow];
+  __shared__ float stat[kWaves][16][2];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, r = lane & 15;
+  const int S = 1 << p.cache.shift;
+  const int64_t total = whole_work<kWaves>(p), share = share_of(p, total);
+  int64_t at = (int64_t)blockIdx.x * share;
+  if (at >= total) return;
+  const int64_t end = at + share < total ? at + share : total;
+  int64_t begin;
+  int b = find_work<kWaves>(p, at, begin);
+  bool first_item = true;
+  while (at < end) {
+    const Cut c = cut_of(p, b);
+    const int64_t span = p.whole ? 1 : c.steps, mine = span * c.tiles * p.cache.heads;
+    if (at >= begin + mine) {                            // on to the next sequence
+      begin += mine;
+      ++b;
+      continue;
+    }
+    const int64_t item = (at - begin) / span, item0 = begin + item * span, stop = item0 + span < end ? item0 + span : end;
+    const bool part = !(at == item0 && stop == item0 + span);
+    const int s0 = p.whole ? 0 : (int)(at - item0), s1 = p.whole ? c.steps : (int)(stop - item0);
+    const int h = (int)(item % p.cache.heads), tile = (int)(item / p.cache.heads);
+
+    Tile<DT, D> x;
+    x.clear();
+    const int row = tile * 16 + r, tokens = c.seq.n;     // row of the sequence: token row / G, head row % G
+    const bool real = row < (int64_t)tokens * p.G;
+    const int i = row / p.G, gh = row - i * p.G;
+    const uint16_t *q = p.q + (int64_t)(c.seq.row0 + i) * p.ldq + (int64_t)(h * p.G + gh) * D + g * (D / 4);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) x.q[k] = real ? reinterpret_cast<const u4_t *>(q)[k] : u4_t{0, 0, 0, 0};
+    x.pos = real ? c.seq.first() + i : -1;
+    x.lo = p.window ? x.pos - p.window + 1 : 0;
+    // what all rows of the tile see, and what any sees
+    const int i0 = tile * 16 / p.G, i1 = min(tokens - 1, (tile * 16 + 15) / p.G);
+    const int pos0 = c.seq.first() + i0, pos1 = c.seq.first() + i1;
+    const int any_lo = p.window ? max(0, pos0 - p.window + 1) : 0, all_lo = p.window ? max(0, pos1 - p.window + 1) : 0;
+    bool bad = c.beyond;
+    const int32_t *pages = p.rows.pages + (int64_t)b * p.rows.ldp;
+    for (int s = s0 + wave; s < s1 && !c.beyond; s += kWaves) {
+      const int t0 = c.from + s * kStep;
+      if (t0 > pos1 || t0 + kStep <= any_lo) continue;
+      const uint8_t *head[2];
+      int in[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int t = t0 + 16 * k, col = t >> p.cache.shift;
+        const bool needed = t <= pos1 && t + 15 >= any_lo;
+        int page = needed && col < p.rows.width ? pages[col] : -1;
+        if ((uint32_t)page >= (uint32_t)p.cache.pages) {
+          bad |= needed;
+          page = 0;
+        }
+        head[k] = p.cache.data + (int64_t)page * p.cache.page_stride + (int64_t)h * kv_head_bytes(S, D);
+        in[k] = t & (S - 1);
+      }
+      if (t0 >= all_lo && t0 + kStep - 1 <= pos0)
+        x.template step<false>(head[0], head[1], in[0], in[1], S, p.scale, t0, g, r, any_lo, pos1);
+      else x.template step<true>(head[0], head[1], in[0], in[1], S, p.scale, t0, g, r, any_lo, pos1);
+    }
+    // the waves' parts, in their order
+    x.sum = row_sum(x.sum);
+    if (bad) x.sum = __builtin_nanf("");
+    __syncthreads();
+    if (g == 0) {
+      stat[wave][r][0] = x.base;
+      stat[wave][r][1] = x.sum;
+    }
+    __syncthreads();
+    float most = stat[0][r][0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) most = fmaxf(most, stat[w][r][0]);
+    const float f = x.base == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(x.base - most);
+#pragma unroll
+    for (int k = 0; k < P::count; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float *to = &acc[wave][r][P::first(k, 4 * g + j)];
+#pragma unroll
+        for (int n = 0; n < P::nib(k); ++n) {
+          // a part that saw nothing adds nothing, whatever it holds
+          to[n] = x.base == -__builtin_inff() ? 0.f : x.o[P::tile0(k) + n][j] * f;
+        }
+      }
+    __syncthreads();
+    const int rows = (int)min((int64_t)16, (int64_t)tokens * p.G - tile * 16);
+    for (int e = threadIdx.x; e < rows * (D / 8); e += kWaves * 64) {
+      const int rr = e / (D / 8), d = (e - rr * (D / 8)) * 8;
+      float m = stat[0][rr][0], l = 0.f, v[8] = {};
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) m = fmaxf(m, stat[w][rr][0]);
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float bw = stat[w][rr][0], sw = stat[w][rr][1];
+        l += bw == -__builtin_inff() ? sw : sw * __builtin_amdgcn_exp2f(bw - m);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) v[n] += acc[w][rr][d + n];
+      }
+      if (part) {
+        float *to = p.part + (((int64_t)blockIdx.x * 2 + (first_item ? 0 : 1)) * p.slot_rows + rr) * (D + 4);
+        if (d == 0) {
+          to[D] = m;
+          to[D + 1] = l;
+        }
+        *reinterpret_cast<f4_t *>(to + d) = f4_t{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f4_t *>(to + d + 4) = f4_t{v[4], v[5], v[6], v[7]};
+      } else {
+        const int ri = (tile * 16 + rr) / p.G, rh = (tile * 16 + rr) - ri * p.G;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) v[n] = l == 0.f ? 0.f : v[n] * inv;
+        store8<DT>(p.y + (int64_t)(c.seq.row0 + ri) * p.ldy + (int64_t)(h * p.G + rh) * D + d, v);
+      }
+    }
+    __syncthreads();
+    at = stop;
+    first_item = false;
+  }
+}
+
+// One workgroup an item, in a grid-wide loop: the parts of items that lie in more than one workgroup's share.
+template <int DT, int D>
+__global__ __launch_bounds__(256) void join_kernel(KvAttnParams p, int64_t items) {
+  const int64_t total = whole_work<4>(p), share = share_of(p, total);
+  for (int64_t n = blockIdx.x; n < items; n += gridDim.x) {
+    // the item's sequence: items counted instead of steps
+    KvAttnParams count = p;
+    count.whole = 1;
+    if (n >= whole_work<4>(count)) return;
+    int64_t item0, begin = 0;
+    const int b = find_work<4>(count, n, item0);
+    for (int b0 = 0; b0 < b; b0 += 256) {
+      int64_t sum;
+      block_scan<4>(b0 + (int)threadIdx.x < b ? cost_of(p, b0 + threadIdx.x) : 0, sum);
+      begin += sum;
+    }
+    const Cut c = cut_of(p, b);
+    const int64_t item = n - item0, s = begin + item * c.steps, e = s + c.steps;
+    const int64_t w0 = s / share, w1 = (e - 1) / share;
+    if (w0 == w1) continue;
+    const int h = (int)(item % p.cache.heads), tile = (int)(item / p.cache.heads);
+    const int rows = (int)min((int64_t)16, (int64_t)c.seq.n * p.G - tile * 16);
+    for (int x = threadIdx.x; x < rows * (D / 4); x += 256) {
+      const int rr = x / (D / 4), d = (x - rr * (D / 4)) * 4;
+      float m = -__builtin_inff(), l = 0.f;
+      auto slot = [&](int64_t w) {
+        // the item is the workgroup's second where another began its share
+        const int second = w == w0 && s > w * share;
+        return p.part + ((w * 2 + second) * p.slot_rows + rr) * (D + 4);
+      };
+      for (int64_t w = w0; w <= w1; ++w) m = fmaxf(m, slot(w)[D]);
+      f4_t v = {0.f, 0.f, 0.f, 0.f};
+      for (int64_t w = w0; w <= w1; ++w) {
+        const float *from = slot(w), bw = from[D], sw = from[D + 1];
+        if (bw == -__builtin_inff()) {
+          l += sw;                                       // 0, or NaN where a page was out of range
+          continue;
+        }
+        const float f = __builtin_amdgcn_exp2f(bw - m);
+        l += sw * f;
+        v += *reinterpret_cast<const f4_t *>(from + d) * f;
+      }
+      const int ri = (tile * 16 + rr) / p.G, rh = (tile * 16 + rr) - ri * p.G;
+      uint16_t *y = p.y + (int64_t)(c.seq.row0 + ri) * p.ldy + (int64_t)(h * p.G + rh) * D + d;
+      if (l == 0.f) v = f4_t{0.f, 0.f, 0.f, 0.f};
+      else v *= 1.f / l;
+      *reinterpret_cast<u2_t *>(y) = u2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+    }
+    __syncthreads();
+  }
+}
+
+template <int DT, int D>
+hipError_t launch(const KvAttnParams &p, int64_t items, hipStream_t s) {
+  hipLaunchKernelGGL((rows_kernel<DT, D>), dim3((uint32_t)p.workgroups), dim3(kWaves * 64), 0, s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.whole) return e;
+  const uint32_t grid = (uint32_t)(items < 4096 ? items : 4096);
+  hipLaunchKernelGGL((join_kernel<DT, D>), dim3(grid), dim3(256), 0, s, p, items);
+  return hipGetLastError();
+}
+template <int DT>
+hipError_t by_head(const KvAttnParams &p, int64_t items, hipStream_t s) {
+  switch (p.cache.D) {
+    case 64: return launch<DT, 64>(p, items, s);
+    case 96: return launch<DT, 96>(p, items, s);
+    case 128: return launch<DT, 128>(p, items, s);
+    case 192: return launch<DT, 192>(p, items, s);
+    default: return launch<DT, 256>(p, items, s);
+  }
+}
+
+}  // namespace
+
+KvPlan kv_attn_plan(const KvCache &c, const KvRows &r, int G, int window) {
+  KvPlan k{};
+  // tiles of 16 rows: at most one short one for each sequence
+  const int64_t tiles = r.starts ? (int64_t)r.rows * G / 16 + r.batch : (int64_t)r.batch * ((G + 15) / 16);
+  k.items = tiles * c.heads;
+  int64_t tokens = (int64_t)r.width << c.shift;
+  if (window && tokens > (int64_t)window + r.rows + kStep) tokens = (int64_t)window + r.rows + kStep;
+  const int64_t steps = (tokens + kStep - 1) / kStep + 1;
+  k.slot_rows = r.starts ? 16 : G < 16 ? G : 16;
+  const int64_t most = k.items * steps / (2 * kWaves);
+  k.whole = k.items >= 4 * kCUs || steps <= 4 * kWaves;
+  k.workgroups = (int)(k.whole ? k.items : most < 4 * kCUs ? most + 1 : 4 * kCUs);
+  return k;
+}
+
+hipError_t launch_kv_attn(int dtype, const KvAttnParams &p, int64_t items, hipStream_t s) {
+  return dtype == DT_F16 ? by_head<DT_F16>(p, items, s) : by_head<DT_BF16>(p, items, s);
+}
+
+}  // namespace mnb

@@ -44,17 +44,6 @@ __device__ __forceinline__ double block_sum(double v) {
   return v;
 }
 
-// To 32 bits, inexact values to the neighbour with an odd last bit, among subnormals too: a later
-// rounding to fewer bits then gives what one rounding of v would (rounding to nearest first
-// would turn values next to an element's border into ties).
-__device__ __forceinline__ float to_odd(double v) {
-  const float f = (float)v;
-  const double g = f;
-  const uint32_t b = __builtin_bit_cast(uint32_t, f);
-  if (g == v || __builtin_isinf(f)) return f;
-  return __builtin_bit_cast(float, (fabs(g) > fabs(v) ? b - 1 : b) | 1u);
-}
-
 // a piece of 8 elements of x and of the residual (-0 without one, which leaves x as it is)
 template <int DT>
 struct Inputs {
