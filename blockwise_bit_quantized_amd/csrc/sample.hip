@@ -6,31 +6,45 @@
 // would move one in some thousand rows of a flat distribution).  The power is a polynomial in 64 bits, whose
 // instructions run at the rate of 32-bit ones here.
 //
-// A workgroup of 16 waves takes a row, thread t pieces of 8 logits t, t + 1024, ..., read again (from L2) in
+// A workgroup of 8 or 16 waves takes a row, each wave a run of it, 512 logits a round, read again (from L2) in
 // each pass.  What stays is told by one key: order bits of the number over the complement of the index.
-//   A top-k of up to kFewK takes a threshold from the maxima of 256 groups of threads (the k-th largest
+//   A top-k of up to kFewK takes a threshold from the maxima of 256 groups of lanes (the k-th largest
 //   of them is reached by at least k logits and few more); the logits above it go to LDS, and everything
 //   is settled among them by counting, for each, the larger ones.  So do rows of up to kList logits, and a min-p alone.
 //   Otherwise the border of top-k or top-p is found by histograms: of counts or weights over equal
 //   steps of the exponent (where neighbouring lanes rarely meet in one place), then over the order bits in
 //   the step that holds the border, until one number is left; of that, the first few by index stay.
-//   The token itself is the place where the running sum passes u times the whole: sums of waves, then of lanes.
+//   The token itself is the place where the running sum passes u times the whole: sums of the waves, of
+//   that wave's rounds (taken by all waves), of that round's lanes.
 #include "decode.h"
 
 namespace mnb {
 namespace {
 
-constexpr int kThreads = 1024, kSampleWaves = kThreads / 64;
 constexpr int kList = 1024;          // logits settled in LDS
 constexpr int kFewK = 180;           // about 310 of 256 groups' logits pass the 180th maximum
 constexpr int kBins = 2048;
-constexpr int kRound = kThreads * 8; // logits of a round of pieces
-constexpr int kRounds = 64;          // rounds whose sums of waves lie in LDS
+constexpr int kRound = 512;          // logits of a wave's round
+constexpr int kMostWaves = 16;
+static_assert((1 << 22) / (kRound * 8) <= kList, "the sums of a wave's rounds lie in LDS");
 
+// lane ^ 1, lane ^ 2, rotated by 4 and 8 in 16 lanes
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp64(uint64_t v) {
+  const uint32_t a = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, 0xf, 0xf, true);
+  const uint32_t b = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, 0xf, 0xf, true);
+  return (uint64_t)b << 32 | a;
+}
+__device__ __forceinline__ uint64_t lane64(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+}
 __device__ __forceinline__ uint64_t wave_sum64(uint64_t v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor((unsigned long long)v, d);
-  return v;
+  v += dpp64<0xB1>(v);
+  v += dpp64<0x4E>(v);
+  v += dpp64<0x124>(v);
+  v += dpp64<0x128>(v);
+  return (lane64(v, 0) + lane64(v, 16)) + (lane64(v, 32) + lane64(v, 48));
 }
 __device__ __forceinline__ uint64_t wave_scan64(uint64_t v) {
   const int lane = threadIdx.x & 63;
@@ -43,49 +57,64 @@ __device__ __forceinline__ uint64_t wave_scan64(uint64_t v) {
 }
 __device__ __forceinline__ float order_number(uint32_t u) { return __builtin_bit_cast(float, u & 0x80000000u ? u ^ 0x80000000u : ~u); }
 
-// 2^a for a in [-100, 0], times 2^S, before rounding: the polynomial interpolates 2^f at the 11 Chebyshev points of
-// [-1/2, 1/2] and is off by 2^-51 of its value at most.
-__device__ __forceinline__ double power(double a, int S) {
-  const double t = a + 0x1.8p52;                       // the nearest whole number in the low bits
-  const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, t);
-  const double f = a - (t - 0x1.8p52);
-  double r = 0x1.e6063f7217bc6p-28;
-  r = fma(r, f, 0x1.b675bca4eeebbp-24);
-  r = fma(r, f, 0x1.62bfd47773353p-20);
-  r = fma(r, f, 0x1.ffcb54062e698p-17);
-  r = fma(r, f, 0x1.430913096fd9fp-13);
-  r = fma(r, f, 0x1.5d87fe9d7a584p-10);
-  r = fma(r, f, 0x1.3b2ab6fba1ddap-7);
-  r = fma(r, f, 0x1.c6b08d703ce49p-5);
-  r = fma(r, f, 0x1.ebfbdff82c598p-3);
-  r = fma(r, f, 0x1.62e42fefa3a19p-1);
-  r = fma(r, f, 1.0);
-  return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, r) + ((uint64_t)(uint32_t)(n + S) << 52));
+// Numbers the compiler may not put into the instruction stream: a 64-bit literal costs two moves at each use,
+// a scalar register pair nothing.
+__device__ __forceinline__ double in_scalars(double v) {
+  asm("" : "+s"(v));
+  return v;
 }
 
+// Weights of a row in units of 2^-S, as doubles that hold whole numbers of them: sums of a thread stay exact.
 struct Scale {
-  double m, c, least;      // weights below `least` (min-p) count 0
+  double m, c, unit;       // unit: 2^(52 - S); adding it rounds to whole numbers of 2^-S
+  double p[10], magic, low;
   int S;
-  __device__ __forceinline__ double exponent(float x) const { return fmax(((double)x - m) * c, -100.0); }
-  // rounded to a whole number, as a double: sums of a thread stay exact
-  __device__ __forceinline__ double weight(float x) const {
-    const double r = power(exponent(x), S);
-    return r >= least ? (r + 0x1p52) - 0x1p52 : 0.0;
+  __device__ __forceinline__ Scale(double largest, double per, int fraction) {
+    m = largest;
+    c = per;
+    S = fraction;
+    unit = in_scalars(__builtin_bit_cast(double, (uint64_t)(1023 + 52 - fraction) << 52));
+    magic = in_scalars(0x1.8p52);
+    low = in_scalars(-100.0);
+    const double q[10] = {0x1.62e42fefa3a19p-1, 0x1.ebfbdff82c598p-3, 0x1.c6b08d703ce49p-5, 0x1.3b2ab6fba1ddap-7, 0x1.5d87fe9d7a584p-10,
+                          0x1.430913096fd9fp-13, 0x1.ffcb54062e698p-17, 0x1.62bfd47773353p-20, 0x1.b675bca4eeebbp-24, 0x1.e6063f7217bc6p-28};
+#pragma unroll
+    for (int i = 0; i < 10; ++i) p[i] = in_scalars(q[i]);
   }
+  __device__ __forceinline__ double exponent(float x) const { return fmax(((double)x - m) * c, low); }
+  // 2^a for a in [-100, 0]: the polynomial interpolates 2^f at the 11 Chebyshev points of [-1/2, 1/2] and is off
+  // by 2^-51 of its value at most
+  __device__ __forceinline__ double power(double a) const {
+    const double t = a + magic;                        // the nearest whole number in the low bits
+    const double f = a - (t - magic);
+    double r = p[9];
+#pragma unroll
+    for (int i = 8; i >= 0; --i) r = fma(r, f, p[i]);
+    r = fma(r, f, 1.0);
+    const uint64_t b = __builtin_bit_cast(uint64_t, r);
+    const u2_t w = {(uint32_t)b, (uint32_t)(b >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, t) << 20)};
+    return __builtin_bit_cast(double, w);
+  }
+  __device__ __forceinline__ double rounded(double r) const { return (r + unit) - unit; }
+  // a sum of weights below 2^(52 - S) as a whole number
+  __device__ __forceinline__ uint64_t whole(double sum) const { return __builtin_bit_cast(uint64_t, sum + unit) & ((1ull << 52) - 1); }
+  __device__ __forceinline__ double weight(float x) const { return rounded(power(exponent(x))); }
+  __device__ __forceinline__ uint64_t whole_weight(float x) const { return whole(power(exponent(x))); }
 };
 
 struct Shared {
-  uint64_t key[kList];               // also sums of waves
+  uint64_t key[kList + 8];           // also sums of a wave's rounds
   uint64_t amount[kList];
   unsigned long long hist[kBins];
-  uint64_t wave[kSampleWaves];
+  uint64_t wave[kMostWaves];
   uint64_t chosen, before;
   float group[256];
-  uint32_t bits[kSampleWaves];
+  uint32_t bits[kMostWaves];
   int count;
 };
 
 // sum over the workgroup
+template <int WAVES>
 __device__ __forceinline__ uint64_t block_sum(Shared &s, uint64_t v) {
   v = wave_sum64(v);
   __syncthreads();
@@ -93,7 +122,7 @@ __device__ __forceinline__ uint64_t block_sum(Shared &s, uint64_t v) {
   __syncthreads();
   v = 0;
 #pragma unroll
-  for (int i = 0; i < kSampleWaves; ++i) v += s.wave[i];
+  for (int i = 0; i < WAVES; ++i) v += s.wave[i];
   return v;
 }
 
@@ -108,38 +137,53 @@ template <int DT>
 struct Row {
   typedef typename Elem<DT>::type T;
   const T *x;
-  int V, rounds, off;      // the first piece begins `off` logits before the row, at a 16-byte boundary
+  int V, off;              // the first piece begins `off` logits before the row, at a 16-byte boundary
+  int rounds, mine;        // of a wave; this wave's first
 
+  const Piece<DT> *edge;   // LDS: the piece with the row's first logits and that with its last, where not whole
+
+  static constexpr uint32_t kAbsent = DT == DT_F32 ? 0xff800000u : DT == DT_F16 ? 0xfc00fc00u : 0xff80ff80u;
   // absent logits are -infinity, which weighs nothing
-  __device__ __forceinline__ Piece<DT> load(int j) const {
-    constexpr uint32_t absent = DT == DT_F32 ? 0xff800000u : DT == DT_F16 ? 0xfc00fc00u : 0xff80ff80u;
+  __device__ __forceinline__ Piece<DT> load(int j) const { return load_at(first(j)); }
+  __device__ __forceinline__ Piece<DT> load_at(int e) const {
     Piece<DT> p;
-    const int e = first(j);
-    if (e >= 0 && e + 8 <= V) {
 #pragma unroll
-      for (int h = 0; h < (DT == DT_F32 ? 2 : 1); ++h) p.v[h] = reinterpret_cast<const u4_t *>(x + e)[h];
-      return p;
-    }
+    for (int h = 0; h < (DT == DT_F32 ? 2 : 1); ++h) p.v[h] = u4_t{kAbsent, kAbsent, kAbsent, kAbsent};
+    if (e < V) {
+      const bool whole = e >= 0 && e + 8 <= V;
+      if (whole) {
 #pragma unroll
-    for (int h = 0; h < (DT == DT_F32 ? 2 : 1); ++h) p.v[h] = u4_t{absent, absent, absent, absent};
-    if (e >= V || e + 8 <= 0) return p;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (e + i < 0 || e + i >= V) continue;
-      if constexpr (DT == DT_F32) p.v[i >> 2][i & 3] = __builtin_bit_cast(uint32_t, x[e + i]);
-      else p.v[0][i >> 1] = (p.v[0][i >> 1] & (0xffffu << (16 * (1 - (i & 1))))) | (uint32_t)x[e + i] << (16 * (i & 1));
+        for (int h = 0; h < (DT == DT_F32 ? 2 : 1); ++h) p.v[h] = reinterpret_cast<const u4_t *>(x + e)[h];
+      } else {
+        p = edge[e >= 0];
+      }
     }
     return p;
   }
-  __device__ __forceinline__ int first(int j) const { return j * kRound + (int)threadIdx.x * 8 - off; }
-  // f(j, piece) for each round, the next piece on its way meanwhile
+  // threads 0..15 write an element each of the two pieces that may not be whole
+  __device__ __forceinline__ static void fill_edges(Piece<DT> *to, const T *x, int V, int off) {
+    const int t = threadIdx.x, i = t & 7;
+    if (t >= 16) return;
+    const int e = (t < 8 ? -off : (V + off) / 8 * 8 - off) + i;
+    T v;
+    if constexpr (DT == DT_F32) v = -__builtin_inff();
+    else v = (uint16_t)kAbsent;
+    if (e >= 0 && e < V) v = x[e];
+    reinterpret_cast<T *>(to + (t >> 3))[i] = v;
+  }
+  // the first logit of this lane's piece in round j of this wave, in round r of all
+  __device__ __forceinline__ int first(int j) const { return first_of(mine + j); }
+  __device__ __forceinline__ int first_of(int r) const { return r * kRound + (int)(threadIdx.x & 63) * 8 - off; }
+  // f(j, piece) for each round, three pieces on their way meanwhile
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    Piece<DT> now = load(0);
+    Piece<DT> a = load(0), b = load(1), c = load(2);
     for (int j = 0; j < rounds; ++j) {
-      const Piece<DT> next = j + 1 < rounds ? load(j + 1) : now;
-      f(j, now);
-      now = next;
+      const Piece<DT> next = load(j + 3);              // past the row: absent, without a load
+      f(j, a);
+      a = b;
+      b = c;
+      c = next;
     }
   }
 };
@@ -148,83 +192,64 @@ struct Row {
 struct Kept {
   uint32_t order = 0;
   int index = 0x7fffffff;          // of the numbers at `order`, those up to this index
-  __device__ __forceinline__ bool holds(uint32_t o, int i) const { return o > order || (o == order && i <= index); }
+  __device__ __forceinline__ bool holds(uint32_t o, int i) const { return (o > order) | ((o == order) & (i <= index)); }
 };
 
-// The first index, in order, at which the running sum of amount(x, index) passes goal(total); -1 where it never does.
-template <typename R, typename A, typename G>
-__device__ __forceinline__ int find_index(Shared &s, R &row, A amount, G goal) {
+// The first index, in order, at which the running sum passes goal(total); -1 where it never does.  amounts(piece, first
+// index, out) gives the eight amounts of a piece as doubles, whole(sum) a sum of eight as a whole number.
+template <int WAVES, typename R, typename A, typename W, typename G>
+__device__ __forceinline__ int find_index(Shared &s, const R &row, A amounts, W whole, G goal) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int per = (row.rounds + kRounds - 1) / kRounds;          // rounds of an entry: 1 but for very long rows
-  auto piece_sum = [&](int j, const auto &p) {
-    double sum = 0.0;
-    const int e = row.first(j);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += amount(piece_at(p, i), e + i);
-    return (uint64_t)sum;
+  auto piece_sum = [&](const auto &p, int e) -> uint64_t {
+    double a[8];
+    amounts(p, e, a);
+    return whole(((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7])));
   };
+  uint64_t sum = 0;
+  row.each([&](int j, const auto &p) { sum += piece_sum(p, row.first(j)); });
+  sum = wave_sum64(sum);
   __syncthreads();
-  if (per > 1) {
-    for (int i = threadIdx.x; i < kRounds * kSampleWaves; i += kThreads) s.key[i] = 0;
-    __syncthreads();
-  }
-  row.each([&](int j, const auto &p) {
-    const uint64_t sum = wave_sum64(piece_sum(j, p));
-    if (lane != 0) return;
-    if (per == 1) s.key[j * kSampleWaves + wave] = sum;
-    else atomicAdd(reinterpret_cast<unsigned long long *>(&s.key[j / per * kSampleWaves]), (unsigned long long)sum);
-  });
+  if (lane == 0) s.wave[wave] = sum;
+  if (threadIdx.x == 0) s.count = -1;
   __syncthreads();
-  // every wave scans the entries, 64 at a time, and so finds the same one
-  auto scan = [&](int n, uint64_t &target, bool &set, uint64_t &total) -> int {
-    uint64_t done = 0;
-    for (int i0 = 0; i0 < n; i0 += 64) {
-      const uint64_t v = i0 + lane < n ? s.key[i0 + lane] : 0, run = wave_scan64(v) + done;
-      if (set) {
-        const uint64_t hit = __ballot(run > target);
-        if (hit) {
-          const int at = __builtin_ctzll(hit);
-          target -= __shfl((unsigned long long)(run - v), at);
-          return i0 + at;
-        }
-      }
-      done = __shfl((unsigned long long)run, 63);
-    }
-    total = done;
-    return -1;
-  };
   uint64_t total = 0, target = 0;
-  bool set = false;
-  const int entries = per == 1 ? row.rounds * kSampleWaves : kRounds * kSampleWaves;
-  scan(entries, target, set, total);
-  if (!goal(total, target)) return -1;
-  set = true;
-  int at = scan(entries, target, set, total);
-  if (at < 0) return -1;
-  if (per > 1) {                                                  // the rounds of that entry, one sum a wave each
-    const int j0 = at / kSampleWaves * per, j1 = min(row.rounds, j0 + per);
-    __syncthreads();
-    for (int j = j0; j < j1; ++j) {
-      const uint64_t sum = wave_sum64(piece_sum(j, row.load(j)));
-      if (lane == 0) s.key[(j - j0) * kSampleWaves + wave] = sum;
-    }
-    __syncthreads();
-    at = scan((j1 - j0) * kSampleWaves, target, set, total);
-    if (at < 0) return -1;
-    at += j0 * kSampleWaves;
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i) total += s.wave[i];
+  if (!goal(total, target) || target >= total) return -1;
+  int at = 0;
+  while (target >= s.wave[at]) target -= s.wave[at++];           // ends: target is below the sum of all
+  // that wave's rounds
+  for (int j = wave; j < row.rounds; j += WAVES) {
+    const int e = row.first_of(at * row.rounds + j);
+    const uint64_t one = wave_sum64(piece_sum(row.load_at(e), e));
+    if (lane == 0) s.key[j] = one;
   }
-  const int j = at / kSampleWaves;
   __syncthreads();
-  if (wave == at % kSampleWaves) {
-    const auto p = row.load(j);
-    const uint64_t mine = piece_sum(j, p), run = wave_scan64(mine);
-    if (run > target && run - mine <= target) {
-      uint64_t left = target - (run - mine);
+  int j = 0;
+  for (int j0 = 0; j0 < row.rounds; j0 += 64) {
+    const uint64_t v = j0 + lane < row.rounds ? s.key[j0 + lane] : 0, run = wave_scan64(v);
+    const uint64_t hit = __ballot(run > target);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      target -= lane64(run - v, l);
+      j = j0 + l;
+      break;
+    }
+    target -= lane64(run, 63);
+  }
+  // that round's lanes
+  if (wave == 0) {
+    const int e = row.first_of(at * row.rounds + j);
+    const auto p = row.load_at(e);
+    const uint64_t own = piece_sum(p, e), run = wave_scan64(own);
+    if (run > target && run - own <= target) {
+      uint64_t left = target - (run - own);
       int found = -1;
-      const int e = row.first(j);
+      double each[8];
+      amounts(p, e, each);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint64_t a = (uint64_t)amount(piece_at(p, i), e + i);
+        const uint64_t a = whole(each[i]);
         if (found < 0 && a > left) found = e + i;
         left -= found < 0 ? a : 0;
       }
@@ -236,19 +261,23 @@ __device__ __forceinline__ int find_index(Shared &s, R &row, A amount, G goal) {
 }
 
 // the place of the histogram where the sum from the largest bin down (bin 0 first) reaches target: before < target <= before + it
+template <int WAVES>
 __device__ __forceinline__ int find_bin(Shared &s, uint64_t target, uint64_t &before) {
-  static_assert(kBins == 2 * kThreads, "two bins a thread");
+  constexpr int kEach = kBins / (WAVES * 64);
   __syncthreads();
-  const uint64_t a = s.hist[2 * threadIdx.x], b = s.hist[2 * threadIdx.x + 1];
-  uint64_t run = wave_scan64(a + b);
+  uint64_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) sum += s.hist[kEach * threadIdx.x + i];
+  uint64_t run = wave_scan64(sum);
   if ((threadIdx.x & 63) == 63) s.wave[threadIdx.x >> 6] = run;
   __syncthreads();
   for (int i = 0; i < (int)(threadIdx.x >> 6); ++i) run += s.wave[i];
-  const uint64_t start = run - a - b + before;
-  if (start < target && target <= start + a + b) {
-    const bool second = target > start + a;
-    s.chosen = 2 * threadIdx.x + second;
-    s.before = start + (second ? a : 0);
+  uint64_t start = run - sum + before;
+  if (start < target && target <= start + sum) {
+    int bin = kEach * threadIdx.x;
+    while (target > start + s.hist[bin]) start += s.hist[bin++];   // ends: target is at most the sum of the thread's
+    s.chosen = bin;
+    s.before = start;
   }
   __syncthreads();
   before = s.before;
@@ -257,12 +286,12 @@ __device__ __forceinline__ int find_bin(Shared &s, uint64_t target, uint64_t &be
 
 // Narrows `kept` to the shortest run of largest numbers whose amounts (1, or the weight) reach target, at most
 // what `kept` holds in all.
-template <typename R>
-__device__ __forceinline__ void narrow(Shared &s, R &row, const Scale &scale, bool weights, uint64_t target, Kept &kept) {
+template <int WAVES, typename R>
+__device__ __forceinline__ void narrow(Shared &s, const R &row, const Scale &scale, bool weights, uint64_t target, Kept &kept) {
   const double steps = (kBins - 1) / (scale.S + 2.0);   // the last bin holds what weighs nothing
   auto clear = [&] {
     __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += kThreads) s.hist[i] = 0;
+    for (int i = threadIdx.x; i < kBins; i += WAVES * 64) s.hist[i] = 0;
     __syncthreads();
   };
   auto bin_of = [&](double a) { return (int)fmin(-a * steps, (double)(kBins - 1)); };
@@ -272,16 +301,15 @@ __device__ __forceinline__ void narrow(Shared &s, R &row, const Scale &scale, bo
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float x = piece_at(p, i);
-      if (!kept.holds(number_order(x), e + i)) continue;
       const double a = scale.exponent(x);
       const int bin = bin_of(a);
-      if (bin == kBins - 1) continue;
-      atomicAdd(&s.hist[bin], weights ? (unsigned long long)((power(a, scale.S) + 0x1p52) - 0x1p52) : 1ull);
+      const unsigned long long v = weights ? (unsigned long long)scale.whole(scale.power(a)) : 1ull;
+      if (kept.holds(number_order(x), e + i) && bin != kBins - 1) atomicAdd(&s.hist[bin], v);
     }
   });
   if (threadIdx.x == 0) s.chosen = kBins;
   uint64_t before = 0;
-  const int bin = find_bin(s, target, before);
+  const int bin = find_bin<WAVES>(s, target, before);
   if (bin == kBins) return;                             // the border is among what weighs nothing: all else stays
   // in that bin: the smallest and the largest number, then a histogram over their order bits, until they are one
   uint32_t lo = 0, hi = 0xffffffffu;
@@ -306,7 +334,7 @@ __device__ __forceinline__ void narrow(Shared &s, R &row, const Scale &scale, bo
     __syncthreads();
     if ((threadIdx.x & 63) == 0) s.wave[threadIdx.x >> 6] = (uint64_t)least << 32 | most;
     __syncthreads();
-    for (int i = 0; i < kSampleWaves; ++i) {
+    for (int i = 0; i < WAVES; ++i) {
       least = min(least, (uint32_t)(s.wave[i] >> 32));
       most = max(most, (uint32_t)s.wave[i]);
     }
@@ -322,19 +350,23 @@ __device__ __forceinline__ void narrow(Shared &s, R &row, const Scale &scale, bo
         const float x = piece_at(p, i);
         const uint32_t o = number_order(x);
         if (o < lo || o > hi || !kept.holds(o, e + i)) continue;
-        atomicAdd(&s.hist[(hi - o) >> shift], weights ? (unsigned long long)((power(scale.exponent(x), scale.S) + 0x1p52) - 0x1p52) : 1ull);
+        atomicAdd(&s.hist[(hi - o) >> shift], weights ? (unsigned long long)scale.whole_weight(x) : 1ull);
       }
     });
-    const uint32_t b = (uint32_t)find_bin(s, target, before);
+    const uint32_t b = (uint32_t)find_bin<WAVES>(s, target, before);
     const uint32_t top = hi - (b << shift);
     lo = max(lo, top - (uint32_t)min((uint64_t)top, (1ull << shift) - 1));
     hi = top;
   }
   // of the numbers at the border, as many as are missing
-  const uint64_t one = weights ? (uint64_t)((power(scale.exponent(order_number(lo)), scale.S) + 0x1p52) - 0x1p52) : 1;
+  const uint64_t one = weights ? scale.whole_weight(order_number(lo)) : 1;
   const uint64_t need = (target - before + one - 1) / one;
   const int old = kept.order == lo ? kept.index : 0x7fffffff;
-  const int at = find_index(s, row, [&](float x, int i) { return i >= 0 && i < row.V && number_order(x) == lo ? 1.0 : 0.0; },
+  const int at = find_index<WAVES>(s, row, [&](const auto &q, int e, double *a) {
+#pragma unroll
+                              for (int i = 0; i < 8; ++i) a[i] = e + i >= 0 && e + i < row.V && number_order(piece_at(q, i)) == lo ? 1.0 : 0.0;
+                            },
+                            [](double sum) { return (uint64_t)sum; },
                             [&](uint64_t total, uint64_t &goal) { goal = need - 1; return need < total; });
   kept.order = lo;
   kept.index = at < 0 ? old : min(at, old);
@@ -348,46 +380,104 @@ __device__ __forceinline__ uint64_t goal_of(float u, uint64_t all) {
 }
 
 // The row's token from the n logits of s.key, all that may stay: for each, sums over the larger ones and over those before it.
+template <int WAVES>
 __device__ __forceinline__ void settle(Shared &s, int n, const Scale &scale, int top_k, float top_p, double least, float u, int64_t *token) {
+  constexpr int kEach = kList / (WAVES * 64);
+  uint64_t key[kEach], w[kEach], before[kEach] = {};
+  double r[kEach];
+  int rank[kEach] = {};
+  bool stays[kEach];
   const int t = threadIdx.x;
-  const bool on = t < n;
-  const uint64_t key = on ? s.key[t] : 0;
-  const double r = on ? power(scale.exponent(order_number((uint32_t)(key >> 32))), scale.S) : 0.0;
-  uint64_t w = (uint64_t)((r + 0x1p52) - 0x1p52);
-  if (on) s.amount[t] = w;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int a = t + k * WAVES * 64;
+    key[k] = a < n ? s.key[a] : 0;
+    r[k] = a < n ? scale.power(scale.exponent(order_number((uint32_t)(key[k] >> 32)))) : 0.0;
+    w[k] = scale.whole(r[k]);
+    if (a < n) s.amount[a] = w[k];
+  }
   __syncthreads();
-  int rank = 0;
-  uint64_t before = 0;
-  if (on) {
+  uint64_t sum = 0;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    if (t + k * WAVES * 64 >= n) {
+      stays[k] = false;
+      continue;
+    }
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
-      const bool larger = s.key[i] > key;
-      rank += larger;
-      before += larger ? s.amount[i] : 0;
+      const bool larger = s.key[i] > key[k];
+      rank[k] += larger;
+      before[k] += larger ? s.amount[i] : 0;
     }
+    stays[k] = top_k <= 0 || rank[k] < top_k;
+    sum += stays[k] ? w[k] : 0;
   }
-  bool stays = on && (top_k <= 0 || rank < top_k);
   if (top_p < 1.f) {
-    const uint64_t all = block_sum(s, stays ? w : 0);
-    const double want = ceil((double)top_p * (double)all);
-    stays = stays && (rank == 0 || (want >= 1.0 && before < (uint64_t)want));
+    const double want = ceil((double)top_p * (double)block_sum<WAVES>(s, sum));
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) stays[k] = stays[k] && (rank[k] == 0 || (want >= 1.0 && before[k] < (uint64_t)want));
   }
-  stays = stays && (rank == 0 || r >= least);
-  w = stays ? w : 0;
-  const uint64_t goal = goal_of(u, block_sum(s, w));              // its barriers also end the reads of s.amount
-  if (on) s.amount[t] = w;
+  sum = 0;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    stays[k] = stays[k] && (rank[k] == 0 || r[k] >= least);
+    w[k] = stays[k] ? w[k] : 0;
+    sum += w[k];
+  }
+  const uint64_t goal = goal_of(u, block_sum<WAVES>(s, sum));     // its barriers also end the reads of s.amount
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    if (t + k * WAVES * 64 < n) s.amount[t + k * WAVES * 64] = w[k];
   __syncthreads();
-  if (w == 0) return;
-  uint64_t run = 0;                                               // of those up to this one: larger complements first
-  const uint32_t mine = (uint32_t)key;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    if (w[k] == 0) continue;
+    uint64_t run = 0;                                             // of those up to this one: larger complements first
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) run += (uint32_t)s.key[i] >= mine ? s.amount[i] : 0;
-  if (run > goal && run - w <= goal) *token = (int64_t)(uint32_t)~mine;
+    for (int i = 0; i < n; ++i) run += (uint32_t)s.key[i] >= (uint32_t)key[k] ? s.amount[i] : 0;
+    if (run > goal && run - w[k] <= goal) *token = (int64_t)(uint32_t)~(uint32_t)key[k];
+  }
 }
 
+// largest number and largest magnitude's bits (past infinity's for a NaN) of a piece, added to those before
 template <int DT>
-__global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p, int fraction) {
+struct Largest {
+  float m = -__builtin_inff();
+  uint32_t bits = 0;
+  h2_t pair = {(_Float16)-__builtin_inff(), (_Float16)-__builtin_inff()};
+  typedef uint16_t us2_t __attribute__((ext_vector_type(2)));
+  us2_t pair_bits = {0, 0};
+  __device__ __forceinline__ void add(const Piece<DT> &q) {
+    if constexpr (DT == DT_F32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        m = fmaxf(m, piece_at(q, i));
+        bits = max(bits, q.v[i >> 2][i & 3] & 0x7fffffffu);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = q.v[0][i];
+        pair_bits = __builtin_elementwise_max(pair_bits, __builtin_bit_cast(us2_t, w & 0x7fff7fffu));
+        if constexpr (DT == DT_F16) pair = __builtin_elementwise_max(pair, as_h2(w));
+        else m = fmaxf(m, fmaxf(__builtin_bit_cast(float, w << 16), __builtin_bit_cast(float, w & 0xffff0000u)));
+      }
+    }
+  }
+  __device__ __forceinline__ void finish() {
+    if constexpr (DT == DT_F16) m = fmaxf((float)pair[0], (float)pair[1]);
+    if constexpr (DT != DT_F32) {
+      const uint32_t b = max(pair_bits[0], pair_bits[1]);
+      bits = DT == DT_BF16 ? b << 16 : b > 0x7c00u ? 0x7fc00000u : 0;
+    }
+  }
+};
+
+template <int DT, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void sample_kernel(SampleParams p, int fraction) {
   __shared__ Shared s;
+  __shared__ Piece<DT> edge[2];
   const int64_t at = blockIdx.x;
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, V = p.V;
   typedef typename Elem<DT>::type T;
@@ -395,26 +485,26 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p, int fr
   row.x = static_cast<const T *>(p.x) + at * p.ldl;
   row.V = V;
   row.off = (int)((uintptr_t)row.x % 16 / sizeof(T));
-  row.rounds = (V + row.off + kRound - 1) / kRound;
+  row.rounds = (V + row.off + WAVES * kRound - 1) / (WAVES * kRound);
+  row.mine = __builtin_amdgcn_readfirstlane(wave) * row.rounds;
+  row.edge = edge;
+  row.fill_edges(edge, row.x, V, row.off);
+  __syncthreads();
   const float u = p.u[at], temperature = p.temperature ? p.temperature[at] : p.temperature_all;
   const float top_p = p.top_p ? p.top_p[at] : p.top_p_all, min_p = p.min_p ? p.min_p[at] : p.min_p_all;
   int top_k = p.top_k ? p.top_k[at] : p.top_k_all;
   if (top_k >= V) top_k = 0;
 
-  // the largest logit, whether all are numbers, and the maxima of 256 groups of four threads
-  float m = -__builtin_inff();
-  uint32_t bits = 0;                                              // of the largest magnitude: past infinity's for a NaN
-  row.each([&](int, const auto &q) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = piece_at(q, i);
-      m = fmaxf(m, x);
-      bits = max(bits, __builtin_bit_cast(uint32_t, x) & 0x7fffffffu);
-    }
-  });
+  // the largest logit, whether all are numbers, and the maxima of 256 groups of neighbouring lanes
+  Largest<DT> all;
+  row.each([&](int, const auto &q) { all.add(q); });
+  all.finish();
+  float m = all.m;
+  uint32_t bits = all.bits;
   float g = fmaxf(m, __shfl_xor(m, 1));
-  g = fmaxf(g, __shfl_xor(g, 2));
-  if ((t & 3) == 0) s.group[t >> 2] = g;
+  if constexpr (WAVES == 16) g = fmaxf(g, __shfl_xor(g, 2));
+  constexpr int kGroup = WAVES / 4;
+  if (t % kGroup == 0) s.group[t / kGroup] = g;
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) bits = max(bits, (uint32_t)__shfl_xor((int)bits, d));
   if (lane == 0) s.bits[wave] = bits;
@@ -427,24 +517,24 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p, int fr
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
 #pragma unroll
-  for (int i = 0; i < kSampleWaves; ++i) bits = max(bits, s.bits[i]);
+  for (int i = 0; i < WAVES; ++i) bits = max(bits, s.bits[i]);
   if (bits > 0x7f800000u || __builtin_isinf(m) || !(temperature >= 0.f) || __builtin_isinf(temperature) || u != u || top_p != top_p ||
       min_p != min_p) {
     if (t == 0) p.tokens[at] = -1;
     return;
   }
   if (temperature == 0.f) {                                       // the first of the largest
-    const int found = find_index(s, row, [&](float x, int i) { return i >= 0 && i < V && x == m ? 1.0 : 0.0; },
+    const int found = find_index<WAVES>(s, row, [&](const auto &q, int e, double *a) {
+#pragma unroll
+                                        for (int i = 0; i < 8; ++i) a[i] = e + i >= 0 && e + i < V && piece_at(q, i) == m ? 1.0 : 0.0;
+                                 },
+                                 [](double sum) { return (uint64_t)sum; },
                                  [](uint64_t, uint64_t &goal) { goal = 0; return true; });
     if (t == 0) p.tokens[at] = found;
     return;
   }
-  Scale scale;
-  scale.m = m;
-  scale.c = 1.4426950408889634 / (double)temperature;
-  scale.S = fraction;
-  scale.least = 0.0;
-  const double one = (double)(1ull << fraction), least = fmin((double)min_p, 1.0) * one;
+  Scale scale(m, 1.4426950408889634 / (double)temperature, fraction);
+  const double least = fmin((double)min_p, 1.0);
 
   // a threshold that all that may stay reach, and few others
   float above = __builtin_nanf("");
@@ -481,7 +571,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p, int fr
     });
     __syncthreads();
     if (s.count <= kList) {
-      settle(s, s.count, scale, top_k, top_p, least, u, p.tokens + at);
+      settle<WAVES>(s, s.count, scale, top_k, top_p, least, u, p.tokens + at);
       return;
     }
   }
@@ -497,26 +587,44 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleParams p, int fr
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float x = piece_at(q, i);
-          if (kept.holds(number_order(x), e + i)) mine += scale.weight(x);
+          const double w = scale.weight(x);
+          mine += kept.holds(number_order(x), e + i) ? w : 0.0;
         }
       });
-      const uint64_t all = block_sum(s, (uint64_t)mine);
+      const uint64_t all = block_sum<WAVES>(s, (uint64_t)ldexp(mine, fraction));
       const double want = ceil((double)top_p * (double)all);
       target = want < 1.0 ? 1 : (uint64_t)want;
       if (target > all) target = all;
     }
-    narrow(s, row, scale, weights != 0, target, kept);
+    narrow<WAVES>(s, row, scale, weights != 0, target, kept);
   }
-  scale.least = least;
-  const int found = find_index(s, row, [&](float x, int i) { return kept.holds(number_order(x), i) ? scale.weight(x) : 0.0; },
-                               [&](uint64_t total, uint64_t &goal) { goal = goal_of(u, total); return true; });
+  const auto goal = [&](uint64_t total, uint64_t &target) { target = goal_of(u, total); return true; };
+  const auto whole = [&](double sum) { return scale.whole(sum); };
+  int found;
+  if (kept.order == 0 && !(least > 0.0)) {
+    found = find_index<WAVES>(s, row, [&](const auto &q, int, double *a) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] = scale.weight(piece_at(q, i));
+    }, whole, goal);
+  } else {
+    found = find_index<WAVES>(s, row, [&](const auto &q, int e, double *a) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float x = piece_at(q, i);
+        const double r = scale.power(scale.exponent(x));
+        const bool stays = (r >= least) & kept.holds(number_order(x), e + i);
+        a[i] = stays ? scale.rounded(r) : 0.0;
+      }
+    }, whole, goal);
+  }
   if (t == 0) p.tokens[at] = found;
 }
 
 template <int DT>
 hipError_t launch(const SampleParams &p, int fraction, hipStream_t s) {
-  const dim3 grid((uint32_t)p.M), block(kThreads);
-  hipLaunchKernelGGL((sample_kernel<DT>), grid, block, 0, s, p, fraction);
+  const dim3 grid((uint32_t)p.M);
+  if (p.M > kCUs) hipLaunchKernelGGL((sample_kernel<DT, 8>), grid, dim3(512), 0, s, p, fraction);
+  else hipLaunchKernelGGL((sample_kernel<DT, 16>), grid, dim3(1024), 0, s, p, fraction);
   return hipGetLastError();
 }
 
