@@ -8,25 +8,32 @@
 //
 // A workgroup of 8 or 16 waves takes a row, each wave a run of it, 512 logits a round, read again (from L2) in
 // each pass.  What stays is told by one key: order bits of the number over the complement of the index.
-//   A top-k of up to kFewK takes a threshold from the maxima of 256 groups of lanes (the k-th largest
-//   of them is reached by at least k logits and few more); the logits above it go to LDS, and everything
-//   is settled among them by counting, for each, the larger ones.  So do rows of up to kList logits, and a min-p alone.
+//   A top-k of up to kMostK takes a threshold from the maxima of 256 or 1024 groups (the k-th largest
+//   of them is reached by at least k logits and not many more); the logits above it go to LDS, are sorted there (or, if they
+//   are few, each is compared with all by one wave), and the rest is settled by sums over them.  So do rows of up to kSort logits, and a min-p alone.
 //   Otherwise the border of top-k or top-p is found by histograms: of counts or weights over equal
-//   steps of the exponent (where neighbouring lanes rarely meet in one place), then over the order bits in
-//   the step that holds the border, until one number is left; of that, the first few by index stay.
+//   steps of the exponent (where neighbouring lanes rarely meet in one place), then in
+//   the step that holds the border, whose logits are sorted, or where they are many (equal ones), halved further by
+//   histograms over their order bits until one number is left, of which the first few by index stay.
 //   The token itself is the place where the running sum passes u times the whole: sums of the waves, of
 //   that wave's rounds (taken by all waves), of that round's lanes.
+#include <type_traits>
+
 #include "decode.h"
 
 namespace mnb {
 namespace {
 
-constexpr int kList = 1024;          // logits settled in LDS
-constexpr int kFewK = 180;           // about 310 of 256 groups' logits pass the 180th maximum
+constexpr int kCollect = 4096;       // logits collected in LDS
+constexpr int kSort = 1024;          // ... and sorted there
+constexpr int kFew = 128;            // ... or settled by one wave
+constexpr int kMostK = 1000;         // about 3900 logits reach the 1000th of 1024 maxima
+constexpr int kFewK = 180;           // about 310 logits reach the 180th of 256 maxima
+constexpr int kHeld = 6;             // rounds of a wave whose pieces stay in registers for the collection
 constexpr int kBins = 2048;
 constexpr int kRound = 512;          // logits of a wave's round
 constexpr int kMostWaves = 16;
-static_assert((1 << 22) / (kRound * 8) <= kList, "the sums of a wave's rounds lie in LDS");
+static_assert((1 << 22) / (kRound * 8) < kCollect, "the sums of a wave's rounds lie in LDS");
 
 // lane ^ 1, lane ^ 2, rotated by 4 and 8 in 16 lanes
 template <int CTRL>
@@ -64,7 +71,7 @@ __device__ __forceinline__ double in_scalars(double v) {
   return v;
 }
 
-// Weights of a row in units of 2^-S, as doubles that hold whole numbers of them: sums of a thread stay exact.
+// Weights of a row, and their whole numbers of 2^-S.
 struct Scale {
   double m, c, unit;       // unit: 2^(52 - S); adding it rounds to whole numbers of 2^-S
   double p[10], magic, low;
@@ -95,20 +102,17 @@ struct Scale {
     const u2_t w = {(uint32_t)b, (uint32_t)(b >> 32) + ((uint32_t)__builtin_bit_cast(uint64_t, t) << 20)};
     return __builtin_bit_cast(double, w);
   }
-  __device__ __forceinline__ double rounded(double r) const { return (r + unit) - unit; }
   // a sum of weights below 2^(52 - S) as a whole number
   __device__ __forceinline__ uint64_t whole(double sum) const { return __builtin_bit_cast(uint64_t, sum + unit) & ((1ull << 52) - 1); }
-  __device__ __forceinline__ double weight(float x) const { return rounded(power(exponent(x))); }
   __device__ __forceinline__ uint64_t whole_weight(float x) const { return whole(power(exponent(x))); }
 };
 
 struct Shared {
-  uint64_t key[kList + 8];           // also sums of a wave's rounds
-  uint64_t amount[kList];
+  uint64_t key[kCollect];            // also sums of a wave's rounds
   unsigned long long hist[kBins];
-  uint64_t wave[kMostWaves];
+  uint64_t wave[2 * kMostWaves];
   uint64_t chosen, before;
-  float group[256];
+  float group[1024];
   uint32_t bits[kMostWaves];
   int count;
 };
@@ -174,19 +178,38 @@ struct Row {
   // the first logit of this lane's piece in round j of this wave, in round r of all
   __device__ __forceinline__ int first(int j) const { return first_of(mine + j); }
   __device__ __forceinline__ int first_of(int r) const { return r * kRound + (int)(threadIdx.x & 63) * 8 - off; }
-  // f(j, piece) for each round, three pieces on their way meanwhile
+  // f(j, piece) for each round, the next ones on their way meanwhile
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    Piece<DT> a = load(0), b = load(1), c = load(2);
+    constexpr int kAhead = DT == DT_F32 ? 2 : 4;
+    Piece<DT> next[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) next[i] = load(i);
     for (int j = 0; j < rounds; ++j) {
-      const Piece<DT> next = load(j + 3);              // past the row: absent, without a load
-      f(j, a);
-      a = b;
-      b = c;
-      c = next;
+      const Piece<DT> now = next[0];
+#pragma unroll
+      for (int i = 0; i + 1 < kAhead; ++i) next[i] = next[i + 1];
+      if (j + kAhead < rounds) next[kAhead - 1] = load(j + kAhead);
+      f(j, now);
     }
   }
 };
+
+// the largest number of a piece
+template <int DT>
+__device__ __forceinline__ float piece_max(const Piece<DT> &q) {
+  if constexpr (DT == DT_F16) {
+    const u4_t v = q.v[0];
+    const h2_t a = __builtin_elementwise_max(as_h2(v[0]), as_h2(v[1])), b = __builtin_elementwise_max(as_h2(v[2]), as_h2(v[3]));
+    const h2_t c = __builtin_elementwise_max(a, b);
+    return fmaxf((float)c[0], (float)c[1]);
+  } else {
+    float m = fmaxf(piece_at<DT>(q, 0), piece_at<DT>(q, 1));
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) m = fmaxf(m, fmaxf(piece_at<DT>(q, i), piece_at<DT>(q, i + 1)));
+    return m;
+  }
+}
 
 // What stays of a row: keys at or above `least`.
 struct Kept {
@@ -196,38 +219,57 @@ struct Kept {
 };
 
 // The first index, in order, at which the running sum passes goal(total); -1 where it never does.  amounts(piece, first
-// index, out) gives the eight amounts of a piece as doubles, whole(sum) a sum of eight as a whole number.
+// index, out) gives the eight amounts of a piece as doubles, whole(sum) a sum of up to eight, rounded to a whole number:
+// what is summed on is a piece's whole.
 template <int WAVES, typename R, typename A, typename W, typename G>
 __device__ __forceinline__ int find_index(Shared &s, const R &row, A amounts, W whole, G goal) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   auto piece_sum = [&](const auto &p, int e) -> uint64_t {
     double a[8];
     amounts(p, e, a);
-    return whole(((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7])));
+#pragma unroll
+    for (int i = 1; i < 8; ++i) a[i] += a[i - 1];
+    return whole(a[7]);
   };
-  uint64_t sum = 0;
-  row.each([&](int j, const auto &p) { sum += piece_sum(p, row.first(j)); });
+  const int half = (row.rounds + 1) / 2;
+  uint64_t sum = 0, early = 0;                                    // of the second half of the wave's rounds, of the first
+  row.each([&](int j, const auto &p) {
+    if (j == half) {
+      early = sum;
+      sum = 0;
+    }
+    sum += piece_sum(p, row.first(j));
+  });
+  if (half == row.rounds) {
+    early = sum;
+    sum = 0;
+  }
+  early = wave_sum64(early);
   sum = wave_sum64(sum);
   __syncthreads();
-  if (lane == 0) s.wave[wave] = sum;
+  if (lane == 0) {
+    s.wave[2 * wave] = early;
+    s.wave[2 * wave + 1] = sum;
+  }
   if (threadIdx.x == 0) s.count = -1;
   __syncthreads();
   uint64_t total = 0, target = 0;
 #pragma unroll
-  for (int i = 0; i < WAVES; ++i) total += s.wave[i];
+  for (int i = 0; i < 2 * WAVES; ++i) total += s.wave[i];
   if (!goal(total, target) || target >= total) return -1;
   int at = 0;
   while (target >= s.wave[at]) target -= s.wave[at++];           // ends: target is below the sum of all
-  // that wave's rounds
-  for (int j = wave; j < row.rounds; j += WAVES) {
-    const int e = row.first_of(at * row.rounds + j);
+  // the rounds of that half
+  const int from = at / 2 * row.rounds + at % 2 * half, rounds = at % 2 ? row.rounds - half : half;
+  for (int j = wave; j < rounds; j += WAVES) {
+    const int e = row.first_of(from + j);
     const uint64_t one = wave_sum64(piece_sum(row.load_at(e), e));
     if (lane == 0) s.key[j] = one;
   }
   __syncthreads();
   int j = 0;
-  for (int j0 = 0; j0 < row.rounds; j0 += 64) {
-    const uint64_t v = j0 + lane < row.rounds ? s.key[j0 + lane] : 0, run = wave_scan64(v);
+  for (int j0 = 0; j0 < rounds; j0 += 64) {
+    const uint64_t v = j0 + lane < rounds ? s.key[j0 + lane] : 0, run = wave_scan64(v);
     const uint64_t hit = __ballot(run > target);
     if (hit) {
       const int l = __builtin_ctzll(hit);
@@ -239,25 +281,71 @@ __device__ __forceinline__ int find_index(Shared &s, const R &row, A amounts, W 
   }
   // that round's lanes
   if (wave == 0) {
-    const int e = row.first_of(at * row.rounds + j);
+    const int e = row.first_of(from + j);
     const auto p = row.load_at(e);
     const uint64_t own = piece_sum(p, e), run = wave_scan64(own);
     if (run > target && run - own <= target) {
-      uint64_t left = target - (run - own);
+      // the same sums as the piece's: the last is its whole
+      const uint64_t left = target - (run - own);
       int found = -1;
-      double each[8];
-      amounts(p, e, each);
+      double a[8];
+      amounts(p, e, a);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint64_t a = whole(each[i]);
-        if (found < 0 && a > left) found = e + i;
-        left -= found < 0 ? a : 0;
+        if (i) a[i] += a[i - 1];
+        if (found < 0 && whole(a[i]) > left) found = e + i;
       }
       s.count = found;
     }
   }
   __syncthreads();
   return s.count;
+}
+
+// sums over the workgroup's threads up to this one, and of all
+template <int WAVES>
+__device__ __forceinline__ uint64_t block_scan(Shared &s, uint64_t v, uint64_t &total) {
+  v = wave_scan64(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 63) s.wave[threadIdx.x >> 6] = v;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i) {
+    v += i < (int)(threadIdx.x >> 6) ? s.wave[i] : 0;
+    total += s.wave[i];
+  }
+  return v;
+}
+
+// The n keys in s.key (n up to kSort) in falling order, zeros behind them up to the power of two that is returned.
+template <int WAVES>
+__device__ __forceinline__ int sort_keys(Shared &s, int n) {
+  int P = 64;
+  while (P < n) P *= 2;
+  __syncthreads();
+  for (int i = n + (int)threadIdx.x; i < P; i += WAVES * 64) s.key[i] = 0;
+  __syncthreads();
+  for (int size = 2; size <= P; size *= 2) {
+    for (int stride = size / 2; stride > 0; stride /= 2) {
+      for (int q = threadIdx.x; q < P / 2; q += WAVES * 64) {
+        const int i = 2 * q - (q & (stride - 1));
+        const uint64_t a = s.key[i], b = s.key[i + stride];
+        if ((a < b) == ((i & size) == 0)) {
+          s.key[i] = b;
+          s.key[i + stride] = a;
+        }
+      }
+      // 64 neighbouring pairs stay among their 128 keys while strides are at most 64: a wave's own
+      if (stride > 64 || (stride == 1 && size >= 128)) __syncthreads();
+      else {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+  }
+  __syncthreads();
+  return P;
 }
 
 // the place of the histogram where the sum from the largest bin down (bin 0 first) reaches target: before < target <= before + it
@@ -284,10 +372,23 @@ __device__ __forceinline__ int find_bin(Shared &s, uint64_t target, uint64_t &be
   return (int)s.chosen;
 }
 
-// Narrows `kept` to the shortest run of largest numbers whose amounts (1, or the weight) reach target, at most
-// what `kept` holds in all.
-template <int WAVES, typename R>
-__device__ __forceinline__ void narrow(Shared &s, const R &row, const Scale &scale, bool weights, uint64_t target, Kept &kept) {
+// Adds the keys of the logits of a piece whose bit is set in `mask` to s.key, as far as there is room.
+template <typename P>
+__device__ __forceinline__ void collect(Shared &s, const P &p, int e, uint32_t mask) {
+  if (mask == 0) return;
+  int n = atomicAdd(&s.count, __popc(mask));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (!(mask >> i & 1)) continue;
+    if (n < kCollect) s.key[n] = (uint64_t)number_order(piece_at(p, i)) << 32 | (uint32_t)~(uint32_t)(e + i);
+    ++n;
+  }
+}
+
+// Narrows `kept` to the shortest run of largest numbers whose amounts (1, or the weight) reach target(whole), which is at
+// most the whole of what `kept` holds and weighs something.
+template <int WAVES, typename R, typename F>
+__device__ __forceinline__ void narrow(Shared &s, const R &row, const Scale &scale, bool weights, F target_of, Kept &kept) {
   const double steps = (kBins - 1) / (scale.S + 2.0);   // the last bin holds what weighs nothing
   auto clear = [&] {
     __syncthreads();
@@ -308,10 +409,59 @@ __device__ __forceinline__ void narrow(Shared &s, const R &row, const Scale &sca
     }
   });
   if (threadIdx.x == 0) s.chosen = kBins;
+  __syncthreads();
+  uint64_t all = 0;
+  for (int i = threadIdx.x; i < kBins; i += WAVES * 64) all += s.hist[i];
+  const uint64_t target = target_of(block_sum<WAVES>(s, all));
   uint64_t before = 0;
   const int bin = find_bin<WAVES>(s, target, before);
   if (bin == kBins) return;                             // the border is among what weighs nothing: all else stays
-  // in that bin: the smallest and the largest number, then a histogram over their order bits, until they are one
+  // those in that bin, if they are not too many, in order
+  const float below = (float)fmax(scale.m - bin / (steps * scale.c), -0x1p127), from = (float)(scale.m - (bin + 1) / (steps * scale.c));
+  const float slack = (fabsf(below) + fabsf((float)scale.m)) * 0x1p-20f;     // whose rounding the bin itself decides
+  if (threadIdx.x == 0) s.count = 0;
+  __syncthreads();
+  row.each([&](int j, const auto &p) {
+    if (!(piece_max(p) >= from - slack)) return;
+    const int e = row.first(j);
+    uint32_t mask = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = piece_at(p, i);
+      mask |= (uint32_t)((x >= from - slack) & (x <= below + slack)) << i;
+    }
+    if (mask == 0) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = piece_at(p, i);
+      if ((mask >> i & 1) && !(kept.holds(number_order(x), e + i) && bin_of(scale.exponent(x)) == bin)) mask &= ~(1u << i);
+    }
+    collect(s, p, e, mask);
+  });
+  __syncthreads();
+  const int n = s.count;
+  if (n <= kSort) {
+    constexpr int kEach = kSort / (WAVES * 64);
+    sort_keys<WAVES>(s, n);
+    uint64_t w[kEach], sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int a = threadIdx.x * kEach + i;
+      w[i] = a >= n ? 0 : weights ? scale.whole_weight(order_number((uint32_t)(s.key[a] >> 32))) : 1;
+      sum += w[i];
+    }
+    uint64_t run = block_scan<WAVES>(s, sum, total) - sum + before;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (run < target && target <= run + w[i]) s.chosen = s.key[threadIdx.x * kEach + i];
+      run += w[i];
+    }
+    __syncthreads();
+    kept.order = (uint32_t)(s.chosen >> 32);
+    kept.index = (int)~(uint32_t)s.chosen;
+    return;
+  }
+  // else the smallest and the largest number there, then a histogram over their order bits, until they are one
   uint32_t lo = 0, hi = 0xffffffffu;
   while (true) {
     uint32_t least = 0xffffffffu, most = 0;
@@ -379,64 +529,157 @@ __device__ __forceinline__ uint64_t goal_of(float u, uint64_t all) {
   return g < all ? g : all - 1;
 }
 
-// The row's token from the n logits of s.key, all that may stay: for each, sums over the larger ones and over those before it.
+// Leaves the k largest of the n keys in s.key (n up to kCollect, k < n), in any order: their k-th by 8 bits at a time.
 template <int WAVES>
-__device__ __forceinline__ void settle(Shared &s, int n, const Scale &scale, int top_k, float top_p, double least, float u, int64_t *token) {
-  constexpr int kEach = kList / (WAVES * 64);
+__device__ __forceinline__ void leave_largest(Shared &s, int n, int k) {
+  constexpr int kEach = kCollect / (WAVES * 64);
+  const int t = threadIdx.x, lane = t & 63;
+  uint64_t key[kEach], prefix = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) key[i] = t + i * WAVES * 64 < n ? s.key[t + i * WAVES * 64] : 0;   // no key is 0
+  uint32_t *hist = reinterpret_cast<uint32_t *>(s.hist);
+  for (int shift = 56; shift >= 0; shift -= 8) {
+    for (int i = t; i < 256; i += WAVES * 64) hist[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (key[i] && (shift == 56 || key[i] >> (shift + 8) == prefix >> (shift + 8))) atomicAdd(&hist[255 - (key[i] >> shift & 255)], 1u);
+    __syncthreads();
+    // every wave: four bins a lane, the largest first
+    uint32_t four[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += four[i] = hist[4 * lane + i];
+    const uint32_t run = (uint32_t)wave_scan64(sum);
+    const int l = __builtin_ctzll(__ballot(run >= (uint32_t)k));
+    int bin = 4 * l, left = k - (int)__builtin_amdgcn_readlane((int)(run - sum), l);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int c = (int)__builtin_amdgcn_readlane((int)four[i], l);
+      if (bin == 4 * l + i && left > c) {
+        left -= c;
+        ++bin;
+      }
+    }
+    prefix |= (uint64_t)(255 - bin) << shift;
+    k = left;
+    __syncthreads();
+  }
+  if (t == 0) s.count = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (key[i] >= prefix && key[i]) s.key[atomicAdd(&s.count, 1)] = key[i];
+  __syncthreads();
+}
+
+// The row's token from the n logits of s.key (n up to kFew), among them all that may stay, by one wave: each of a lane's
+// logits against all, for its rank and the sum of the larger ones, then for the sum of those before it.
+__device__ __forceinline__ void settle_few(Shared &s, int n, const Scale &scale, int top_k, float top_p, double least, float u, int64_t *token) {
+  constexpr int kEach = kFew / 64;
+  const int lane = threadIdx.x;
+  uint64_t *weight = reinterpret_cast<uint64_t *>(s.hist);
   uint64_t key[kEach], w[kEach], before[kEach] = {};
   double r[kEach];
   int rank[kEach] = {};
-  bool stays[kEach];
-  const int t = threadIdx.x;
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    const int a = t + k * WAVES * 64;
+    const int a = lane + 64 * k;
     key[k] = a < n ? s.key[a] : 0;
     r[k] = a < n ? scale.power(scale.exponent(order_number((uint32_t)(key[k] >> 32)))) : 0.0;
     w[k] = scale.whole(r[k]);
-    if (a < n) s.amount[a] = w[k];
+    if (a < n) weight[a] = w[k];
   }
-  __syncthreads();
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const uint64_t other = s.key[i], amount = weight[i];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const bool larger = other > key[k];
+      rank[k] += larger;
+      before[k] += larger ? amount : 0;
+    }
+  }
   uint64_t sum = 0;
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    if (t + k * WAVES * 64 >= n) {
-      stays[k] = false;
-      continue;
-    }
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const bool larger = s.key[i] > key[k];
-      rank[k] += larger;
-      before[k] += larger ? s.amount[i] : 0;
-    }
-    stays[k] = top_k <= 0 || rank[k] < top_k;
-    sum += stays[k] ? w[k] : 0;
+    if (top_k > 0 && rank[k] >= top_k) w[k] = 0;
+    sum += w[k];
   }
-  if (top_p < 1.f) {
-    const double want = ceil((double)top_p * (double)block_sum<WAVES>(s, sum));
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) stays[k] = stays[k] && (rank[k] == 0 || (want >= 1.0 && before[k] < (uint64_t)want));
-  }
+  const double want = top_p < 1.f ? ceil((double)top_p * (double)wave_sum64(sum)) : 0x1p64;
   sum = 0;
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
-    stays[k] = stays[k] && (rank[k] == 0 || r[k] >= least);
-    w[k] = stays[k] ? w[k] : 0;
+    if (rank[k] != 0 && !((double)before[k] < want && r[k] >= least)) w[k] = 0;
     sum += w[k];
   }
-  const uint64_t goal = goal_of(u, block_sum<WAVES>(s, sum));     // its barriers also end the reads of s.amount
+  const uint64_t goal = goal_of(u, wave_sum64(sum));
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 #pragma unroll
   for (int k = 0; k < kEach; ++k)
-    if (t + k * WAVES * 64 < n) s.amount[t + k * WAVES * 64] = w[k];
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kEach; ++k) {
-    if (w[k] == 0) continue;
-    uint64_t run = 0;                                             // of those up to this one: larger complements first
+    if (lane + 64 * k < n) weight[lane + 64 * k] = w[k];
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  uint64_t run[kEach] = {};                                       // larger complements of the index come first
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) run += (uint32_t)s.key[i] >= (uint32_t)key[k] ? s.amount[i] : 0;
-    if (run > goal && run - w[k] <= goal) *token = (int64_t)(uint32_t)~(uint32_t)key[k];
+  for (int i = 0; i < n; ++i) {
+    const uint32_t other = (uint32_t)s.key[i];
+    const uint64_t amount = weight[i];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) run[k] += other >= (uint32_t)key[k] ? amount : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    if (w[k] && run[k] > goal && run[k] - w[k] <= goal) *token = (int64_t)(uint32_t)~(uint32_t)key[k];
+}
+
+// The row's token from the n logits of s.key (n up to kSort), among them all that may stay: in the order of the numbers, what top-k, top-p and
+// min-p leave; then in the order of the index, where the running sum passes.
+template <int WAVES>
+__device__ __forceinline__ void settle(Shared &s, int n, const Scale &scale, int top_k, float top_p, double least, float u, int64_t *token) {
+  constexpr int kEach = kSort / (WAVES * 64);
+  const int P = sort_keys<WAVES>(s, n), each = (P + WAVES * 64 - 1) / (WAVES * 64), first = threadIdx.x * each;
+  if (top_k > 0 && n > top_k) n = top_k;
+  uint64_t key[kEach], w[kEach], sum = 0, all;
+  double r[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    w[i] = 0;
+    if (i >= each || first + i >= n) continue;
+    key[i] = s.key[first + i];
+    r[i] = scale.power(scale.exponent(order_number((uint32_t)(key[i] >> 32))));
+    sum += w[i] = scale.whole(r[i]);
+  }
+  uint64_t before = block_scan<WAVES>(s, sum, all) - sum;
+  const double want = top_p < 1.f ? ceil((double)top_p * (double)all) : 0x1p64;
+  sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (i >= each || first + i >= P) continue;
+    const bool stays = w[i] && (first + i == 0 || ((double)before < want && r[i] >= least));
+    before += w[i];
+    // the index counted down over the weight, of S + 1 bits: S and the index's bits are 62
+    const uint64_t back = ((1ull << (62 - scale.S)) - 1 - (uint32_t)~(uint32_t)key[i]) << (scale.S + 1);
+    s.key[first + i] = stays ? back | w[i] : 0;
+    sum += stays ? w[i] : 0;
+  }
+  const uint64_t goal = goal_of(u, block_sum<WAVES>(s, sum));
+  sort_keys<WAVES>(s, P);
+  sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (i >= each || first + i >= P) continue;
+    key[i] = s.key[first + i];
+    sum += w[i] = key[i] & ((2ull << scale.S) - 1);
+  }
+  uint64_t run = block_scan<WAVES>(s, sum, all) - sum;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (i >= each || first + i >= P) continue;
+    if (run <= goal && goal < run + w[i]) *token = (int64_t)((1ull << (62 - scale.S)) - 1 - (key[i] >> (scale.S + 1)));
+    run += w[i];
   }
 }
 
@@ -475,7 +718,7 @@ struct Largest {
 };
 
 template <int DT, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void sample_kernel(SampleParams p, int fraction) {
+__global__ __launch_bounds__(WAVES * 64, 4) void sample_kernel(SampleParams p, int fraction) {
   __shared__ Shared s;
   __shared__ Piece<DT> edge[2];
   const int64_t at = blockIdx.x;
@@ -495,24 +738,45 @@ __global__ __launch_bounds__(WAVES * 64) void sample_kernel(SampleParams p, int 
   int top_k = p.top_k ? p.top_k[at] : p.top_k_all;
   if (top_k >= V) top_k = 0;
 
-  // the largest logit, whether all are numbers, and the maxima of 256 groups of neighbouring lanes
-  Largest<DT> all;
-  row.each([&](int, const auto &q) { all.add(q); });
+  // the largest logit, whether all are numbers, and the maxima of 1024 lanes, or half lanes with 8 waves
+  Piece<DT> held[kHeld];
+  const bool holds = row.rounds <= kHeld;
+  Largest<DT> all, second;
+  if (holds) {
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+      if (j < row.rounds) held[j] = row.load(j);
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j) {
+      if (j >= row.rounds) continue;
+      if (WAVES == 8 && (j & 1)) second.add(held[j]);
+      else all.add(held[j]);
+    }
+  } else {
+    row.each([&](int j, const auto &q) {
+      if (WAVES == 8 && (j & 1)) second.add(q);
+      else all.add(q);
+    });
+  }
   all.finish();
+  s.group[t] = all.m;
   float m = all.m;
   uint32_t bits = all.bits;
-  float g = fmaxf(m, __shfl_xor(m, 1));
-  if constexpr (WAVES == 16) g = fmaxf(g, __shfl_xor(g, 2));
-  constexpr int kGroup = WAVES / 4;
-  if (t % kGroup == 0) s.group[t / kGroup] = g;
+  if constexpr (WAVES == 8) {
+    second.finish();
+    s.group[t + 512] = second.m;
+    m = fmaxf(m, second.m);
+    bits = max(bits, second.bits);
+  }
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) bits = max(bits, (uint32_t)__shfl_xor((int)bits, d));
   if (lane == 0) s.bits[wave] = bits;
   if (t == 0) s.count = 0;
   __syncthreads();
-  float four[4];
+  float four[4];                                                  // of 256 groups
 #pragma unroll
-  for (int i = 0; i < 4; ++i) four[i] = s.group[lane + 64 * i];
+  for (int i = 0; i < 4; ++i)
+    four[i] = fmaxf(fmaxf(s.group[lane + 64 * i], s.group[lane + 64 * i + 256]), fmaxf(s.group[lane + 64 * i + 512], s.group[lane + 64 * i + 768]));
   m = fmaxf(fmaxf(four[0], four[1]), fmaxf(four[2], four[3]));
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
@@ -538,19 +802,25 @@ __global__ __launch_bounds__(WAVES * 64) void sample_kernel(SampleParams p, int 
 
   // a threshold that all that may stay reach, and few others
   float above = __builtin_nanf("");
-  if (V <= kList) above = -__builtin_inff();
-  else if (top_k > 0 && top_k <= kFewK) {
-    uint32_t o[4], found = 0;
+  if (V <= kSort) above = -__builtin_inff();
+  else if (top_k > 0 && top_k <= kMostK) {
+    // the largest 16-bit prefix of order bits that top_k maxima reach
+    uint32_t found = 0;
+    auto reach = [&](auto count, auto value) {
+      constexpr int N = decltype(count)::value;
+      uint32_t o[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = number_order(four[i]) >> 16;
+      for (int i = 0; i < N; ++i) o[i] = number_order(value(i)) >> 16;
+      for (int bit = 15; bit >= 0; --bit) {
+        const uint32_t test = found | 1u << bit;
+        int c = 0;
 #pragma unroll
-    for (int bit = 15; bit >= 0; --bit) {                         // the largest 16-bit prefix that top_k maxima reach
-      const uint32_t test = found | 1u << bit;
-      int c = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c += __popcll(__ballot(o[i] >= test));
-      if (c >= top_k) found = test;
-    }
+        for (int i = 0; i < N; ++i) c += __popcll(__ballot(o[i] >= test));
+        if (c >= top_k) found = test;
+      }
+    };
+    if (top_k <= kFewK) reach(std::integral_constant<int, 4>(), [&](int i) { return four[i]; });
+    else reach(std::integral_constant<int, 16>(), [&](int i) { return s.group[lane + 64 * i]; });
     above = found <= number_order(-__builtin_inff()) >> 16 ? -__builtin_inff() : order_number(found << 16);
   } else if (top_k <= 0 && top_p >= 1.f && min_p > 0.f) {
     // a little below the least that stays, whose weight decides
@@ -558,45 +828,46 @@ __global__ __launch_bounds__(WAVES * 64) void sample_kernel(SampleParams p, int 
     above -= fabsf(above) * 0x1p-20f + fabsf(m) * 0x1p-20f;
   }
   if (above == above) {
-    row.each([&](int j, const auto &q) {
+    auto take = [&](int j, const auto &q) {
+      if (!(piece_max(q) >= above)) return;
       const int e = row.first(j);
+      uint32_t mask = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = piece_at(q, i);
-        if (x >= above && e + i >= 0 && e + i < V) {
-          const int n = atomicAdd(&s.count, 1);
-          if (n < kList) s.key[n] = (uint64_t)number_order(x) << 32 | (uint32_t)~(uint32_t)(e + i);
-        }
-      }
-    });
+      for (int i = 0; i < 8; ++i) mask |= (uint32_t)((piece_at(q, i) >= above) & (e + i >= 0) & (e + i < V)) << i;
+      collect(s, q, e, mask);
+    };
+    if (holds) {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j)
+        if (j < row.rounds) take(j, held[j]);
+    } else {
+      row.each(take);
+    }
     __syncthreads();
-    if (s.count <= kList) {
-      settle<WAVES>(s, s.count, scale, top_k, top_p, least, u, p.tokens + at);
+    int n = s.count;
+    __syncthreads();
+    if (n <= kFew) {
+      if (wave == 0) settle_few(s, n, scale, top_k, top_p, least, u, p.tokens + at);
+      return;
+    }
+    if (n > kSort && n <= kCollect && top_k > 0 && top_k <= kSort) {
+      leave_largest<WAVES>(s, n, top_k);
+      n = top_k;
+    }
+    if (n <= kSort) {
+      settle<WAVES>(s, n, scale, top_k, top_p, least, u, p.tokens + at);
       return;
     }
   }
 
   Kept kept;
   for (int weights = 0; weights < 2; ++weights) {                 // top-k, then top-p
-    uint64_t target = (uint64_t)top_k;
     if (weights ? top_p >= 1.f : top_k <= 0) continue;
-    if (weights) {
-      double mine = 0.0;
-      row.each([&](int j, const auto &q) {
-        const int e = row.first(j);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x = piece_at(q, i);
-          const double w = scale.weight(x);
-          mine += kept.holds(number_order(x), e + i) ? w : 0.0;
-        }
-      });
-      const uint64_t all = block_sum<WAVES>(s, (uint64_t)ldexp(mine, fraction));
+    narrow<WAVES>(s, row, scale, weights != 0, [&](uint64_t all) -> uint64_t {
+      if (!weights) return (uint64_t)top_k;
       const double want = ceil((double)top_p * (double)all);
-      target = want < 1.0 ? 1 : (uint64_t)want;
-      if (target > all) target = all;
-    }
-    narrow<WAVES>(s, row, scale, weights != 0, target, kept);
+      return want < 1.0 ? 1 : want < (double)all ? (uint64_t)want : all;
+    }, kept);
   }
   const auto goal = [&](uint64_t total, uint64_t &target) { target = goal_of(u, total); return true; };
   const auto whole = [&](double sum) { return scale.whole(sum); };
@@ -604,7 +875,7 @@ __global__ __launch_bounds__(WAVES * 64) void sample_kernel(SampleParams p, int 
   if (kept.order == 0 && !(least > 0.0)) {
     found = find_index<WAVES>(s, row, [&](const auto &q, int, double *a) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = scale.weight(piece_at(q, i));
+      for (int i = 0; i < 8; ++i) a[i] = scale.power(scale.exponent(piece_at(q, i)));
     }, whole, goal);
   } else {
     found = find_index<WAVES>(s, row, [&](const auto &q, int e, double *a) {
@@ -613,7 +884,7 @@ __global__ __launch_bounds__(WAVES * 64) void sample_kernel(SampleParams p, int 
         const float x = piece_at(q, i);
         const double r = scale.power(scale.exponent(x));
         const bool stays = (r >= least) & kept.holds(number_order(x), e + i);
-        a[i] = stays ? scale.rounded(r) : 0.0;
+        a[i] = stays ? r : 0.0;
       }
     }, whole, goal);
   }
