@@ -88,7 +88,6 @@ int check_attention(const mnb_kv_cache *c, const mnb_kv_rows *r, int q_heads, in
   if (kv_attn_plan(cache_of(c), rows_of(r), q_heads / c->kv_heads, window_of(c, r, window)).items > 1 << 23) return MNB_ERR_UNSUPPORTED;
   return MNB_OK;
 }
-size_t plan_bytes(const KvPlan &k, int D) { return k.whole ? 0 : (size_t)k.workgroups * 2 * k.slot_rows * (D + 4) * 4; }
 
 }  // namespace
 
@@ -166,8 +165,7 @@ int mnb_kv_read(const mnb_kv_cache *cache, const mnb_kv_rows *rows, void *k, int
 
 size_t mnb_kv_attention_workspace_bytes(const mnb_kv_cache *cache, const mnb_kv_rows *rows, int q_heads, int window) {
   if (check_attention(cache, rows, q_heads, window) || nothing(cache, rows) || q_heads == 0) return 0;
-  return plan_bytes(kv_attn_plan(cache_of(cache), rows_of(rows), q_heads / cache->kv_heads, window_of(cache, rows, window)),
-                    cache->head_dim);
+  return kv_attn_plan(cache_of(cache), rows_of(rows), q_heads / cache->kv_heads, window_of(cache, rows, window)).bytes;
 }
 
 int mnb_kv_describe_route(const mnb_kv_cache *cache, const mnb_kv_rows *rows, int q_heads, int window, char *buf, size_t buf_len) {
@@ -199,7 +197,7 @@ int mnb_kv_attention(const mnb_kv_cache *cache, const mnb_kv_rows *rows, const v
   p.G = q_heads / cache->kv_heads;
   p.window = window_of(cache, rows, window);
   const KvPlan k = kv_attn_plan(p.cache, p.rows, p.G, p.window);
-  const size_t need = plan_bytes(k, D);
+  const size_t need = k.bytes;
   if (need && (!workspace || ws_bytes < need)) return MNB_ERR_WORKSPACE;
   const Span c = cache_span(cache), sq = heads_span(q, ldq, rows->rows, q_heads, D, 2), sy = heads_span(y, ldy, rows->rows, q_heads, D, 2),
              ws{need ? workspace : nullptr, 1, 0, (int64_t)need};
@@ -214,7 +212,7 @@ int mnb_kv_attention(const mnb_kv_cache *cache, const mnb_kv_rows *rows, const v
   p.workgroups = k.workgroups;
   p.slot_rows = k.slot_rows;
   p.part = static_cast<float *>(workspace);
-  return status(launch_kv_attn(dtype, p, k.items, as_stream(stream)));
+  return status(launch_kv_attn(dtype, p, as_stream(stream)));
 }
 
 int mnb_sample(const void *logits, int dtype, int M, int V, int64_t ldl, const float *u, const float *temperature,

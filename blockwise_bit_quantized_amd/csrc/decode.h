@@ -79,15 +79,16 @@ struct KvAttnParams {
   int whole;           // every item goes to one workgroup
   int workgroups;      // of the first kernel
   int slot_rows;       // rows of a partial result
-  float *part;         // [workgroups, 2, slot_rows, D + 2]
+  float *part;         // what the second kernel is told of each workgroup, then [workgroups, 2, slot_rows, D + 4]
 };
 // The workgroups of the kernel of few rows for these sizes, and whether items are split over them.
 struct KvPlan {
   int workgroups, whole, slot_rows;
   int64_t items;       // at most
+  size_t bytes;        // of the workspace
 };
 KvPlan kv_attn_plan(const KvCache &c, const KvRows &r, int G, int window);
-hipError_t launch_kv_attn(int dtype, const KvAttnParams &p, int64_t items, hipStream_t s);
+hipError_t launch_kv_attn(int dtype, const KvAttnParams &p, hipStream_t s);
 
 struct SampleParams {
   const void *x;

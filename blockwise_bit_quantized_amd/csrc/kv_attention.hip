@@ -23,7 +23,9 @@ namespace mnb {
 namespace {
 
 constexpr int kStep = 32;      // tokens of a wave's step
-constexpr int kWaves = 4;
+constexpr int kWaves = 8;
+constexpr int kLeast = 2 * kWaves;   // steps of a workgroup's share at least
+constexpr int kAdd = 4;        // waves whose sums meet in LDS at once
 
 typedef __bf16 b8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 hh_t __attribute__((ext_vector_type(2)));
@@ -35,6 +37,13 @@ __device__ __forceinline__ f4_t mfma16(u4_t a, u4_t b, f4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8_t, a), __builtin_bit_cast(h8_t, b), c, 0, 0, 0);
   else
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8_t, a), __builtin_bit_cast(b8_t, b), c, 0, 0, 0);
+}
+// two numbers rounded to nearest even, in one instruction
+template <int DT>
+__device__ __forceinline__ uint32_t round2(float a, float b) {
+  const f2_t v = {a, b};
+  if constexpr (DT == DT_F16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, hh_t));
+  else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bb_t));
 }
 // byte B of w as two 16-bit numbers, times the power of two in the exponent field of `s`
 template <int DT, int B>
@@ -50,7 +59,8 @@ __device__ __forceinline__ u4_t expand8(uint32_t w, uint32_t s) {
 // scale byte I of w in the exponent field (the conversion reads nothing else of it)
 template <int I>
 __device__ __forceinline__ uint32_t scale_of(uint32_t w) {
-  return I < 3 ? w << (23 - 8 * I) : w >> 1;
+  if constexpr (I < 3) return w << (23 - 8 * I);
+  else return w >> 1;
 }
 
 // The value operand's parts: 16 lanes share 128, 64 or 32 elements, 8, 4 or 2 each; lane r of part k has the
@@ -141,28 +151,41 @@ struct Tile {
     }
   }
 
-  // 32 tokens from t0 (a multiple of 32) in the heads at ha and hb (16 tokens each, already offset to the
-  // first of them in their pages)
+  // What a step reads: 16 tokens each of two places, K and V with their scales.
+  struct Raw {
+    uint32_t kw[2][KS], ke[2][2];
+    u4_t v[2][P::count];
+    uint32_t vs[2][P::count];
+  };
+  // head: uniform; in: the first token's place in the page
+  __device__ static __forceinline__ void load(Raw &x, int half, const uint8_t *head, uint32_t in, uint32_t S, int g, int r) {
+    const uint32_t tok = in + r, unit = (in >> 2) + g;
+    const uint32_t *k = reinterpret_cast<const uint32_t *>(head + (tok * (D / 2) + g * (D / 8)));
+#pragma unroll
+    for (int i = 0; i < KS; ++i) x.kw[half][i] = k[i];
+    const uint32_t block = g * (D / 4) / 32, last = (g * (D / 4) + D / 4 - 1) / 32;
+    x.ke[half][0] = head[S * D + tok * (D / 32) + block];
+    // a lane's fourth of the head lies in one block where D is 64 or 128
+    x.ke[half][1] = D == 64 || D == 128 ? 0 : head[S * D + tok * (D / 32) + last];
+#pragma unroll
+    for (int p = 0; p < P::count; ++p) {
+      const uint32_t word = P::word(p, r);
+      x.v[half][p] = *reinterpret_cast<const u4_t *>(head + (S * (D / 2) + (unit * (D / 8) + word) * 16));
+      x.vs[half][p] = *reinterpret_cast<const uint32_t *>(head + (S * D + S * (D / 32) + (unit * (D / 32) + word / 4) * 4));
+    }
+  }
+
+  // 32 tokens from t0; EDGE: some row does not see some of them
   template <bool EDGE>
-  __device__ __forceinline__ void step(const uint8_t *ha, const uint8_t *hb, int ia, int ib, int S, float scale, int t0, int g, int r,
-                                       int tile_lo, int tile_hi) {
-    // keys
+  __device__ __forceinline__ void step(const Raw &raw, float scale, int t0, int g, int r, int tile_lo, int tile_hi) {
     f4_t s[2];
-    const uint8_t *const head[2] = {ha, hb};
-    const int in[2] = {ia, ib};                          // token of the page
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int tok = in[h] + r;
-      uint32_t w[KS];
-      const uint32_t *src = reinterpret_cast<const uint32_t *>(head[h] + (int64_t)tok * (D / 2) + g * (D / 8));
-#pragma unroll
-      for (int i = 0; i < KS; ++i) w[i] = src[i];
-      const uint8_t *sc = head[h] + kv_key_scales(S, D) + (int64_t)tok * (D / 32);
       s[h] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
-        const uint32_t e = sc[(g * (D / 4) + 8 * i) / 32];
-        s[h] = mfma16<DT>(expand8<DT>(w[i], e << 23), q[i], s[h]);
+        const bool later = D != 64 && D != 128 && (g * (D / 4) + 8 * i) / 32 != g * (D / 4) / 32;
+        s[h] = mfma16<DT>(expand8<DT>(raw.kw[h][i], (later ? raw.ke[h][1] : raw.ke[h][0]) << 23), q[i], s[h]);
       }
     }
     float t[8];
@@ -172,10 +195,10 @@ struct Tile {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
-        if (tok < lo || tok > pos) t[i] = -__builtin_inff();
+        t[i] = tok < lo || tok > pos ? -__builtin_inff() : t[i];
       }
     }
-    float most = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+    const float most = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
     if (__any(most > base + (kOff + 8.f))) {
       const float now = fmaxf(base, row_max(most) - kOff);
       const float f = now == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(base - now);
@@ -190,37 +213,25 @@ struct Tile {
       t[i] = __builtin_amdgcn_exp2f(t[i] - from);
       sum += t[i];
     }
-    const u4_t prob = {pack2<DT>(t[0], t[1]), pack2<DT>(t[2], t[3]), pack2<DT>(t[4], t[5]), pack2<DT>(t[6], t[7])};
-    // values
-    u4_t va[P::count], vb[P::count];
-    uint32_t sa[P::count], sb[P::count];
-#pragma unroll
-    for (int k = 0; k < P::count; ++k) {
-      const int word = P::word(k, r), ua = (ia >> 2) + g, ub = (ib >> 2) + g;
-      va[k] = *reinterpret_cast<const u4_t *>(ha + kv_value_codes(S, D) + ((int64_t)ua * (D / 8) + word) * 16);
-      vb[k] = *reinterpret_cast<const u4_t *>(hb + kv_value_codes(S, D) + ((int64_t)ub * (D / 8) + word) * 16);
-      sa[k] = *reinterpret_cast<const uint32_t *>(ha + kv_value_scales(S, D) + ((int64_t)ua * (D / 32) + word / 4) * 4);
-      sb[k] = *reinterpret_cast<const uint32_t *>(hb + kv_value_scales(S, D) + ((int64_t)ub * (D / 32) + word / 4) * 4);
-    }
+    const u4_t prob = {round2<DT>(t[0], t[1]), round2<DT>(t[2], t[3]), round2<DT>(t[4], t[5]), round2<DT>(t[6], t[7])};
     if constexpr (!EDGE) {
-      values<false>(va, vb, sa, sb, prob, r, true);
+      values<false>(raw.v[0], raw.v[1], raw.vs[0], raw.vs[1], prob, r, true);
       return;
     }
     // Tokens that no row sees may hold anything: their scales become 0.  Of the others, one whose values
     // are no numbers of q's type must not reach a row that does not see it (0 times infinity): such tokens go
     // one at a time, into the rows that do.
-    uint32_t far = 0, keep_a = 0, keep_b = 0;
+    uint32_t far = 0, keep_a = 0, keep_b = 0, sa[P::count], sb[P::count], na[P::count], nb[P::count];   // n: without the far ones
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int a = t0 + 4 * g + i, b = a + 16;
       if (a >= tile_lo && a <= tile_hi) keep_a |= 0xffu << (8 * i);
       if (b >= tile_lo && b <= tile_hi) keep_b |= 0xffu << (8 * i);
     }
-    uint32_t na[P::count], nb[P::count];                 // without the far ones
 #pragma unroll
     for (int k = 0; k < P::count; ++k) {
-      sa[k] &= keep_a;
-      sb[k] &= keep_b;
+      sa[k] = raw.vs[0][k] & keep_a;
+      sb[k] = raw.vs[1][k] & keep_b;
       uint32_t fa = 0, fb = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -231,29 +242,26 @@ struct Tile {
       nb[k] = sb[k] & ~fb;
       far |= fa | fb;
     }
-    values<false>(va, vb, na, nb, prob, r, true);
-    if (__any(far != 0)) {
-      for (int x = 0; x < 32; ++x) {                     // token t0 + x: lanes of group (x & 15) / 4, place x & 3
-        const bool mine = (x & 15) >> 2 == g;
-        const uint32_t byte = mine ? 0xffu << (8 * (x & 3)) : 0;
-        uint32_t oa[P::count], ob[P::count];
+    values<false>(raw.v[0], raw.v[1], na, nb, prob, r, true);
+    if (!__any(far != 0)) return;
+    for (int x = 0; x < 32; ++x) {                       // token t0 + x: lanes of group (x & 15) / 4, place x & 3
+      const bool mine = (x & 15) >> 2 == g;
+      const uint32_t byte = mine ? 0xffu << (8 * (x & 3)) : 0;
+      uint32_t oa[P::count], ob[P::count], any = 0;
 #pragma unroll
-        for (int k = 0; k < P::count; ++k) {
-          oa[k] = x < 16 ? sa[k] & ~na[k] & byte : 0;
-          ob[k] = x < 16 ? 0 : sb[k] & ~nb[k] & byte;
-        }
-        uint32_t any = 0;
-#pragma unroll
-        for (int k = 0; k < P::count; ++k) any |= oa[k] | ob[k];
-        if (!__any(any != 0)) continue;
-        // probabilities of this token alone
-        const uint32_t half = 0xffffu << (16 * (x & 1));
-        u4_t one = {0, 0, 0, 0};
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          if (mine && w == (x >> 4) * 2 + ((x & 3) >> 1)) one[w] = prob[w] & half;
-        values<true>(va, vb, oa, ob, one, r, t0 + x >= lo && t0 + x <= pos);
+      for (int k = 0; k < P::count; ++k) {
+        oa[k] = x < 16 ? sa[k] & ~na[k] & byte : 0;
+        ob[k] = x < 16 ? 0 : sb[k] & ~nb[k] & byte;
+        any |= oa[k] | ob[k];
       }
+      if (!__any(any != 0)) continue;
+      // probabilities of this token alone
+      const uint32_t half = 0xffffu << (16 * (x & 1));
+      u4_t one = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        if (mine && w == (x >> 4) * 2 + ((x & 3) >> 1)) one[w] = prob[w] & half;
+      values<true>(raw.v[0], raw.v[1], oa, ob, one, r, t0 + x >= lo && t0 + x <= pos);
     }
   }
 };
@@ -281,83 +289,79 @@ __device__ __forceinline__ int64_t cost_of(const KvAttnParams &p, int b) {
   return (int64_t)c.tiles * p.cache.heads * (p.whole ? 1 : c.steps);
 }
 
-// sums over the workgroup: inclusive over its threads, and of all
-template <int WAVES>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t &total) {
-  __shared__ int64_t part[WAVES];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// Sums over the wave's lanes up to this one.  (Every wave finds the workgroup's place in the work by itself.)
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int64_t o = __shfl_up((long long)v, d);
     if (lane >= d) v += o;
   }
-  __syncthreads();
-  if (lane == 63) part[wave] = v;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < WAVES; ++i) {
-    if (i < wave) v += part[i];
-    total += part[i];
-  }
   return v;
 }
-// the sequence that holds place `at` of the work, and the place where it begins
-template <int WAVES>
-__device__ __forceinline__ int find_work(const KvAttnParams &p, int64_t at, int64_t &begin) {
-  __shared__ int found;
-  __shared__ int64_t found_begin;
+__device__ __forceinline__ int64_t lane_of(int64_t v, int lane) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+                   (uint32_t)__builtin_amdgcn_readlane((int)v, lane));
+}
+// The workgroup's steps [at, end) of the work, and the sequence that holds `at` with the place where it begins;
+// false where nothing is left for it.
+struct Work {
+  int64_t at, end, begin, share;
+  int b;
+};
+__device__ __forceinline__ bool find_work(const KvAttnParams &p, Work &w) {
+  const int lane = threadIdx.x & 63;
+  const int64_t first = cost_of(p, lane), first_run = wave_scan(first);
+  w.share = 1;
+  if (!p.whole) {
+    int64_t total = lane_of(first_run, 63);
+    for (int b0 = 64; b0 < p.rows.batch; b0 += 64) total += lane_of(wave_scan(cost_of(p, b0 + lane)), 63);
+    w.share = (total + p.workgroups - 1) / p.workgroups;
+    if (w.share < kLeast) w.share = kLeast;
+  }
+  w.at = (int64_t)blockIdx.x * w.share;
   int64_t before = 0;
-  for (int b0 = 0; b0 < p.rows.batch; b0 += WAVES * 64) {
-    int64_t total;
-    const int64_t mine = cost_of(p, b0 + threadIdx.x), end = block_scan<WAVES>(mine, total) + before;
-    if (at < before + total) {
-      if (at >= end - mine && at < end) {
-        found = b0 + threadIdx.x;
-        found_begin = end - mine;
-      }
-      break;
-    }
-    before += total;
+  for (int b0 = 0; b0 < p.rows.batch; b0 += 64) {
+    const int64_t mine = b0 ? cost_of(p, b0 + lane) : first, run = (b0 ? wave_scan(mine) : first_run) + before;
+    const uint64_t hit = __ballot(run > w.at);
+    before = lane_of(run, 63);
+    if (!hit) continue;
+    const int l = __builtin_ctzll(hit);
+    w.b = b0 + l;
+    w.begin = lane_of(run - mine, l);
+    w.end = w.at + w.share;
+    return true;
   }
-  __syncthreads();
-  begin = found_begin;
-  const int b = found;
-  __syncthreads();
-  return b;
-}
-template <int WAVES>
-__device__ __forceinline__ int64_t whole_work(const KvAttnParams &p) {
-  int64_t sum = 0, total;
-  for (int b0 = 0; b0 < p.rows.batch; b0 += WAVES * 64) {
-    block_scan<WAVES>(cost_of(p, b0 + threadIdx.x), total);
-    sum += total;
-  }
-  return sum;
-}
-// steps of a workgroup
-__device__ __forceinline__ int64_t share_of(const KvAttnParams &p, int64_t total) {
-  if (p.whole) return 1;
-  const int64_t s = (total + p.workgroups - 1) / p.workgroups;
-  return s < 2 * kWaves ? 2 * kWaves : s;
+  return false;
 }
 
+// What the second kernel is told of a workgroup: the item that ends in its first part, if it began in another's.
+struct Joint {
+  int rows;                    // 0: none
+  int first, second;           // the workgroup where it began, and whether as its second part
+  int row0, tile, head;        // first row of the sequence, the tile, the key/value head
+  int pad[2];
+};
+
 template <int DT, int D>
-__global__ __launch_bounds__(kWaves * 64) void rows_kernel(KvAttnParams p) {
+__global__ __launch_bounds__(kWaves * 64, 2) void rows_kernel(KvAttnParams p) {
   typedef Parts<D> P;
+  typedef Tile<DT, D> T;
   constexpr int kRow = D + 4;                            // FP32 of a row in LDS, off the bank period
-  __shared__ float acc[kWaves][16][kRow];
+  __shared__ float acc[kAdd][16][kRow];
   __shared__ float stat[kWaves][16][2];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, r = lane & 15;
-  const int S = 1 << p.cache.shift;
-  const int64_t total = whole_work<kWaves>(p), share = share_of(p, total);
-  int64_t at = (int64_t)blockIdx.x * share;
-  if (at >= total) return;
-  const int64_t end = at + share < total ? at + share : total;
-  int64_t begin;
-  int b = find_work<kWaves>(p, at, begin);
+  const uint32_t S = 1u << p.cache.shift;
+  Joint *joint = reinterpret_cast<Joint *>(p.part) + blockIdx.x;
+  float *parts = p.part + (int64_t)p.workgroups * (sizeof(Joint) / 4);
+  Work work;
+  const bool any = find_work(p, work);
+  if (!p.whole && threadIdx.x == 0) joint->rows = 0;
+  if (!any) return;
+  int64_t at = work.at, begin = work.begin;
+  int b = work.b;
   bool first_item = true;
-  while (at < end) {
+  while (at < work.end && b < p.rows.batch) {
     const Cut c = cut_of(p, b);
     const int64_t span = p.whole ? 1 : c.steps, mine = span * c.tiles * p.cache.heads;
     if (at >= begin + mine) {                            // on to the next sequence
@@ -365,12 +369,13 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(KvAttnParams p) {
       ++b;
       continue;
     }
-    const int64_t item = (at - begin) / span, item0 = begin + item * span, stop = item0 + span < end ? item0 + span : end;
+    const int item = (int)((at - begin) / span);
+    const int64_t item0 = begin + item * span, stop = item0 + span < work.end ? item0 + span : work.end;
     const bool part = !(at == item0 && stop == item0 + span);
     const int s0 = p.whole ? 0 : (int)(at - item0), s1 = p.whole ? c.steps : (int)(stop - item0);
-    const int h = (int)(item % p.cache.heads), tile = (int)(item / p.cache.heads);
+    const int h = item % p.cache.heads, tile = item / p.cache.heads;
 
-    Tile<DT, D> x;
+    T x;
     x.clear();
     const int row = tile * 16 + r, tokens = c.seq.n;     // row of the sequence: token row / G, head row % G
     const bool real = row < (int64_t)tokens * p.G;
@@ -384,33 +389,62 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(KvAttnParams p) {
     const int i0 = tile * 16 / p.G, i1 = min(tokens - 1, (tile * 16 + 15) / p.G);
     const int pos0 = c.seq.first() + i0, pos1 = c.seq.first() + i1;
     const int any_lo = p.window ? max(0, pos0 - p.window + 1) : 0, all_lo = p.window ? max(0, pos1 - p.window + 1) : 0;
+    // the steps with tokens that any row sees
+    const int e0 = max(s0, (any_lo - c.from) / kStep), e1 = c.beyond || pos1 < 0 ? e0 : min(s1, (pos1 - c.from) / kStep + 1);
+    // ... and those whose tokens all see
+    const int f0 = min(e1, max(e0, (all_lo - c.from + kStep - 1) / kStep)), f1 = max(f0, min(e1, (pos0 + 1 - c.from) / kStep));
     bool bad = c.beyond;
     const int32_t *pages = p.rows.pages + (int64_t)b * p.rows.ldp;
-    for (int s = s0 + wave; s < s1 && !c.beyond; s += kWaves) {
+    const uint8_t *const data = p.cache.data + (int64_t)h * kv_head_bytes(S, D);
+    auto page_of = [&](int t, bool needed) {
+      const int col = t >> p.cache.shift;
+      int page = needed && col < p.rows.width ? pages[col] : -1;
+      if ((uint32_t)page >= (uint32_t)p.cache.pages) {
+        bad |= needed;
+        page = 0;
+      }
+      return page;
+    };
+    auto load = [&](typename T::Raw &raw, int half, int page, int t) {
+      T::load(raw, half, data + (int64_t)page * p.cache.page_stride, t & (S - 1), S, g, r);
+    };
+    // Page numbers of 32 steps of the wave, two a step, a lane each; a step's data is loaded while the one before is used.
+    for (int s = f0 + wave; s < f1;) {
+      const int ahead = s + (lane >> 1) * kWaves;
+      const int page = page_of(c.from + ahead * kStep + 16 * (lane & 1), ahead < f1);
+      auto fetch = [&](typename T::Raw &raw, int n) {
+        const int t = c.from + (s + n * kWaves) * kStep;
+        load(raw, 0, __builtin_amdgcn_readlane(page, 2 * n), t);
+        load(raw, 1, __builtin_amdgcn_readlane(page, 2 * n + 1), t + 16);
+      };
+      const int count = min(32, (f1 - s + kWaves - 1) / kWaves);
+      typename T::Raw one, two;
+      fetch(one, 0);
+      // (the last step is loaded again behind itself: a load under a condition would make every step wait for all)
+      for (int n = 0;;) {
+        fetch(two, min(n + 1, count - 1));
+        x.template step<false>(one, p.scale, 0, g, r, 0, 0);
+        if (++n == count) break;
+        fetch(one, min(n + 1, count - 1));
+        x.template step<false>(two, p.scale, 0, g, r, 0, 0);
+        if (++n == count) break;
+      }
+      s += count * kWaves;
+    }
+    for (int s = e0 + wave; s < e1; s += kWaves) {
+      if (s >= f0 && s < f1) continue;
       const int t0 = c.from + s * kStep;
-      if (t0 > pos1 || t0 + kStep <= any_lo) continue;
-      const uint8_t *head[2];
-      int in[2];
+      typename T::Raw raw;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int t = t0 + 16 * k, col = t >> p.cache.shift;
-        const bool needed = t <= pos1 && t + 15 >= any_lo;
-        int page = needed && col < p.rows.width ? pages[col] : -1;
-        if ((uint32_t)page >= (uint32_t)p.cache.pages) {
-          bad |= needed;
-          page = 0;
-        }
-        head[k] = p.cache.data + (int64_t)page * p.cache.page_stride + (int64_t)h * kv_head_bytes(S, D);
-        in[k] = t & (S - 1);
+        const int t = t0 + 16 * k;
+        load(raw, k, page_of(t, t <= pos1 && t + 15 >= any_lo), t);
       }
-      if (t0 >= all_lo && t0 + kStep - 1 <= pos0)
-        x.template step<false>(head[0], head[1], in[0], in[1], S, p.scale, t0, g, r, any_lo, pos1);
-      else x.template step<true>(head[0], head[1], in[0], in[1], S, p.scale, t0, g, r, any_lo, pos1);
+      x.template step<true>(raw, p.scale, t0, g, r, any_lo, pos1);
     }
     // the waves' parts, in their order
     x.sum = row_sum(x.sum);
-    if (bad) x.sum = __builtin_nanf("");
-    __syncthreads();
+    if (__any(bad)) x.sum = __builtin_nanf("");
     if (g == 0) {
       stat[wave][r][0] = x.base;
       stat[wave][r][1] = x.sum;
@@ -419,20 +453,33 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(KvAttnParams p) {
     float most = stat[0][r][0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) most = fmaxf(most, stat[w][r][0]);
-    const float f = x.base == -__builtin_inff() ? 0.f : __builtin_amdgcn_exp2f(x.base - most);
+    // a part that saw nothing adds nothing, whatever it holds
+    const bool saw = x.base != -__builtin_inff();
+    const float f = saw ? __builtin_amdgcn_exp2f(x.base - most) : 0.f;
 #pragma unroll
-    for (int k = 0; k < P::count; ++k)
+    for (int j = 0; j < P::tiles; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float *to = &acc[wave][r][P::first(k, 4 * g + j)];
+      for (int k = 0; k < 4; ++k) x.o[j][k] = saw ? x.o[j][k] * f : 0.f;
+    // the second four waves' go to the first four, whose are added below
+    auto exchange = [&](int place, bool add) {
 #pragma unroll
-        for (int n = 0; n < P::nib(k); ++n) {
-          // a part that saw nothing adds nothing, whatever it holds
-          to[n] = x.base == -__builtin_inff() ? 0.f : x.o[P::tile0(k) + n][j] * f;
+      for (int k = 0; k < P::count; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float *at4 = &acc[place][r][P::first(k, 4 * g + j)];
+#pragma unroll
+          for (int n = 0; n < P::nib(k); ++n) at4[n] = x.o[P::tile0(k) + n][j] + (add ? at4[n] : 0.f);
         }
-      }
+    };
+    if (wave >= kAdd) exchange(wave - kAdd, false);
+    __syncthreads();
+    if (wave < kAdd) exchange(wave, true);
     __syncthreads();
     const int rows = (int)min((int64_t)16, (int64_t)tokens * p.G - tile * 16);
+    if (part && threadIdx.x == 0 && stop == item0 + span) {
+      const int64_t w0 = item0 / work.share;
+      *joint = Joint{rows, (int)w0, item0 > w0 * work.share, c.seq.row0, tile, h, {0, 0}};
+    }
     for (int e = threadIdx.x; e < rows * (D / 8); e += kWaves * 64) {
       const int rr = e / (D / 8), d = (e - rr * (D / 8)) * 8;
       float m = stat[0][rr][0], l = 0.f, v[8] = {};
@@ -442,11 +489,13 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(KvAttnParams p) {
       for (int w = 0; w < kWaves; ++w) {
         const float bw = stat[w][rr][0], sw = stat[w][rr][1];
         l += bw == -__builtin_inff() ? sw : sw * __builtin_amdgcn_exp2f(bw - m);
+      }
+#pragma unroll
+      for (int w = 0; w < kAdd; ++w)
 #pragma unroll
         for (int n = 0; n < 8; ++n) v[n] += acc[w][rr][d + n];
-      }
       if (part) {
-        float *to = p.part + (((int64_t)blockIdx.x * 2 + (first_item ? 0 : 1)) * p.slot_rows + rr) * (D + 4);
+        float *to = parts + (((int64_t)blockIdx.x * 2 + (first_item ? 0 : 1)) * p.slot_rows + rr) * (D + 4);
         if (d == 0) {
           to[D] = m;
           to[D + 1] = l;
@@ -467,75 +516,76 @@ __global__ __launch_bounds__(kWaves * 64) void rows_kernel(KvAttnParams p) {
   }
 }
 
-// One workgroup an item, in a grid-wide loop: the parts of items that lie in more than one workgroup's share.
+// The parts of items that lie in more than one workgroup's share, joined in their order by a workgroup for each that
+// holds the end of one.  Groups of threads take the parts in turn.
+constexpr int kJoinThreads = 512;
 template <int DT, int D>
-__global__ __launch_bounds__(256) void join_kernel(KvAttnParams p, int64_t items) {
-  const int64_t total = whole_work<4>(p), share = share_of(p, total);
-  for (int64_t n = blockIdx.x; n < items; n += gridDim.x) {
-    // the item's sequence: items counted instead of steps
-    KvAttnParams count = p;
-    count.whole = 1;
-    if (n >= whole_work<4>(count)) return;
-    int64_t item0, begin = 0;
-    const int b = find_work<4>(count, n, item0);
-    for (int b0 = 0; b0 < b; b0 += 256) {
-      int64_t sum;
-      block_scan<4>(b0 + (int)threadIdx.x < b ? cost_of(p, b0 + threadIdx.x) : 0, sum);
-      begin += sum;
-    }
-    const Cut c = cut_of(p, b);
-    const int64_t item = n - item0, s = begin + item * c.steps, e = s + c.steps;
-    const int64_t w0 = s / share, w1 = (e - 1) / share;
-    if (w0 == w1) continue;
-    const int h = (int)(item % p.cache.heads), tile = (int)(item / p.cache.heads);
-    const int rows = (int)min((int64_t)16, (int64_t)c.seq.n * p.G - tile * 16);
-    for (int x = threadIdx.x; x < rows * (D / 4); x += 256) {
-      const int rr = x / (D / 4), d = (x - rr * (D / 4)) * 4;
-      float m = -__builtin_inff(), l = 0.f;
-      auto slot = [&](int64_t w) {
-        // the item is the workgroup's second where another began its share
-        const int second = w == w0 && s > w * share;
-        return p.part + ((w * 2 + second) * p.slot_rows + rr) * (D + 4);
-      };
-      for (int64_t w = w0; w <= w1; ++w) m = fmaxf(m, slot(w)[D]);
-      f4_t v = {0.f, 0.f, 0.f, 0.f};
-      for (int64_t w = w0; w <= w1; ++w) {
-        const float *from = slot(w), bw = from[D], sw = from[D + 1];
-        if (bw == -__builtin_inff()) {
-          l += sw;                                       // 0, or NaN where a page was out of range
-          continue;
-        }
-        const float f = __builtin_amdgcn_exp2f(bw - m);
-        l += sw * f;
-        v += *reinterpret_cast<const f4_t *>(from + d) * f;
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(KvAttnParams p) {
+  const Joint j = reinterpret_cast<const Joint *>(p.part)[blockIdx.x];
+  if (j.rows == 0) return;
+  const float *parts = p.part + (int64_t)p.workgroups * (sizeof(Joint) / 4);
+  const int n = (int)blockIdx.x - j.first + 1, slots = j.rows * (D / 4);
+  auto slot = [&](int i, int rr) {
+    return parts + (((int64_t)(j.first + i) * 2 + (i == 0 && j.second)) * p.slot_rows + rr) * (D + 4);
+  };
+  const int groups = max(1, kJoinThreads / slots);       // several, or rounds of slots
+  __shared__ f4_t sums[kJoinThreads];
+  __shared__ float weight[kJoinThreads];
+  for (int s0 = 0; s0 < slots; s0 += kJoinThreads) {
+    const int t = threadIdx.x, s = groups > 1 ? t % slots : s0 + t, group = groups > 1 ? t / slots : 0;
+    const bool on = group < groups && s < slots;
+    const int rr = on ? s / (D / 4) : 0, d = (s - rr * (D / 4)) * 4;
+    float m = -__builtin_inff(), l = 0.f;
+    f4_t v = {0.f, 0.f, 0.f, 0.f};
+    if (on) {
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) m = fmaxf(m, slot(i, rr)[D]);
+#pragma unroll 4
+      for (int i = group; i < n; i += groups) {
+        const float *from = slot(i, rr);
+        const float bw = from[D], sw = from[D + 1];
+        const f4_t o = *reinterpret_cast<const f4_t *>(from + d);
+        const bool saw = bw != -__builtin_inff();
+        const float f = saw ? __builtin_amdgcn_exp2f(bw - m) : 0.f;
+        l += saw ? sw * f : sw;                          // 0 of a part that saw nothing, or NaN where a page was out of range
+        v += o * f;
       }
-      const int ri = (tile * 16 + rr) / p.G, rh = (tile * 16 + rr) - ri * p.G;
-      uint16_t *y = p.y + (int64_t)(c.seq.row0 + ri) * p.ldy + (int64_t)(h * p.G + rh) * D + d;
+    }
+    __syncthreads();
+    sums[t] = v;
+    weight[t] = l;
+    __syncthreads();
+    if (on && group == 0) {
+      for (int k = 1; k < groups; ++k) {
+        v += sums[t + k * slots];
+        l += weight[t + k * slots];
+      }
+      const int row = j.tile * 16 + rr, ri = row / p.G, rh = row - ri * p.G;
+      uint16_t *y = p.y + (int64_t)(j.row0 + ri) * p.ldy + (int64_t)(j.head * p.G + rh) * D + d;
       if (l == 0.f) v = f4_t{0.f, 0.f, 0.f, 0.f};
       else v *= 1.f / l;
       *reinterpret_cast<u2_t *>(y) = u2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
     }
-    __syncthreads();
+    if (groups > 1) break;
   }
 }
 
 template <int DT, int D>
-hipError_t launch(const KvAttnParams &p, int64_t items, hipStream_t s) {
+hipError_t launch(const KvAttnParams &p, hipStream_t s) {
   hipLaunchKernelGGL((rows_kernel<DT, D>), dim3((uint32_t)p.workgroups), dim3(kWaves * 64), 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.whole) return e;
-  const uint32_t grid = (uint32_t)(items < 4096 ? items : 4096);
-  hipLaunchKernelGGL((join_kernel<DT, D>), dim3(grid), dim3(256), 0, s, p, items);
+  hipLaunchKernelGGL((join_kernel<DT, D>), dim3((uint32_t)p.workgroups), dim3(kJoinThreads), 0, s, p);
   return hipGetLastError();
 }
 template <int DT>
-hipError_t by_head(const KvAttnParams &p, int64_t items, hipStream_t s) {
+hipError_t by_head(const KvAttnParams &p, hipStream_t s) {
   switch (p.cache.D) {
-    case 64: return launch<DT, 64>(p, items, s);
-    case 96: return launch<DT, 96>(p, items, s);
-    case 128: return launch<DT, 128>(p, items, s);
-    case 192: return launch<DT, 192>(p, items, s);
-    default: return launch<DT, 256>(p, items, s);
+    case 64: return launch<DT, 64>(p, s);
+    case 96: return launch<DT, 96>(p, s);
+    case 128: return launch<DT, 128>(p, s);
+    case 192: return launch<DT, 192>(p, s);
+    default: return launch<DT, 256>(p, s);
   }
 }
 
@@ -550,14 +600,15 @@ KvPlan kv_attn_plan(const KvCache &c, const KvRows &r, int G, int window) {
   if (window && tokens > (int64_t)window + r.rows + kStep) tokens = (int64_t)window + r.rows + kStep;
   const int64_t steps = (tokens + kStep - 1) / kStep + 1;
   k.slot_rows = r.starts ? 16 : G < 16 ? G : 16;
-  const int64_t most = k.items * steps / (2 * kWaves);
+  const int64_t most = k.items * steps / kLeast + 1;
   k.whole = k.items >= 4 * kCUs || steps <= 4 * kWaves;
-  k.workgroups = (int)(k.whole ? k.items : most < 4 * kCUs ? most + 1 : 4 * kCUs);
+  k.workgroups = (int)(k.whole ? k.items : most < kCUs ? most : kCUs);
+  k.bytes = k.whole ? 0 : (size_t)k.workgroups * (sizeof(Joint) + (size_t)2 * k.slot_rows * (c.D + 4) * 4);
   return k;
 }
 
-hipError_t launch_kv_attn(int dtype, const KvAttnParams &p, int64_t items, hipStream_t s) {
-  return dtype == DT_F16 ? by_head<DT_F16>(p, items, s) : by_head<DT_BF16>(p, items, s);
+hipError_t launch_kv_attn(int dtype, const KvAttnParams &p, hipStream_t s) {
+  return dtype == DT_F16 ? by_head<DT_F16>(p, s) : by_head<DT_BF16>(p, s);
 }
 
 }  // namespace mnb
