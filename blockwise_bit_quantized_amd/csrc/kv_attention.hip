@@ -23,7 +23,7 @@ namespace mnb {
 namespace {
 
 constexpr int kStep = 32;      // tokens of a wave's step
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
 constexpr int kLeast = 2 * kWaves;   // steps of a workgroup's share at least
 constexpr int kAdd = 4;        // waves whose sums meet in LDS at once
 
@@ -311,8 +311,16 @@ struct Work {
 };
 __device__ __forceinline__ bool find_work(const KvAttnParams &p, Work &w) {
   const int lane = threadIdx.x & 63;
-  const int64_t first = cost_of(p, lane), first_run = wave_scan(first);
   w.share = 1;
+  if (p.whole && !p.rows.starts) {                       // as many items for each sequence
+    const int each = (p.G + 15) / 16 * p.cache.heads;
+    w.at = blockIdx.x;
+    w.end = w.at + 1;
+    w.b = blockIdx.x / each;
+    w.begin = (int64_t)w.b * each;
+    return true;
+  }
+  const int64_t first = cost_of(p, lane), first_run = wave_scan(first);
   if (!p.whole) {
     int64_t total = lane_of(first_run, 63);
     for (int b0 = 64; b0 < p.rows.batch; b0 += 64) total += lane_of(wave_scan(cost_of(p, b0 + lane)), 63);
@@ -344,7 +352,7 @@ struct Joint {
 };
 
 template <int DT, int D>
-__global__ __launch_bounds__(kWaves * 64, 2) void rows_kernel(KvAttnParams p) {
+__global__ __launch_bounds__(kWaves * 64, D <= 128 ? 3 : 2) void rows_kernel(KvAttnParams p) {
   typedef Parts<D> P;
   typedef Tile<DT, D> T;
   constexpr int kRow = D + 4;                            // FP32 of a row in LDS, off the bank period
@@ -471,9 +479,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rows_kernel(KvAttnParams p) {
           for (int n = 0; n < P::nib(k); ++n) at4[n] = x.o[P::tile0(k) + n][j] + (add ? at4[n] : 0.f);
         }
     };
-    if (wave >= kAdd) exchange(wave - kAdd, false);
-    __syncthreads();
-    if (wave < kAdd) exchange(wave, true);
+    if constexpr (kWaves > kAdd) {
+      if (wave >= kAdd) exchange(wave - kAdd, false);
+      __syncthreads();
+    }
+    if (wave < kAdd) exchange(wave, kWaves > kAdd);
     __syncthreads();
     const int rows = (int)min((int64_t)16, (int64_t)tokens * p.G - tile * 16);
     if (part && threadIdx.x == 0 && stop == item0 + span) {
@@ -516,58 +526,56 @@ __global__ __launch_bounds__(kWaves * 64, 2) void rows_kernel(KvAttnParams p) {
   }
 }
 
-// The parts of items that lie in more than one workgroup's share, joined in their order by a workgroup for each that
-// holds the end of one.  Groups of threads take the parts in turn.
-constexpr int kJoinThreads = 512;
+// The parts of items that lie in more than one workgroup's share, joined by a workgroup for each that holds the end of
+// one.  Groups of threads take the parts in turn, and the groups' results meet in their order.
+constexpr int kJoinThreads = 1024;
 template <int DT, int D>
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(KvAttnParams p) {
   const Joint j = reinterpret_cast<const Joint *>(p.part)[blockIdx.x];
   if (j.rows == 0) return;
   const float *parts = p.part + (int64_t)p.workgroups * (sizeof(Joint) / 4);
-  const int n = (int)blockIdx.x - j.first + 1, slots = j.rows * (D / 4);
-  auto slot = [&](int i, int rr) {
-    return parts + (((int64_t)(j.first + i) * 2 + (i == 0 && j.second)) * p.slot_rows + rr) * (D + 4);
-  };
-  const int groups = max(1, kJoinThreads / slots);       // several, or rounds of slots
+  const int n = (int)blockIdx.x - j.first + 1, slots = j.rows * (D / 4);   // at most 1024, of 16 rows of 256
+  const int groups = kJoinThreads / slots, t = threadIdx.x, group = t / slots, s = t - group * slots;
+  const int rr = s / (D / 4), d = (s - rr * (D / 4)) * 4;
   __shared__ f4_t sums[kJoinThreads];
-  __shared__ float weight[kJoinThreads];
-  for (int s0 = 0; s0 < slots; s0 += kJoinThreads) {
-    const int t = threadIdx.x, s = groups > 1 ? t % slots : s0 + t, group = groups > 1 ? t / slots : 0;
-    const bool on = group < groups && s < slots;
-    const int rr = on ? s / (D / 4) : 0, d = (s - rr * (D / 4)) * 4;
-    float m = -__builtin_inff(), l = 0.f;
-    f4_t v = {0.f, 0.f, 0.f, 0.f};
-    if (on) {
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) m = fmaxf(m, slot(i, rr)[D]);
-#pragma unroll 4
-      for (int i = group; i < n; i += groups) {
-        const float *from = slot(i, rr);
-        const float bw = from[D], sw = from[D + 1];
-        const f4_t o = *reinterpret_cast<const f4_t *>(from + d);
-        const bool saw = bw != -__builtin_inff();
-        const float f = saw ? __builtin_amdgcn_exp2f(bw - m) : 0.f;
-        l += saw ? sw * f : sw;                          // 0 of a part that saw nothing, or NaN where a page was out of range
-        v += o * f;
+  __shared__ f2_t stat[kJoinThreads];                    // base and sum
+  float m = -__builtin_inff(), l = 0.f;
+  f4_t v = {0.f, 0.f, 0.f, 0.f};
+  // v, l against m, and another part's against its own
+  auto add = [&](float bw, float sw, f4_t o) {
+    const bool saw = bw != -__builtin_inff();            // a part that saw nothing has the sum 0, or NaN where a page was out of range
+    const float now = fmaxf(m, bw), f = m == now ? 1.f : __builtin_amdgcn_exp2f(m - now), g = saw ? __builtin_amdgcn_exp2f(bw - now) : 0.f;
+    m = now;
+    l = l * f + (saw ? sw * g : sw);
+    v = v * f + o * g;
+  };
+  if (group < groups) {
+    for (int i = group; i < n; i += 4 * groups) {
+      float bw[4], sw[4];
+      f4_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int part = min(i + k * groups, n - 1);     // (again, where there is none)
+        const float *from = parts + (((int64_t)(j.first + part) * 2 + (part == 0 && j.second)) * p.slot_rows + rr) * (D + 4);
+        bw[k] = from[D];
+        sw[k] = from[D + 1];
+        o[k] = *reinterpret_cast<const f4_t *>(from + d);
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i + k * groups < n) add(bw[k], sw[k], o[k]);
     }
-    __syncthreads();
     sums[t] = v;
-    weight[t] = l;
-    __syncthreads();
-    if (on && group == 0) {
-      for (int k = 1; k < groups; ++k) {
-        v += sums[t + k * slots];
-        l += weight[t + k * slots];
-      }
-      const int row = j.tile * 16 + rr, ri = row / p.G, rh = row - ri * p.G;
-      uint16_t *y = p.y + (int64_t)(j.row0 + ri) * p.ldy + (int64_t)(j.head * p.G + rh) * D + d;
-      if (l == 0.f) v = f4_t{0.f, 0.f, 0.f, 0.f};
-      else v *= 1.f / l;
-      *reinterpret_cast<u2_t *>(y) = u2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
-    }
-    if (groups > 1) break;
+    stat[t] = f2_t{m, l};
   }
+  __syncthreads();
+  if (group != 0) return;
+  for (int k = 1; k < groups; ++k) add(stat[s + k * slots][0], stat[s + k * slots][1], sums[s + k * slots]);
+  const int row = j.tile * 16 + rr, ri = row / p.G, rh = row - ri * p.G;
+  uint16_t *y = p.y + (int64_t)(j.row0 + ri) * p.ldy + (int64_t)(j.head * p.G + rh) * D + d;
+  if (l == 0.f) v = f4_t{0.f, 0.f, 0.f, 0.f};
+  else v *= 1.f / l;
+  *reinterpret_cast<u2_t *>(y) = u2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
 }
 
 template <int DT, int D>
@@ -601,8 +609,8 @@ KvPlan kv_attn_plan(const KvCache &c, const KvRows &r, int G, int window) {
   const int64_t steps = (tokens + kStep - 1) / kStep + 1;
   k.slot_rows = r.starts ? 16 : G < 16 ? G : 16;
   const int64_t most = k.items * steps / kLeast + 1;
-  k.whole = k.items >= 4 * kCUs || steps <= 4 * kWaves;
-  k.workgroups = (int)(k.whole ? k.items : most < kCUs ? most : kCUs);
+  k.whole = k.items >= 4 * kCUs || steps <= 32;
+  k.workgroups = (int)(k.whole ? k.items : most < 3 * kCUs ? most : 3 * kCUs);
   k.bytes = k.whole ? 0 : (size_t)k.workgroups * (sizeof(Joint) + (size_t)2 * k.slot_rows * (c.D + 4) * 4);
   return k;
 }
