@@ -177,7 +177,7 @@ int mnb_kv_describe_route(const mnb_kv_cache *cache, const mnb_kv_rows *rows, in
     return MNB_OK;
   }
   const KvPlan k = kv_attn_plan(cache_of(cache), rows_of(rows), q_heads / cache->kv_heads, window_of(cache, rows, window));
-  snprintf(buf, buf_len, "kv_rows workgroups=%d%s", k.workgroups, k.whole ? "" : " join");
+  snprintf(buf, buf_len, "kv_rows tile=%d workgroups=%d%s", k.tile_rows, k.workgroups, k.whole ? "" : " join");
   return MNB_OK;
 }
 
@@ -207,9 +207,12 @@ int mnb_kv_attention(const mnb_kv_cache *cache, const mnb_kv_rows *rows, const v
   p.y = static_cast<uint16_t *>(y);
   p.ldq = ldq;
   p.ldy = ldy;
-  p.scale = scale * 1.4426950408889634f;
+  // at 0 a masked score would be no number (infinity times 0): the least scale instead, which leaves finite scores alike
+  p.scale = scale == 0.f ? 0x1p-126f : fabsf(scale) * 1.4426950408889634f;
+  p.flip = scale < 0.f ? 0x80008000u : 0;
   p.whole = k.whole;
   p.workgroups = k.workgroups;
+  p.tile_rows = k.tile_rows;
   p.slot_rows = k.slot_rows;
   p.part = static_cast<float *>(workspace);
   return status(launch_kv_attn(dtype, p, as_stream(stream)));

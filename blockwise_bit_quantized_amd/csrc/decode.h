@@ -75,15 +75,17 @@ struct KvAttnParams {
   int64_t ldq, ldy;
   int G;               // query heads of a key/value head
   int window;          // 0: none
-  float scale;         // times log2(e)
+  float scale;         // |scale| times log2(e); a negative one turns q's signs by
+  uint32_t flip;       // these bits
   int whole;           // every item goes to one workgroup
   int workgroups;      // of the first kernel
+  int tile_rows;       // 16 or 32
   int slot_rows;       // rows of a partial result
   float *part;         // what the second kernel is told of each workgroup, then [workgroups, 2, slot_rows, D + 4]
 };
 // The workgroups of the kernel of few rows for these sizes, and whether items are split over them.
 struct KvPlan {
-  int workgroups, whole, slot_rows;
+  int workgroups, whole, tile_rows, slot_rows;
   int64_t items;       // at most
   size_t bytes;        // of the workspace
 };

@@ -25,7 +25,6 @@ namespace {
 constexpr int kStep = 32;      // tokens of a wave's step
 constexpr int kWaves = 4;
 constexpr int kLeast = 2 * kWaves;   // steps of a workgroup's share at least
-constexpr int kAdd = 4;        // waves whose sums meet in LDS at once
 
 typedef __bf16 b8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 hh_t __attribute__((ext_vector_type(2)));
@@ -81,33 +80,32 @@ __device__ __forceinline__ float row_max(float v) {
   v = fmaxf(v, __shfl_xor(v, 16));
   return fmaxf(v, __shfl_xor(v, 32));
 }
-__device__ __forceinline__ float row_sum(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
-}
-
-template <int DT, int D>
+template <int DT, int D, int R>
 struct Tile {
   typedef Parts<D> P;
   static constexpr int KS = D / 32;                       // matrix instructions along the head
   static constexpr float kOff = DT == DT_F16 ? 6.f : 0.f; // fp16 keeps small probabilities by 2^6
   static constexpr uint32_t kFar = DT == DT_F16 ? 141 : 253;   // first scale whose values may pass q's type
-  u4_t q[KS];
-  f4_t o[P::tiles];
-  float base, sum;         // base: what scores are taken against; the sum of this lane's probabilities
-  int pos, lo;             // the row sees tokens lo .. pos
+  u4_t q[R][KS];
+  f4_t o[R][P::tiles];
+  float base[R];           // what scores are taken against
+  f4_t sum[R];             // the sum of the row's probabilities, in every place, as a product with ones
+  int pos[R], lo[R];       // the row sees tokens lo .. pos
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int j = 0; j < P::tiles; ++j) o[j] = f4_t{0.f, 0.f, 0.f, 0.f};
-    base = -__builtin_inff();
-    sum = 0.f;
+    for (int x = 0; x < R; ++x) {
+#pragma unroll
+      for (int j = 0; j < P::tiles; ++j) o[x][j] = f4_t{0.f, 0.f, 0.f, 0.f};
+      base[x] = -__builtin_inff();
+      sum[x] = f4_t{0.f, 0.f, 0.f, 0.f};
+    }
   }
 
   // O^T += V^T P^T for 32 tokens; with `only`, rows that do not see the token keep theirs
   template <bool ONLY>
-  __device__ __forceinline__ void values(const u4_t *va, const u4_t *vb, const uint32_t *sa, const uint32_t *sb, u4_t prob, int r,
-                                         bool sees) {
+  __device__ __forceinline__ void values(const u4_t *va, const u4_t *vb, const uint32_t *sa, const uint32_t *sb, const u4_t *prob, int r,
+                                         const bool *sees) {
 #pragma unroll
     for (int k = 0; k < P::count; ++k) {
       const int sh = P::shift(k, r);
@@ -128,18 +126,21 @@ struct Tile {
                           __builtin_amdgcn_perm(b3, b2, L)};
         const u4_t hi4 = {__builtin_amdgcn_perm(a1, a0, H), __builtin_amdgcn_perm(a3, a2, H), __builtin_amdgcn_perm(b1, b0, H),
                           __builtin_amdgcn_perm(b3, b2, H)};
-        f4_t &x = o[P::tile0(k) + 2 * B], &y = o[P::tile0(k) + 2 * B + 1];
-        if constexpr (ONLY) {
-          const f4_t zero = {0.f, 0.f, 0.f, 0.f};
-          const f4_t dx = mfma16<DT>(lo4, prob, zero), dy = mfma16<DT>(hi4, prob, zero);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] += sees ? dx[i] : 0.f;
-            y[i] += sees ? dy[i] : 0.f;
+        for (int w = 0; w < R; ++w) {
+          f4_t &x = o[w][P::tile0(k) + 2 * B], &y = o[w][P::tile0(k) + 2 * B + 1];
+          if constexpr (ONLY) {
+            const f4_t zero = {0.f, 0.f, 0.f, 0.f};
+            const f4_t dx = mfma16<DT>(lo4, prob[w], zero), dy = mfma16<DT>(hi4, prob[w], zero);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[i] += sees[w] ? dx[i] : 0.f;
+              y[i] += sees[w] ? dy[i] : 0.f;
+            }
+          } else {
+            x = mfma16<DT>(lo4, prob[w], x);
+            y = mfma16<DT>(hi4, prob[w], y);
           }
-        } else {
-          x = mfma16<DT>(lo4, prob, x);
-          y = mfma16<DT>(hi4, prob, y);
         }
       };
       pair(std::integral_constant<int, 0>());
@@ -178,44 +179,58 @@ struct Tile {
   // 32 tokens from t0; EDGE: some row does not see some of them
   template <bool EDGE>
   __device__ __forceinline__ void step(const Raw &raw, float scale, int t0, int g, int r, int tile_lo, int tile_hi) {
-    f4_t s[2];
+    f4_t s[R][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      s[h] = f4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < R; ++w) s[w][h] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < KS; ++i) {
         const bool later = D != 64 && D != 128 && (g * (D / 4) + 8 * i) / 32 != g * (D / 4) / 32;
-        s[h] = mfma16<DT>(expand8<DT>(raw.kw[h][i], (later ? raw.ke[h][1] : raw.ke[h][0]) << 23), q[i], s[h]);
+        const u4_t k = expand8<DT>(raw.kw[h][i], (later ? raw.ke[h][1] : raw.ke[h][0]) << 23);
+#pragma unroll
+        for (int w = 0; w < R; ++w) s[w][h] = mfma16<DT>(k, q[w][i], s[w][h]);
       }
     }
-    float t[8];
+    u4_t prob[R];
+    float most[R];
+    bool raise = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = s[i >> 2][i & 3] * scale;
-    if constexpr (EDGE) {
+    for (int w = 0; w < R; ++w) {
+      f4_t *t = s[w];
+      if constexpr (EDGE) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
-        t[i] = tok < lo || tok > pos ? -__builtin_inff() : t[i];
+        for (int i = 0; i < 8; ++i) {
+          const int tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
+          t[i >> 2][i & 3] = tok < lo[w] || tok > pos[w] ? -__builtin_inff() : t[i >> 2][i & 3];
+        }
+      }
+      most[w] = fmaxf(fmaxf(fmaxf(t[0][0], t[0][1]), fmaxf(t[0][2], t[0][3])), fmaxf(fmaxf(t[1][0], t[1][1]), fmaxf(t[1][2], t[1][3]))) * scale;
+      raise |= most[w] > base[w] + (kOff + 8.f);
+    }
+    if (__any(raise)) {
+#pragma unroll
+      for (int w = 0; w < R; ++w) {
+        const float now = fmaxf(base[w], row_max(most[w]) - kOff);
+        const float f = now == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(base[w] - now);
+        base[w] = now;
+        sum[w] *= f;
+#pragma unroll
+        for (int j = 0; j < P::tiles; ++j) o[w][j] *= f;
       }
     }
-    const float most = fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
-    if (__any(most > base + (kOff + 8.f))) {
-      const float now = fmaxf(base, row_max(most) - kOff);
-      const float f = now == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(base - now);
-      base = now;
-      sum *= f;
 #pragma unroll
-      for (int j = 0; j < P::tiles; ++j) o[j] *= f;
-    }
-    const float from = base == -__builtin_inff() ? 0.f : base;
+    for (int w = 0; w < R; ++w) {
+      const float from = base[w] == -__builtin_inff() ? 0.f : base[w];
+      float t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      t[i] = __builtin_amdgcn_exp2f(t[i] - from);
-      sum += t[i];
+      for (int i = 0; i < 8; ++i) t[i] = __builtin_amdgcn_exp2f(fmaf(s[w][i >> 2][i & 3], scale, -from));
+      prob[w] = u4_t{round2<DT>(t[0], t[1]), round2<DT>(t[2], t[3]), round2<DT>(t[4], t[5]), round2<DT>(t[6], t[7])};
+      constexpr uint32_t one = DT == DT_F16 ? 0x3c003c00u : 0x3f803f80u;
+      sum[w] = mfma16<DT>(u4_t{one, one, one, one}, prob[w], sum[w]);
     }
-    const u4_t prob = {round2<DT>(t[0], t[1]), round2<DT>(t[2], t[3]), round2<DT>(t[4], t[5]), round2<DT>(t[6], t[7])};
     if constexpr (!EDGE) {
-      values<false>(raw.v[0], raw.v[1], raw.vs[0], raw.vs[1], prob, r, true);
+      values<false>(raw.v[0], raw.v[1], raw.vs[0], raw.vs[1], prob, r, nullptr);
       return;
     }
     // Tokens that no row sees may hold anything: their scales become 0.  Of the others, one whose values
@@ -242,7 +257,7 @@ struct Tile {
       nb[k] = sb[k] & ~fb;
       far |= fa | fb;
     }
-    values<false>(raw.v[0], raw.v[1], na, nb, prob, r, true);
+    values<false>(raw.v[0], raw.v[1], na, nb, prob, r, nullptr);
     if (!__any(far != 0)) return;
     for (int x = 0; x < 32; ++x) {                       // token t0 + x: lanes of group (x & 15) / 4, place x & 3
       const bool mine = (x & 15) >> 2 == g;
@@ -257,16 +272,20 @@ struct Tile {
       if (!__any(any != 0)) continue;
       // probabilities of this token alone
       const uint32_t half = 0xffffu << (16 * (x & 1));
-      u4_t one = {0, 0, 0, 0};
+      u4_t one[R];
+      bool sees[R];
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        if (mine && w == (x >> 4) * 2 + ((x & 3) >> 1)) one[w] = prob[w] & half;
-      values<true>(raw.v[0], raw.v[1], oa, ob, one, r, t0 + x >= lo && t0 + x <= pos);
+      for (int w = 0; w < R; ++w) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) one[w][i] = mine && i == (x >> 4) * 2 + ((x & 3) >> 1) ? prob[w][i] & half : 0;
+        sees[w] = t0 + x >= lo[w] && t0 + x <= pos[w];
+      }
+      values<true>(raw.v[0], raw.v[1], oa, ob, one, r, sees);
     }
   }
 };
 
-// How a sequence's work is cut: its tiles of 16 rows, and the tokens that any of its rows sees.
+// How a sequence's work is cut: its tiles of 16 or 32 rows, and the tokens that any of its rows sees.
 struct Cut {
   KvSeq seq;
   int tiles, from, steps;      // from: a multiple of kStep
@@ -275,7 +294,7 @@ struct Cut {
 __device__ __forceinline__ Cut cut_of(const KvAttnParams &p, int b) {
   Cut c;
   c.seq = kv_seq(p.rows, b);
-  c.tiles = (int)(((int64_t)c.seq.n * p.G + 15) / 16);
+  c.tiles = (int)(((int64_t)c.seq.n * p.G + p.tile_rows - 1) / p.tile_rows);
   const int lo = p.window ? max(0, c.seq.first() - p.window + 1) : 0;
   c.from = lo / kStep * kStep;
   c.beyond = c.seq.len > p.rows.width << p.cache.shift;
@@ -303,22 +322,23 @@ __device__ __forceinline__ int64_t lane_of(int64_t v, int lane) {
   return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
                    (uint32_t)__builtin_amdgcn_readlane((int)v, lane));
 }
-// The workgroup's steps [at, end) of the work, and the sequence that holds `at` with the place where it begins;
-// false where nothing is left for it.
+// The workgroup's steps [at, end) of the work (none left: end 0), and the sequence that holds `at` with the place where
+// it begins.
 struct Work {
   int64_t at, end, begin, share;
   int b;
 };
-__device__ __forceinline__ bool find_work(const KvAttnParams &p, Work &w) {
+__device__ __forceinline__ Work find_work(const KvAttnParams &p) {
+  Work w{};
   const int lane = threadIdx.x & 63;
   w.share = 1;
   if (p.whole && !p.rows.starts) {                       // as many items for each sequence
-    const int each = (p.G + 15) / 16 * p.cache.heads;
+    const int each = (p.G + p.tile_rows - 1) / p.tile_rows * p.cache.heads;
     w.at = blockIdx.x;
     w.end = w.at + 1;
     w.b = blockIdx.x / each;
     w.begin = (int64_t)w.b * each;
-    return true;
+    return w;
   }
   const int64_t first = cost_of(p, lane), first_run = wave_scan(first);
   if (!p.whole) {
@@ -333,39 +353,43 @@ __device__ __forceinline__ bool find_work(const KvAttnParams &p, Work &w) {
     const int64_t mine = b0 ? cost_of(p, b0 + lane) : first, run = (b0 ? wave_scan(mine) : first_run) + before;
     const uint64_t hit = __ballot(run > w.at);
     before = lane_of(run, 63);
-    if (!hit) continue;
-    const int l = __builtin_ctzll(hit);
-    w.b = b0 + l;
-    w.begin = lane_of(run - mine, l);
-    w.end = w.at + w.share;
-    return true;
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      w.b = b0 + l;
+      w.begin = lane_of(run - mine, l);
+      w.end = w.at + w.share;
+      break;
+    }
   }
-  return false;
+  return w;
 }
 
 // What the second kernel is told of a workgroup: the item that ends in its first part, if it began in another's.
 struct Joint {
   int rows;                    // 0: none
   int first, second;           // the workgroup where it began, and whether as its second part
-  int row0, tile, head;        // first row of the sequence, the tile, the key/value head
+  int row0, row, head;         // first row of the sequence, row of it where the tile begins, key/value head
   int pad[2];
 };
 
-template <int DT, int D>
-__global__ __launch_bounds__(kWaves * 64, D <= 128 ? 3 : 2) void rows_kernel(KvAttnParams p) {
+// Workgroups of this kernel that share a CU, by the registers of its tile.
+constexpr int resident(int D, int R) { return R == 1 ? (D <= 128 ? 3 : 2) : R == 2 && D <= 128 ? 2 : 1; }
+
+template <int DT, int D, int R>
+__global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAttnParams p) {
   typedef Parts<D> P;
-  typedef Tile<DT, D> T;
+  typedef Tile<DT, D, R> T;
+  constexpr int kRows = 16 * R;
   constexpr int kRow = D + 4;                            // FP32 of a row in LDS, off the bank period
-  __shared__ float acc[kAdd][16][kRow];
+  __shared__ float acc[kWaves][16][kRow];
   __shared__ float stat[kWaves][16][2];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, r = lane & 15;
   const uint32_t S = 1u << p.cache.shift;
   Joint *joint = reinterpret_cast<Joint *>(p.part) + blockIdx.x;
   float *parts = p.part + (int64_t)p.workgroups * (sizeof(Joint) / 4);
-  Work work;
-  const bool any = find_work(p, work);
+  const Work work = find_work(p);
   if (!p.whole && threadIdx.x == 0) joint->rows = 0;
-  if (!any) return;
+  if (work.end == 0) return;
   int64_t at = work.at, begin = work.begin;
   int b = work.b;
   bool first_item = true;
@@ -381,20 +405,24 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 3 : 2) void rows_kernel(KvA
     const int64_t item0 = begin + item * span, stop = item0 + span < work.end ? item0 + span : work.end;
     const bool part = !(at == item0 && stop == item0 + span);
     const int s0 = p.whole ? 0 : (int)(at - item0), s1 = p.whole ? c.steps : (int)(stop - item0);
-    const int h = item % p.cache.heads, tile = item / p.cache.heads;
+    // the last rows, which see most, first
+    const int h = item % p.cache.heads, tile = c.tiles - 1 - item / p.cache.heads;
 
     T x;
     x.clear();
-    const int row = tile * 16 + r, tokens = c.seq.n;     // row of the sequence: token row / G, head row % G
-    const bool real = row < (int64_t)tokens * p.G;
-    const int i = row / p.G, gh = row - i * p.G;
-    const uint16_t *q = p.q + (int64_t)(c.seq.row0 + i) * p.ldq + (int64_t)(h * p.G + gh) * D + g * (D / 4);
+    const int tokens = c.seq.n, row0 = tile * kRows;     // row of the sequence: token row / G, head row % G
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) x.q[k] = real ? reinterpret_cast<const u4_t *>(q)[k] : u4_t{0, 0, 0, 0};
-    x.pos = real ? c.seq.first() + i : -1;
-    x.lo = p.window ? x.pos - p.window + 1 : 0;
+    for (int w = 0; w < R; ++w) {
+      const int row = row0 + 16 * w + r, i = row / p.G, gh = row - i * p.G;
+      const bool real = i < tokens;
+      const uint16_t *q = p.q + (int64_t)(c.seq.row0 + i) * p.ldq + (int64_t)(h * p.G + gh) * D + g * (D / 4);
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) x.q[w][k] = real ? reinterpret_cast<const u4_t *>(q)[k] ^ p.flip : u4_t{0, 0, 0, 0};
+      x.pos[w] = real ? c.seq.first() + i : -1;
+      x.lo[w] = p.window ? x.pos[w] - p.window + 1 : 0;
+    }
     // what all rows of the tile see, and what any sees
-    const int i0 = tile * 16 / p.G, i1 = min(tokens - 1, (tile * 16 + 15) / p.G);
+    const int i0 = row0 / p.G, i1 = min(tokens - 1, (row0 + kRows - 1) / p.G);
     const int pos0 = c.seq.first() + i0, pos1 = c.seq.first() + i1;
     const int any_lo = p.window ? max(0, pos0 - p.window + 1) : 0, all_lo = p.window ? max(0, pos1 - p.window + 1) : 0;
     // the steps with tokens that any row sees
@@ -450,91 +478,82 @@ __global__ __launch_bounds__(kWaves * 64, D <= 128 ? 3 : 2) void rows_kernel(KvA
       }
       x.template step<true>(raw, p.scale, t0, g, r, any_lo, pos1);
     }
-    // the waves' parts, in their order
-    x.sum = row_sum(x.sum);
-    if (__any(bad)) x.sum = __builtin_nanf("");
-    if (g == 0) {
-      stat[wave][r][0] = x.base;
-      stat[wave][r][1] = x.sum;
+    const int rows = (int)min((int64_t)kRows, (int64_t)tokens * p.G - row0);
+    if (part && threadIdx.x == 0 && stop == item0 + span) {
+      const int64_t w0 = item0 / work.share;
+      *joint = Joint{rows, (int)w0, item0 > w0 * work.share, c.seq.row0, row0, h, {0, 0}};
     }
-    __syncthreads();
-    float most = stat[0][r][0];
+    // the waves' parts, 16 rows at a time, in the waves' order
+    const bool nan = __any(bad);
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) most = fmaxf(most, stat[w][r][0]);
-    // a part that saw nothing adds nothing, whatever it holds
-    const bool saw = x.base != -__builtin_inff();
-    const float f = saw ? __builtin_amdgcn_exp2f(x.base - most) : 0.f;
+    for (int w = 0; w < R; ++w) {
+      const float base = x.base[w], sum = nan ? __builtin_nanf("") : x.sum[w][0];
+      if (g == 0) {
+        stat[wave][r][0] = base;
+        stat[wave][r][1] = sum;
+      }
+      __syncthreads();
+      float most = stat[0][r][0];
 #pragma unroll
-    for (int j = 0; j < P::tiles; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x.o[j][k] = saw ? x.o[j][k] * f : 0.f;
-    // the second four waves' go to the first four, whose are added below
-    auto exchange = [&](int place, bool add) {
+      for (int v = 1; v < kWaves; ++v) most = fmaxf(most, stat[v][r][0]);
+      // a part that saw nothing adds nothing, whatever it holds
+      const bool saw = base != -__builtin_inff();
+      const float f = saw ? __builtin_amdgcn_exp2f(base - most) : 0.f;
 #pragma unroll
       for (int k = 0; k < P::count; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          float *at4 = &acc[place][r][P::first(k, 4 * g + j)];
+          float *to = &acc[wave][r][P::first(k, 4 * g + j)];
 #pragma unroll
-          for (int n = 0; n < P::nib(k); ++n) at4[n] = x.o[P::tile0(k) + n][j] + (add ? at4[n] : 0.f);
+          for (int n = 0; n < P::nib(k); ++n) to[n] = saw ? x.o[w][P::tile0(k) + n][j] * f : 0.f;
         }
-    };
-    if constexpr (kWaves > kAdd) {
-      if (wave >= kAdd) exchange(wave - kAdd, false);
+      __syncthreads();
+      for (int e = threadIdx.x; e < min(16, rows - 16 * w) * (D / 8); e += kWaves * 64) {
+        const int rr = e / (D / 8), d = (e - rr * (D / 8)) * 8;
+        float m = stat[0][rr][0], l = 0.f, v[8] = {};
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) m = fmaxf(m, stat[i][rr][0]);
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+          const float bw = stat[i][rr][0], sw = stat[i][rr][1];
+          l += bw == -__builtin_inff() ? sw : sw * __builtin_amdgcn_exp2f(bw - m);
+#pragma unroll
+          for (int n = 0; n < 8; ++n) v[n] += acc[i][rr][d + n];
+        }
+        const int row = row0 + 16 * w + rr;
+        if (part) {
+          float *to = parts + (((int64_t)blockIdx.x * 2 + (first_item ? 0 : 1)) * p.slot_rows + 16 * w + rr) * (D + 4);
+          if (d == 0) {
+            to[D] = m;
+            to[D + 1] = l;
+          }
+          *reinterpret_cast<f4_t *>(to + d) = f4_t{v[0], v[1], v[2], v[3]};
+          *reinterpret_cast<f4_t *>(to + d + 4) = f4_t{v[4], v[5], v[6], v[7]};
+        } else {
+          const int ri = row / p.G, rh = row - ri * p.G;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+          for (int n = 0; n < 8; ++n) v[n] = l == 0.f ? 0.f : v[n] * inv;
+          store8<DT>(p.y + (int64_t)(c.seq.row0 + ri) * p.ldy + (int64_t)(h * p.G + rh) * D + d, v);
+        }
+      }
       __syncthreads();
     }
-    if (wave < kAdd) exchange(wave, kWaves > kAdd);
-    __syncthreads();
-    const int rows = (int)min((int64_t)16, (int64_t)tokens * p.G - tile * 16);
-    if (part && threadIdx.x == 0 && stop == item0 + span) {
-      const int64_t w0 = item0 / work.share;
-      *joint = Joint{rows, (int)w0, item0 > w0 * work.share, c.seq.row0, tile, h, {0, 0}};
-    }
-    for (int e = threadIdx.x; e < rows * (D / 8); e += kWaves * 64) {
-      const int rr = e / (D / 8), d = (e - rr * (D / 8)) * 8;
-      float m = stat[0][rr][0], l = 0.f, v[8] = {};
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) m = fmaxf(m, stat[w][rr][0]);
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float bw = stat[w][rr][0], sw = stat[w][rr][1];
-        l += bw == -__builtin_inff() ? sw : sw * __builtin_amdgcn_exp2f(bw - m);
-      }
-#pragma unroll
-      for (int w = 0; w < kAdd; ++w)
-#pragma unroll
-        for (int n = 0; n < 8; ++n) v[n] += acc[w][rr][d + n];
-      if (part) {
-        float *to = parts + (((int64_t)blockIdx.x * 2 + (first_item ? 0 : 1)) * p.slot_rows + rr) * (D + 4);
-        if (d == 0) {
-          to[D] = m;
-          to[D + 1] = l;
-        }
-        *reinterpret_cast<f4_t *>(to + d) = f4_t{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<f4_t *>(to + d + 4) = f4_t{v[4], v[5], v[6], v[7]};
-      } else {
-        const int ri = (tile * 16 + rr) / p.G, rh = (tile * 16 + rr) - ri * p.G;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) v[n] = l == 0.f ? 0.f : v[n] * inv;
-        store8<DT>(p.y + (int64_t)(c.seq.row0 + ri) * p.ldy + (int64_t)(h * p.G + rh) * D + d, v);
-      }
-    }
-    __syncthreads();
     at = stop;
     first_item = false;
   }
 }
 
 // The parts of items that lie in more than one workgroup's share, joined by a workgroup for each that holds the end of
-// one.  Groups of threads take the parts in turn, and the groups' results meet in their order.
+// one, 16 rows each.  Groups of threads take the parts in turn, and the groups' results meet in their order.
 constexpr int kJoinThreads = 1024;
 template <int DT, int D>
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(KvAttnParams p) {
   const Joint j = reinterpret_cast<const Joint *>(p.part)[blockIdx.x];
-  if (j.rows == 0) return;
+  const int from_row = 16 * blockIdx.y, rows = min(16, j.rows - from_row);
+  if (rows <= 0) return;
   const float *parts = p.part + (int64_t)p.workgroups * (sizeof(Joint) / 4);
-  const int n = (int)blockIdx.x - j.first + 1, slots = j.rows * (D / 4);   // at most 1024, of 16 rows of 256
+  const int n = (int)blockIdx.x - j.first + 1, slots = rows * (D / 4);   // at most 1024, of 16 rows of 256
   const int groups = kJoinThreads / slots, t = threadIdx.x, group = t / slots, s = t - group * slots;
   const int rr = s / (D / 4), d = (s - rr * (D / 4)) * 4;
   __shared__ f4_t sums[kJoinThreads];
@@ -556,7 +575,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(KvAttnParams p) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int part = min(i + k * groups, n - 1);     // (again, where there is none)
-        const float *from = parts + (((int64_t)(j.first + part) * 2 + (part == 0 && j.second)) * p.slot_rows + rr) * (D + 4);
+        const float *from = parts + (((int64_t)(j.first + part) * 2 + (part == 0 && j.second)) * p.slot_rows + from_row + rr) * (D + 4);
         bw[k] = from[D];
         sw[k] = from[D + 1];
         o[k] = *reinterpret_cast<const f4_t *>(from + d);
@@ -571,7 +590,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(KvAttnParams p) {
   __syncthreads();
   if (group != 0) return;
   for (int k = 1; k < groups; ++k) add(stat[s + k * slots][0], stat[s + k * slots][1], sums[s + k * slots]);
-  const int row = j.tile * 16 + rr, ri = row / p.G, rh = row - ri * p.G;
+  const int row = j.row + from_row + rr, ri = row / p.G, rh = row - ri * p.G;
   uint16_t *y = p.y + (int64_t)(j.row0 + ri) * p.ldy + (int64_t)(j.head * p.G + rh) * D + d;
   if (l == 0.f) v = f4_t{0.f, 0.f, 0.f, 0.f};
   else v *= 1.f / l;
@@ -580,10 +599,12 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(KvAttnParams p) {
 
 template <int DT, int D>
 hipError_t launch(const KvAttnParams &p, hipStream_t s) {
-  hipLaunchKernelGGL((rows_kernel<DT, D>), dim3((uint32_t)p.workgroups), dim3(kWaves * 64), 0, s, p);
+  const dim3 grid((uint32_t)p.workgroups), block(kWaves * 64);
+  if (p.tile_rows == 16) hipLaunchKernelGGL((rows_kernel<DT, D, 1>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((rows_kernel<DT, D, 2>), grid, block, 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.whole) return e;
-  hipLaunchKernelGGL((join_kernel<DT, D>), dim3((uint32_t)p.workgroups), dim3(kJoinThreads), 0, s, p);
+  hipLaunchKernelGGL((join_kernel<DT, D>), dim3((uint32_t)p.workgroups, p.tile_rows / 16), dim3(kJoinThreads), 0, s, p);
   return hipGetLastError();
 }
 template <int DT>
@@ -601,16 +622,20 @@ hipError_t by_head(const KvAttnParams &p, hipStream_t s) {
 
 KvPlan kv_attn_plan(const KvCache &c, const KvRows &r, int G, int window) {
   KvPlan k{};
-  // tiles of 16 rows: at most one short one for each sequence
-  const int64_t tiles = r.starts ? (int64_t)r.rows * G / 16 + r.batch : (int64_t)r.batch * ((G + 15) / 16);
-  k.items = tiles * c.heads;
   int64_t tokens = (int64_t)r.width << c.shift;
   if (window && tokens > (int64_t)window + r.rows + kStep) tokens = (int64_t)window + r.rows + kStep;
   const int64_t steps = (tokens + kStep - 1) / kStep + 1;
-  k.slot_rows = r.starts ? 16 : G < 16 ? G : 16;
-  const int64_t most = k.items * steps / kLeast + 1;
-  k.whole = k.items >= 4 * kCUs || steps <= 32;
-  k.workgroups = (int)(k.whole ? k.items : most < 3 * kCUs ? most : 3 * kCUs);
+  // at most one short tile for each sequence
+  auto tiles = [&](int rows) { return r.starts ? (int64_t)r.rows * G / rows + r.batch : (int64_t)r.batch * ((G + rows - 1) / rows); };
+  // Tiles of 32 rows read and expand the cache half as often, where sequences have more than 16 rows and
+  // there is work for every CU.
+  const int64_t rows = r.starts ? (int64_t)r.rows * G / r.batch : G;
+  k.tile_rows = rows > 16 && tiles(32) * c.heads * steps >= (int64_t)resident(c.D, 2) * kCUs * kLeast ? 32 : 16;
+  k.items = tiles(k.tile_rows) * c.heads;
+  k.slot_rows = r.starts || G > k.tile_rows ? k.tile_rows : G;
+  const int64_t most = k.items * steps / kLeast + 1, room = resident(c.D, k.tile_rows / 16) * kCUs;
+  k.whole = k.items >= 2 * room || steps <= 32;
+  k.workgroups = (int)(k.whole ? k.items : most < room ? most : room);
   k.bytes = k.whole ? 0 : (size_t)k.workgroups * (sizeof(Joint) + (size_t)2 * k.slot_rows * (c.D + 4) * 4);
   return k;
 }
