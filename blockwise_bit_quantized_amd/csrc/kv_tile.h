@@ -1,0 +1,372 @@
+// kv_tile.h -- the mathematics of attention over the paged FP4 cache that its kernels share: a wave's tile of rows, the
+// loads of a step, and a workgroup's place in the work.
+#pragma once
+
+#include <type_traits>
+
+#include "decode.h"
+
+namespace mnb {
+
+constexpr int kStep = 32;      // tokens of a wave's step
+constexpr int kWaves = 4;      // of a workgroup
+
+typedef __bf16 b8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 hh_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bb_t __attribute__((ext_vector_type(2)));
+
+template <int DT>
+__device__ __forceinline__ f4_t mfma16(u4_t a, u4_t b, f4_t c) {
+  if constexpr (DT == DT_F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8_t, a), __builtin_bit_cast(h8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8_t, a), __builtin_bit_cast(b8_t, b), c, 0, 0, 0);
+}
+// two numbers rounded to nearest even, in one instruction
+template <int DT>
+__device__ __forceinline__ uint32_t round2(float a, float b) {
+  const f2_t v = {a, b};
+  if constexpr (DT == DT_F16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, hh_t));
+  else return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bb_t));
+}
+// byte B of w as two 16-bit numbers, times the power of two in the exponent field of `s`
+template <int DT, int B>
+__device__ __forceinline__ uint32_t expand2(uint32_t w, uint32_t s) {
+  const float f = __builtin_bit_cast(float, s);
+  if constexpr (DT == DT_F16) return __builtin_bit_cast(uint32_t, (hh_t)__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, f, B));
+  else return __builtin_bit_cast(uint32_t, (bb_t)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, B));
+}
+template <int DT>
+__device__ __forceinline__ u4_t expand8(uint32_t w, uint32_t s) {
+  return u4_t{expand2<DT, 0>(w, s), expand2<DT, 1>(w, s), expand2<DT, 2>(w, s), expand2<DT, 3>(w, s)};
+}
+// scale byte I of w in the exponent field (the conversion reads nothing else of it)
+template <int I>
+__device__ __forceinline__ uint32_t scale_of(uint32_t w) {
+  if constexpr (I < 3) return w << (23 - 8 * I);
+  else return w >> 1;
+}
+
+// The value operand's parts: 16 lanes share 128, 64 or 32 elements, 8, 4 or 2 each; lane r of part k has the
+// elements d0 + 8 word + (first nibble) + j of unit `word`.
+template <int D> struct Parts {
+  static constexpr int n8 = D / 128, n4 = D % 128 / 64, n2 = D % 64 / 32, count = n8 + n4 + n2, tiles = D / 16;
+  static constexpr int nib(int k) { return k < n8 ? 8 : k < n8 + n4 ? 4 : 2; }
+  static constexpr int d0(int k) { return k < n8 ? 128 * k : k < n8 + n4 ? 128 * n8 : 128 * n8 + 64 * n4; }
+  static constexpr int tile0(int k) { return d0(k) / 16; }
+  __device__ static __forceinline__ int word(int k, int r) { return d0(k) / 8 + (nib(k) == 8 ? r : nib(k) == 4 ? r & 7 : r & 3); }
+  __device__ static __forceinline__ int shift(int k, int r) { return nib(k) == 8 ? 0 : nib(k) == 4 ? 16 * (r >> 3) : 8 * (r >> 2); }
+  // first of the elements that row r of the tiles of part k holds (r = 4 g + i in a result)
+  __device__ static __forceinline__ int first(int k, int r) { return 8 * word(k, r) + shift(k, r) / 4; }
+};
+
+// largest of the four lanes of a row
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+template <int DT, int D, int R>
+struct Tile {
+  typedef Parts<D> P;
+  static constexpr int KS = D / 32;                       // matrix instructions along the head
+  static constexpr float kOff = DT == DT_F16 ? 6.f : 0.f; // fp16 keeps small probabilities by 2^6
+  static constexpr uint32_t kFar = DT == DT_F16 ? 141 : 253;   // first scale whose values may pass q's type
+  u4_t q[R][KS];
+  f4_t o[R][P::tiles];
+  float base[R];           // what scores are taken against
+  f4_t sum[R];             // the sum of the row's probabilities, in every place, as a product with ones
+  int pos[R], lo[R];       // the row sees tokens lo .. pos
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+#pragma unroll
+      for (int j = 0; j < P::tiles; ++j) o[x][j] = f4_t{0.f, 0.f, 0.f, 0.f};
+      base[x] = -__builtin_inff();
+      sum[x] = f4_t{0.f, 0.f, 0.f, 0.f};
+    }
+  }
+
+  // O^T += V^T P^T for 32 tokens; with `only`, rows that do not see the token keep theirs
+  template <bool ONLY>
+  __device__ __forceinline__ void values(const u4_t *va, const u4_t *vb, const uint32_t *sa, const uint32_t *sb, const u4_t *prob, int r,
+                                         const bool *sees) {
+#pragma unroll
+    for (int k = 0; k < P::count; ++k) {
+      const int sh = P::shift(k, r);
+      uint32_t a[4], b[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        a[t] = P::nib(k) == 8 ? va[k][t] : va[k][t] >> sh;
+        b[t] = P::nib(k) == 8 ? vb[k][t] : vb[k][t] >> sh;
+      }
+      auto pair = [&](auto byte) {
+        constexpr int B = decltype(byte)::value;
+        const uint32_t a0 = expand2<DT, B>(a[0], scale_of<0>(sa[k])), a1 = expand2<DT, B>(a[1], scale_of<1>(sa[k]));
+        const uint32_t a2 = expand2<DT, B>(a[2], scale_of<2>(sa[k])), a3 = expand2<DT, B>(a[3], scale_of<3>(sa[k]));
+        const uint32_t b0 = expand2<DT, B>(b[0], scale_of<0>(sb[k])), b1 = expand2<DT, B>(b[1], scale_of<1>(sb[k]));
+        const uint32_t b2 = expand2<DT, B>(b[2], scale_of<2>(sb[k])), b3 = expand2<DT, B>(b[3], scale_of<3>(sb[k]));
+        constexpr uint32_t L = 0x05040100u, H = 0x07060302u;
+        const u4_t lo4 = {__builtin_amdgcn_perm(a1, a0, L), __builtin_amdgcn_perm(a3, a2, L), __builtin_amdgcn_perm(b1, b0, L),
+                          __builtin_amdgcn_perm(b3, b2, L)};
+        const u4_t hi4 = {__builtin_amdgcn_perm(a1, a0, H), __builtin_amdgcn_perm(a3, a2, H), __builtin_amdgcn_perm(b1, b0, H),
+                          __builtin_amdgcn_perm(b3, b2, H)};
+#pragma unroll
+        for (int w = 0; w < R; ++w) {
+          f4_t &x = o[w][P::tile0(k) + 2 * B], &y = o[w][P::tile0(k) + 2 * B + 1];
+          if constexpr (ONLY) {
+            const f4_t zero = {0.f, 0.f, 0.f, 0.f};
+            const f4_t dx = mfma16<DT>(lo4, prob[w], zero), dy = mfma16<DT>(hi4, prob[w], zero);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[i] += sees[w] ? dx[i] : 0.f;
+              y[i] += sees[w] ? dy[i] : 0.f;
+            }
+          } else {
+            x = mfma16<DT>(lo4, prob[w], x);
+            y = mfma16<DT>(hi4, prob[w], y);
+          }
+        }
+      };
+      pair(std::integral_constant<int, 0>());
+      if (P::nib(k) >= 4) pair(std::integral_constant<int, 1>());
+      if (P::nib(k) == 8) {
+        pair(std::integral_constant<int, 2>());
+        pair(std::integral_constant<int, 3>());
+      }
+    }
+  }
+
+  // What a step reads: 16 tokens each of two places, K and V with their scales.
+  struct Raw {
+    uint32_t kw[2][KS], ke[2][2];
+    u4_t v[2][P::count];
+    uint32_t vs[2][P::count];
+  };
+  // a lane's offsets from the first token's place in each of a page's four arrays: all of a step's addresses are these
+  // over bases in scalar registers
+  struct Offsets {
+    uint32_t k, ke[2], v[P::count], vs[P::count];
+    __device__ __forceinline__ Offsets(int g, int r) {
+      k = r * (D / 2) + g * (D / 8);
+      ke[0] = r * (D / 32) + g * (D / 4) / 32;
+      ke[1] = r * (D / 32) + (g * (D / 4) + D / 4 - 1) / 32;
+#pragma unroll
+      for (int p = 0; p < P::count; ++p) {
+        v[p] = (g * (D / 8) + P::word(p, r)) * 16;
+        vs[p] = (g * (D / 32) + P::word(p, r) / 4) * 4;
+      }
+    }
+  };
+  // head: the page of this head; in: the first token's place in it, a multiple of 16
+  __device__ static __forceinline__ void load(Raw &x, int half, const uint8_t *head, uint32_t in, uint32_t S, const Offsets &o) {
+    const uint8_t *k = head + in * (D / 2), *ke = head + (S * D + in * (D / 32)), *v = head + (S + in) * (D / 2),
+                  *vs = head + (S * D + (S + in) * (D / 32));
+#pragma unroll
+    for (int i = 0; i < KS; ++i) x.kw[half][i] = reinterpret_cast<const uint32_t *>(k + o.k)[i];
+    x.ke[half][0] = ke[o.ke[0]];
+    // a lane's fourth of the head lies in one block where D is 64 or 128
+    x.ke[half][1] = D == 64 || D == 128 ? 0 : ke[o.ke[1]];
+#pragma unroll
+    for (int p = 0; p < P::count; ++p) {
+      x.v[half][p] = *reinterpret_cast<const u4_t *>(v + o.v[p]);
+      x.vs[half][p] = *reinterpret_cast<const uint32_t *>(vs + o.vs[p]);
+    }
+  }
+
+  // base and sum raised where a score passes, and the probabilities of scores s against it
+  __device__ __forceinline__ void soften(const f4_t (*s)[2], float scale, u4_t *prob) {
+    float most[R];
+    bool raise = false;
+#pragma unroll
+    for (int w = 0; w < R; ++w) {
+      const f4_t *t = s[w];
+      most[w] = fmaxf(fmaxf(fmaxf(t[0][0], t[0][1]), fmaxf(t[0][2], t[0][3])), fmaxf(fmaxf(t[1][0], t[1][1]), fmaxf(t[1][2], t[1][3]))) * scale;
+      raise |= most[w] > base[w] + (kOff + 8.f);
+    }
+    if (__any(raise)) {
+#pragma unroll
+      for (int w = 0; w < R; ++w) {
+        const float now = fmaxf(base[w], row_max(most[w]) - kOff);
+        const float f = now == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(base[w] - now);
+        base[w] = now;
+        sum[w] *= f;
+#pragma unroll
+        for (int j = 0; j < P::tiles; ++j) o[w][j] *= f;
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < R; ++w) {
+      const float from = base[w] == -__builtin_inff() ? 0.f : base[w];
+      float t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = __builtin_amdgcn_exp2f(fmaf(s[w][i >> 2][i & 3], scale, -from));
+      prob[w] = u4_t{round2<DT>(t[0], t[1]), round2<DT>(t[2], t[3]), round2<DT>(t[4], t[5]), round2<DT>(t[6], t[7])};
+      constexpr uint32_t one = DT == DT_F16 ? 0x3c003c00u : 0x3f803f80u;
+      sum[w] = mfma16<DT>(u4_t{one, one, one, one}, prob[w], sum[w]);
+    }
+  }
+
+  // 32 tokens from t0; EDGE: some row does not see some of them
+  template <bool EDGE>
+  __device__ __forceinline__ void step(const Raw &raw, float scale, int t0, int g, int r, int tile_lo, int tile_hi) {
+    f4_t s[R][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int w = 0; w < R; ++w) s[w][h] = f4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        const bool later = D != 64 && D != 128 && (g * (D / 4) + 8 * i) / 32 != g * (D / 4) / 32;
+        const u4_t k = expand8<DT>(raw.kw[h][i], (later ? raw.ke[h][1] : raw.ke[h][0]) << 23);
+#pragma unroll
+        for (int w = 0; w < R; ++w) s[w][h] = mfma16<DT>(k, q[w][i], s[w][h]);
+      }
+    }
+    if constexpr (EDGE) {
+#pragma unroll
+      for (int w = 0; w < R; ++w)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
+          s[w][i >> 2][i & 3] = tok < lo[w] || tok > pos[w] ? -__builtin_inff() : s[w][i >> 2][i & 3];
+        }
+    }
+    u4_t prob[R];
+    soften(s, scale, prob);
+    if constexpr (!EDGE) {
+      values<false>(raw.v[0], raw.v[1], raw.vs[0], raw.vs[1], prob, r, nullptr);
+      return;
+    }
+    // Tokens that no row sees may hold anything: their scales become 0.  Of the others, one whose values
+    // are no numbers of q's type must not reach a row that does not see it (0 times infinity): such tokens go
+    // one at a time, into the rows that do.
+    uint32_t far = 0, keep_a = 0, keep_b = 0, sa[P::count], sb[P::count], na[P::count], nb[P::count];   // n: without the far ones
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int a = t0 + 4 * g + i, b = a + 16;
+      if (a >= tile_lo && a <= tile_hi) keep_a |= 0xffu << (8 * i);
+      if (b >= tile_lo && b <= tile_hi) keep_b |= 0xffu << (8 * i);
+    }
+#pragma unroll
+    for (int k = 0; k < P::count; ++k) {
+      sa[k] = raw.vs[0][k] & keep_a;
+      sb[k] = raw.vs[1][k] & keep_b;
+      uint32_t fa = 0, fb = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if ((sa[k] >> (8 * i) & 255) >= kFar) fa |= 0xffu << (8 * i);
+        if ((sb[k] >> (8 * i) & 255) >= kFar) fb |= 0xffu << (8 * i);
+      }
+      na[k] = sa[k] & ~fa;
+      nb[k] = sb[k] & ~fb;
+      far |= fa | fb;
+    }
+    values<false>(raw.v[0], raw.v[1], na, nb, prob, r, nullptr);
+    if (!__any(far != 0)) return;
+    for (int x = 0; x < 32; ++x) {                       // token t0 + x: lanes of group (x & 15) / 4, place x & 3
+      const bool mine = (x & 15) >> 2 == g;
+      const uint32_t byte = mine ? 0xffu << (8 * (x & 3)) : 0;
+      uint32_t oa[P::count], ob[P::count], any = 0;
+#pragma unroll
+      for (int k = 0; k < P::count; ++k) {
+        oa[k] = x < 16 ? sa[k] & ~na[k] & byte : 0;
+        ob[k] = x < 16 ? 0 : sb[k] & ~nb[k] & byte;
+        any |= oa[k] | ob[k];
+      }
+      if (!__any(any != 0)) continue;
+      // probabilities of this token alone
+      const uint32_t half = 0xffffu << (16 * (x & 1));
+      u4_t one[R];
+      bool sees[R];
+#pragma unroll
+      for (int w = 0; w < R; ++w) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) one[w][i] = mine && i == (x >> 4) * 2 + ((x & 3) >> 1) ? prob[w][i] & half : 0;
+        sees[w] = t0 + x >= lo[w] && t0 + x <= pos[w];
+      }
+      values<true>(raw.v[0], raw.v[1], oa, ob, one, r, sees);
+    }
+  }
+};
+
+// How a sequence's work is cut: its tiles of 16 or 32 rows, and the tokens that any of its rows sees.
+struct Cut {
+  KvSeq seq;
+  int tiles, from, steps;      // from: a multiple of kStep
+  bool beyond;                 // more tokens than the pages hold: its rows become NaN
+};
+__device__ __forceinline__ Cut cut_of(const KvAttnParams &p, int b) {
+  Cut c;
+  c.seq = kv_seq(p.rows, b);
+  c.tiles = (int)(((int64_t)c.seq.n * p.G + p.tile_rows - 1) / p.tile_rows);
+  const int lo = p.window ? max(0, c.seq.first() - p.window + 1) : 0;
+  c.from = lo / kStep * kStep;
+  c.beyond = c.seq.len > p.rows.width << p.cache.shift;
+  // a row that sees nothing is written too
+  c.steps = c.beyond ? 1 : max(1, (c.seq.len - c.from + kStep - 1) / kStep);
+  return c;
+}
+__device__ __forceinline__ int64_t cost_of(const KvAttnParams &p, int b) {
+  if (b >= p.rows.batch) return 0;
+  const Cut c = cut_of(p, b);
+  return (int64_t)c.tiles * p.cache.heads * (p.whole ? 1 : c.steps);
+}
+
+// Sums over the wave's lanes up to this one.  (Every wave finds the workgroup's place in the work by itself.)
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t o = __shfl_up((long long)v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+__device__ __forceinline__ int64_t lane_of(int64_t v, int lane) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+                   (uint32_t)__builtin_amdgcn_readlane((int)v, lane));
+}
+// The workgroup's steps [at, end) of the work (none left: end 0), and the sequence that holds `at` with the place where
+// it begins.
+struct Work {
+  int64_t at, end, begin, share;
+  int b;
+};
+__device__ __forceinline__ Work find_work(const KvAttnParams &p) {
+  Work w{};
+  const int lane = threadIdx.x & 63;
+  w.share = 1;
+  if (p.whole && !p.rows.starts) {                       // as many items for each sequence
+    const int each = (p.G + p.tile_rows - 1) / p.tile_rows * p.cache.heads;
+    w.at = blockIdx.x;
+    w.end = w.at + 1;
+    w.b = blockIdx.x / each;
+    w.begin = (int64_t)w.b * each;
+    return w;
+  }
+  const int64_t first = cost_of(p, lane), first_run = wave_scan(first);
+  if (!p.whole) {
+    int64_t total = lane_of(first_run, 63);
+    for (int b0 = 64; b0 < p.rows.batch; b0 += 64) total += lane_of(wave_scan(cost_of(p, b0 + lane)), 63);
+    w.share = (total + p.workgroups - 1) / p.workgroups;
+    if (w.share < 2 * kWaves) w.share = 2 * kWaves;       // no smaller parts than two steps a wave
+  }
+  w.at = (int64_t)blockIdx.x * w.share;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < p.rows.batch; b0 += 64) {
+    const int64_t mine = b0 ? cost_of(p, b0 + lane) : first, run = (b0 ? wave_scan(mine) : first_run) + before;
+    const uint64_t hit = __ballot(run > w.at);
+    before = lane_of(run, 63);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      w.b = b0 + l;
+      w.begin = lane_of(run - mine, l);
+      w.end = w.at + w.share;
+      break;
+    }
+  }
+  return w;
+}
+
+}  // namespace mnb

@@ -458,3 +458,101 @@ def test_sample_frequencies():
     u = ((torch.arange(4000, device=DEV).double() + 0.5) / 4000).float()
     got = np.bincount(mnb.sample(x, u).cpu().numpy(), minlength=5)
     assert (np.abs(got - 4000 * p) <= 1).all()
+
+
+# ------------------------------------------------------------------------------------------
+# attention of many rows (its reference in 64 bits on the GPU, by heads)
+# ------------------------------------------------------------------------------------------
+
+
+def attention64(q, k, v, first, scale, window):
+    """dref.attention for [n, Hq, D] float64 tensors on the GPU: (y, sum of |p v|)."""
+    n, hq, _ = q.shape
+    p = first + torch.arange(n, device=DEV)[:, None]
+    t = torch.arange(k.shape[0], device=DEV)[None]
+    hidden = (t > p) | ((t <= p - window) if window else torch.zeros_like(t > p))
+    blank = hidden.all(1)
+    y, size = torch.zeros_like(q), torch.zeros_like(q)
+    for h in range(hq):
+        kh, vh = (x[:, h // (hq // x.shape[1])].contiguous() for x in (k, v))
+        s = (q[:, h].contiguous() @ kh.t().contiguous() * scale).masked_fill(hidden, -float("inf"))
+        e = torch.softmax(s, 1).masked_fill(blank[:, None], 0.0)
+        y[:, h], size[:, h] = e @ vh, e @ vh.abs()
+    return y, size
+
+
+def route(s, hq, rows, starts, window):
+    c = mnb.mnb_kv_cache(None, 0, s.cache.pages, s.hkv, s.D, s.S)
+    r = mnb.mnb_kv_rows(None, 0, None, 1 if starts else None, len(s.lengths_host), s.width, rows)
+    return mnb.mnb_kv_describe_route(c, r, hq, window)[1]
+
+
+MANY = [  # lengths, starts, hq, hkv, D, page, window
+    ([1100, 300], [0, 1100, 1250], 64, 64, 64, 16, 0),
+    ([700, 0, 650], [0, 700, 700, 1333], 52, 26, 96, 32, 100),
+    ([2500], [0, 2111], 32, 8, 128, 64, 0),
+    ([900, 1500, 40], [0, 333, 1600, 1640], 40, 40, 128, 128, 333),
+    ([1000], [0, 1000], 36, 36, 192, 16, 0),
+    ([1300, 129], [0, 777, 906], 40, 20, 256, 256, 0),
+    ([500, 600], [0, 503, 1100], 56, 56, 128, 16, 0),             # rows before a sequence's first token
+]
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_attention_of_many_rows(case, dtype):
+    lengths, starts, hq, hkv, D, S, window = MANY[case]
+    t, r = DT[dtype], rng(20, case)
+    s = Setup(r, lengths, hkv, D, S)
+    total = sum(lengths)
+    g = torch.Generator(device=DEV).manual_seed(case)
+    k, v, q = (torch.randn(n, h, D, generator=g, device=DEV).mul(torch.exp(0.3 * torch.randn(h, D, generator=g, device=DEV))).to(t)
+               for n, h in ((total, hkv), (total, hkv), (starts[-1], hq)))
+    whole = [0, *np.cumsum(lengths).tolist()]
+    mnb.kv_append(None, k, v, s.cache, s.pages, s.lengths, starts=ints(whole))
+    assert route(s, hq, starts[-1], starts, window).startswith("kv_prefill")
+    out = torch.full_like(q, 7.0)
+    y = mnb.kv_attention(q, s.cache, s.pages, s.lengths, starts=ints(starts), window=window, out=out)
+    kq, vq = mnb.kv_read(s.cache, s.pages, s.lengths, total, starts=ints(whole), dtype=torch.float32)
+    for b, n in enumerate(lengths):
+        a, e = starts[b], starts[b + 1]
+        if a == e:
+            continue
+        kb, vb = kq[whole[b]:whole[b + 1]].double(), vq[whole[b]:whole[b + 1]].double()
+        want, size = attention64(q[a:e].double(), kb, vb, n - (e - a), D ** -0.5, window)
+        score = float((q[a:e].double().abs().amax(0) * 1.0).amax() * kb.abs().amax()) * D ** 0.5
+        err = (y[a:e].double() - want).abs()
+        assert bool((err <= torch.from_numpy(bound(f64(want), f64(size), t, min(score, 60.0), n, D)).to(DEV)).all()), (b, float(err.max()))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_rows_and_what_they_do_not_see(D):
+    """NaN among later tokens, and in the bytes behind a sequence, reaches no earlier row."""
+    n, H, S, t = 700, 96 if D < 256 else 48, 64, torch.bfloat16
+    s = Setup(rng(21), [n], H, D, S)
+    g = torch.Generator(device=DEV).manual_seed(D)
+    q, k, v = (torch.randn(n, H, D, generator=g, device=DEV).to(t) for _ in range(3))
+    v[600, 3, D - 1] = v[333, 0, 0] = float("nan")
+    k[500, 2, 5] = float("inf")
+    mnb.kv_append(None, k, v, s.cache, s.pages, s.lengths, starts=ints([0, n]))
+    assert route(s, H, n, [0, n], 0).startswith("kv_prefill")
+    y = mnb.kv_attention(q, s.cache, s.pages, s.lengths, starts=ints([0, n]))
+    bad = torch.zeros(n, H, D, dtype=torch.bool, device=DEV)
+    bad[600:, 3, D - 32:] = bad[333:, 0, :32] = bad[500:, 2] = True
+    assert torch.equal(y.isnan(), bad)
+
+
+def test_many_rows_out_of_reach():
+    """A page out of range, and more tokens than the pages hold: the rows of that sequence are NaN, others not; rows behind the
+    last sequence stay."""
+    n, H, D, S, t = 520, 44, 64, 64, torch.float16
+    s = Setup(rng(22), [n, n, n + 200], H, D, S, width=9)
+    s.data.zero_()
+    s.pages[1, 4] = s.cache.pages
+    q = torch.randn(3 * n + 5, H, D, device=DEV).to(t)
+    out = torch.full_like(q, 7.0)
+    starts = [0, n, 2 * n, 3 * n]
+    assert route(s, H, 3 * n + 5, starts, 0).startswith("kv_prefill")
+    mnb.kv_attention(q, s.cache, s.pages, s.lengths, starts=ints(starts), out=out)
+    assert not bool(out[:n].isnan().any()) and bool((out[3 * n:] == 7).all())
+    assert bool(out[n + 64 * 4 + 128:2 * n].isnan().all()) and bool(out[2 * n:3 * n].isnan().all())
