@@ -157,29 +157,36 @@ __global__ __launch_bounds__(kWaves * 64, 2) void prefill_kernel(KvAttnParams p)
     get(next, 1);
     __syncthreads();
     for (int n = 0; n < count; ++n) {
+      // All of a product's operands are asked for before its first instruction: LDS answers after some hundred
+      // cycles, which two at a time would be paid eight times.
       const u4_t(*at)[64] = frag[n & 1];
+      u4_t use[2 * KS];
+#pragma unroll
+      for (int i = 0; i < 2 * KS; ++i) use[i] = at[i][lane];
+      __builtin_amdgcn_sched_barrier(0);
       f4_t s[R][2];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
 #pragma unroll
         for (int w = 0; w < R; ++w) s[w][half] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          const u4_t k = at[half * KS + i][lane];
+        for (int i = 0; i < KS; ++i)
 #pragma unroll
-          for (int w = 0; w < R; ++w) s[w][half] = mfma16<DT>(k, x.q[w][i], s[w][half]);
-        }
+          for (int w = 0; w < R; ++w) s[w][half] = mfma16<DT>(use[half * KS + i], x.q[w][i], s[w][half]);
       }
+      __builtin_amdgcn_sched_barrier(0);
+      static_assert(P::tiles == 2 * KS, "as many operands of values as of keys");
+#pragma unroll
+      for (int j = 0; j < P::tiles; ++j) use[j] = at[2 * KS + j][lane];
+      __builtin_amdgcn_sched_barrier(0);
       expand(next, frag[(n + 1) & 1]);                   // (a copy of the last, behind it)
       get(next, n + 2);
       u4_t prob[R];
       x.soften(s, p.scale, prob);
 #pragma unroll
-      for (int j = 0; j < P::tiles; ++j) {
-        const u4_t v = at[2 * KS + j][lane];
+      for (int j = 0; j < P::tiles; ++j)
 #pragma unroll
-        for (int w = 0; w < R; ++w) x.o[w][j] = mfma16<DT>(v, prob[w], x.o[w][j]);
-      }
+        for (int w = 0; w < R; ++w) x.o[w][j] = mfma16<DT>(use[j], prob[w], x.o[w][j]);
       __syncthreads();
     }
   }

@@ -174,34 +174,40 @@ struct Tile {
     }
   }
 
-  // base and sum raised where a score passes, and the probabilities of scores s against it
+  // The probabilities of scores s against the base, which is raised, and what was summed lowered, where a score passes it far.
+  // (The maxima are taken of what the multiplication gives: of the matrix instruction's own results each would cost
+  // another instruction, to quiet a NaN.)
   __device__ __forceinline__ void soften(const f4_t (*s)[2], float scale, u4_t *prob) {
-    float most[R];
+    float t[R][8], most[R];
     bool raise = false;
 #pragma unroll
     for (int w = 0; w < R; ++w) {
-      const f4_t *t = s[w];
-      most[w] = fmaxf(fmaxf(fmaxf(t[0][0], t[0][1]), fmaxf(t[0][2], t[0][3])), fmaxf(fmaxf(t[1][0], t[1][1]), fmaxf(t[1][2], t[1][3]))) * scale;
-      raise |= most[w] > base[w] + (kOff + 8.f);
+      const float from = base[w] == -__builtin_inff() ? 0.f : base[w];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[w][i] = fmaf(s[w][i >> 2][i & 3], scale, -from);
+      most[w] = fmaxf(fmaxf(fmaxf(t[w][0], t[w][1]), fmaxf(t[w][2], t[w][3])), fmaxf(fmaxf(t[w][4], t[w][5]), fmaxf(t[w][6], t[w][7])));
+      raise |= most[w] > (base[w] == -__builtin_inff() ? -__builtin_inff() : kOff + 8.f);
     }
     if (__any(raise)) {
 #pragma unroll
       for (int w = 0; w < R; ++w) {
-        const float now = fmaxf(base[w], row_max(most[w]) - kOff);
+        const float from = base[w] == -__builtin_inff() ? 0.f : base[w];
+        const float now = fmaxf(base[w], row_max(most[w] + from) - kOff);
         const float f = now == -__builtin_inff() ? 1.f : __builtin_amdgcn_exp2f(base[w] - now);
+        const float by = from - (now == -__builtin_inff() ? 0.f : now);
         base[w] = now;
         sum[w] *= f;
 #pragma unroll
         for (int j = 0; j < P::tiles; ++j) o[w][j] *= f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[w][i] += by;
       }
     }
 #pragma unroll
     for (int w = 0; w < R; ++w) {
-      const float from = base[w] == -__builtin_inff() ? 0.f : base[w];
-      float t[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = __builtin_amdgcn_exp2f(fmaf(s[w][i >> 2][i & 3], scale, -from));
-      prob[w] = u4_t{round2<DT>(t[0], t[1]), round2<DT>(t[2], t[3]), round2<DT>(t[4], t[5]), round2<DT>(t[6], t[7])};
+      for (int i = 0; i < 8; ++i) t[w][i] = __builtin_amdgcn_exp2f(t[w][i]);
+      prob[w] = u4_t{round2<DT>(t[w][0], t[w][1]), round2<DT>(t[w][2], t[w][3]), round2<DT>(t[w][4], t[w][5]), round2<DT>(t[w][6], t[w][7])};
       constexpr uint32_t one = DT == DT_F16 ? 0x3c003c00u : 0x3f803f80u;
       sum[w] = mfma16<DT>(u4_t{one, one, one, one}, prob[w], sum[w]);
     }
