@@ -27,7 +27,7 @@ BINDING_SOURCE = "binding.cpp"
 OBJ = os.path.join(PKG, "_build")
 SOURCES = ["api.hip", "gemv.hip", "gemv_mfma.hip", "gemv_acc4.hip", "tproj.hip", "gemm.hip", "pack.hip",
            "api_ops.hip", "mx_quant.hip", "mx_gemv.hip", "mx_gemm.hip", "rmsnorm.hip", "logprobs.hip",
-           "api_decode.hip", "kv_append.hip", "kv_attention.hip", "kv_prefill.hip", "sample.hip"]
+           "api_decode.hip", "kv_append.hip", "kv_attention.hip", "sample.hip"]
 ARCH = os.environ.get("MNB_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

@@ -177,7 +177,7 @@ int mnb_kv_describe_route(const mnb_kv_cache *cache, const mnb_kv_rows *rows, in
     return MNB_OK;
   }
   const KvPlan k = kv_attn_plan(cache_of(cache), rows_of(rows), q_heads / cache->kv_heads, window_of(cache, rows, window));
-  snprintf(buf, buf_len, "%s tile=%d workgroups=%d%s", k.many ? "kv_prefill" : "kv_rows", k.tile_rows, k.workgroups, k.whole ? "" : " join");
+  snprintf(buf, buf_len, "kv_attention tile=%d workgroups=%d%s", k.tile_rows, k.workgroups, k.whole ? "" : " join");
   return MNB_OK;
 }
 
@@ -215,7 +215,7 @@ int mnb_kv_attention(const mnb_kv_cache *cache, const mnb_kv_rows *rows, const v
   p.tile_rows = k.tile_rows;
   p.slot_rows = k.slot_rows;
   p.part = static_cast<float *>(workspace);
-  return status(k.many ? launch_kv_prefill(dtype, p, as_stream(stream)) : launch_kv_attn(dtype, p, as_stream(stream)));
+  return status(launch_kv_attn(dtype, p, as_stream(stream)));
 }
 
 int mnb_sample(const void *logits, int dtype, int M, int V, int64_t ldl, const float *u, const float *temperature,

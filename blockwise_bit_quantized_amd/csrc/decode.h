@@ -79,22 +79,18 @@ struct KvAttnParams {
   uint32_t flip;       // these bits
   int whole;           // every item goes to one workgroup
   int workgroups;      // of the first kernel
-  int tile_rows;       // 16 or 32 of a workgroup of few rows; kv_prefill_rows of one of many
+  int tile_rows;       // 16 or 32
   int slot_rows;       // rows of a partial result
   float *part;         // what the second kernel is told of each workgroup, then [workgroups, 2, slot_rows, D + 4]
 };
 // The workgroups of the kernel of few rows for these sizes, and whether items are split over them.
 struct KvPlan {
   int workgroups, whole, tile_rows, slot_rows;
-  int many;            // the kernel of many rows
   int64_t items;       // at most
   size_t bytes;        // of the workspace
 };
 KvPlan kv_attn_plan(const KvCache &c, const KvRows &r, int G, int window);
 hipError_t launch_kv_attn(int dtype, const KvAttnParams &p, hipStream_t s);
-// rows of a workgroup of the kernel of many rows
-constexpr int kv_prefill_rows(int D) { return D <= 128 ? 128 : 64; }
-hipError_t launch_kv_prefill(int dtype, const KvAttnParams &p, hipStream_t s);
 
 struct SampleParams {
   const void *x;

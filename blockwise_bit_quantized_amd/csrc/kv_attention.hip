@@ -31,7 +31,11 @@ struct Joint {
 constexpr int kLeast = 2 * kWaves;   // steps of a workgroup's share at least
 
 // Workgroups of this kernel that share a CU, by the registers of its tile.
-constexpr int resident(int D, int R) { return R == 1 ? (D <= 128 ? 3 : 2) : R == 2 && D <= 128 ? 2 : 1; }
+constexpr int resident(int D, int R) { return D > 128 || R == 2 ? 2 : 3; }
+
+// Tiles of 32 rows read and expand the cache half as often as those of 16.  They are taken where sequences have more than 16
+// rows and there is work for every CU, of heads whose tile leaves two waves to a SIMD.
+constexpr int kTwoTiles = 128;
 
 template <int DT, int D, int R>
 __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAttnParams p) {
@@ -43,7 +47,7 @@ __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAtt
   __shared__ float stat[kWaves][16][2];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, r = lane & 15;
   const uint32_t S = 1u << p.cache.shift;
-  const typename T::Offsets offsets(g, r);
+  const typename T::Offsets offsets(g, r, S);
   Joint *joint = reinterpret_cast<Joint *>(p.part) + blockIdx.x;
   float *parts = p.part + (int64_t)p.workgroups * (sizeof(Joint) / 4);
   const Work work = find_work(p);
@@ -90,7 +94,6 @@ __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAtt
     const int f0 = min(e1, max(e0, (all_lo - c.from + kStep - 1) / kStep)), f1 = max(f0, min(e1, (pos0 + 1 - c.from) / kStep));
     bool bad = c.beyond;
     const int32_t *pages = p.rows.pages + (int64_t)b * p.rows.ldp;
-    const uint8_t *const data = p.cache.data + (int64_t)h * kv_head_bytes(S, D);
     auto page_of = [&](int t, bool needed) {
       const int col = t >> p.cache.shift;
       int page = needed && col < p.rows.width ? pages[col] : -1;
@@ -100,17 +103,14 @@ __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAtt
       }
       return page;
     };
-    auto load = [&](typename T::Raw &raw, int half, int page, int t) {
-      T::load(raw, half, data + (int64_t)page * p.cache.page_stride, t & (S - 1), S, offsets);
-    };
-    // Page numbers of 32 steps of the wave, two a step, a lane each; a step's data is loaded while the one before is used.
+    // The places of 32 steps of the wave, two a step, a lane each; a step's data is loaded while the one before is used.
     for (int s = f0 + wave; s < f1;) {
       const int ahead = s + (lane >> 1) * kWaves;
-      const int page = page_of(c.from + ahead * kStep + 16 * (lane & 1), ahead < f1);
+      const int token = c.from + ahead * kStep + 16 * (lane & 1);
+      const HalfStep at = half_step(p.cache, h, page_of(token, ahead < f1), token);
       auto fetch = [&](typename T::Raw &raw, int n) {
-        const int t = c.from + (s + n * kWaves) * kStep;
-        load(raw, 0, __builtin_amdgcn_readlane(page, 2 * n), t);
-        load(raw, 1, __builtin_amdgcn_readlane(page, 2 * n + 1), t + 16);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) T::load(raw, k, p.cache.data, HalfStep{lane_of(at.codes, 2 * n + k), lane_of(at.scales, 2 * n + k)}, offsets);
       };
       const int count = min(32, (f1 - s + kWaves - 1) / kWaves);
       typename T::Raw one, two;
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAtt
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int t = t0 + 16 * k;
-        load(raw, k, page_of(t, t <= pos1 && t + 15 >= any_lo), t);
+        T::load(raw, k, p.cache.data, half_step(p.cache, h, page_of(t, t <= pos1 && t + 15 >= any_lo), t), offsets);
       }
       x.template step<true>(raw, p.scale, t0, g, r, any_lo, pos1);
     }
@@ -259,8 +259,10 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(KvAttnParams p) {
 template <int DT, int D>
 hipError_t launch(const KvAttnParams &p, hipStream_t s) {
   const dim3 grid((uint32_t)p.workgroups), block(kWaves * 64);
+  if constexpr (D <= kTwoTiles) {
+    if (p.tile_rows == 32) hipLaunchKernelGGL((rows_kernel<DT, D, 2>), grid, block, 0, s, p);
+  }
   if (p.tile_rows == 16) hipLaunchKernelGGL((rows_kernel<DT, D, 1>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((rows_kernel<DT, D, 2>), grid, block, 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.whole) return e;
   hipLaunchKernelGGL((join_kernel<DT, D>), dim3((uint32_t)p.workgroups, p.tile_rows / 16), dim3(kJoinThreads), 0, s, p);
@@ -286,20 +288,9 @@ KvPlan kv_attn_plan(const KvCache &c, const KvRows &r, int G, int window) {
   const int64_t steps = (tokens + kStep - 1) / kStep + 1;
   // at most one short tile for each sequence
   auto tiles = [&](int rows) { return r.starts ? (int64_t)r.rows * G / rows + r.batch : (int64_t)r.batch * ((G + rows - 1) / rows); };
-  // Tiles of 32 rows read and expand the cache half as often, where sequences have more than 16 rows and
-  // there is work for every CU.
   const int64_t rows = r.starts ? (int64_t)r.rows * G / r.batch : G;
-  k.tile_rows = rows > 16 && tiles(32) * c.heads * steps >= (int64_t)resident(c.D, 2) * kCUs * kLeast ? 32 : 16;
+  k.tile_rows = c.D <= kTwoTiles && rows > 16 && tiles(32) * c.heads * steps >= (int64_t)resident(c.D, 2) * kCUs * kLeast ? 32 : 16;
   k.items = tiles(k.tile_rows) * c.heads;
-  // Many rows: workgroups of 128 (or 64) that expand the cache once for all of them, where these fill the chip.
-  const int64_t many = tiles(kv_prefill_rows(c.D)) * c.heads;
-  if (rows >= kv_prefill_rows(c.D) && many >= 2 * kCUs) {
-    k.many = k.whole = 1;
-    k.tile_rows = kv_prefill_rows(c.D);
-    k.items = many;
-    k.workgroups = (int)many;
-    return k;
-  }
   k.slot_rows = r.starts || G > k.tile_rows ? k.tile_rows : G;
   const int64_t most = k.items * steps / kLeast + 1, room = resident(c.D, k.tile_rows / 16) * kCUs;
   k.whole = k.items >= 2 * room || steps <= 32;

@@ -47,6 +47,27 @@ __device__ __forceinline__ uint32_t scale_of(uint32_t w) {
   else return w >> 1;
 }
 
+// Where 16 tokens of a step lie: their key codes and key scales in a page of a head, from the cache's first byte (values' lie a
+// constant further).  Each lane works out the places of other steps; a step reads its two from theirs into
+// scalar registers.
+struct HalfStep {
+  int64_t codes, scales;
+};
+__device__ __forceinline__ HalfStep half_step(const KvCache &c, int h, int page, int token) {
+  const int S = 1 << c.shift, in = token & (S - 1);
+  const int64_t head = (int64_t)page * c.page_stride + (int64_t)h * kv_head_bytes(S, c.D);
+  return HalfStep{head + (int64_t)in * (c.D / 2), head + ((int64_t)S * c.D + in * (c.D / 32))};
+}
+__device__ __forceinline__ int64_t lane_of(int64_t v, int lane) {
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+                   (uint32_t)__builtin_amdgcn_readlane((int)v, lane));
+}
+// An offset whose widening stays in the loop: widened before it, it costs a 64-bit addition at each load.
+__device__ __forceinline__ uint32_t in_loop(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // The value operand's parts: 16 lanes share 128, 64 or 32 elements, 8, 4 or 2 each; lane r of part k has the
 // elements d0 + 8 word + (first nibble) + j of unit `word`.
 template <int D> struct Parts {
@@ -143,34 +164,32 @@ struct Tile {
     u4_t v[2][P::count];
     uint32_t vs[2][P::count];
   };
-  // a lane's offsets from the first token's place in each of a page's four arrays: all of a step's addresses are these
-  // over bases in scalar registers
+  // A lane's offsets from the two addresses of a step's half (HalfStep): into codes and into scales, keys then values.
   struct Offsets {
     uint32_t k, ke[2], v[P::count], vs[P::count];
-    __device__ __forceinline__ Offsets(int g, int r) {
+    __device__ __forceinline__ Offsets(int g, int r, uint32_t S) {
       k = r * (D / 2) + g * (D / 8);
       ke[0] = r * (D / 32) + g * (D / 4) / 32;
       ke[1] = r * (D / 32) + (g * (D / 4) + D / 4 - 1) / 32;
 #pragma unroll
       for (int p = 0; p < P::count; ++p) {
-        v[p] = (g * (D / 8) + P::word(p, r)) * 16;
-        vs[p] = (g * (D / 32) + P::word(p, r) / 4) * 4;
+        v[p] = S * (D / 2) + (g * (D / 8) + P::word(p, r)) * 16;
+        vs[p] = S * (D / 32) + (g * (D / 32) + P::word(p, r) / 4) * 4;
       }
     }
   };
-  // head: the page of this head; in: the first token's place in it, a multiple of 16
-  __device__ static __forceinline__ void load(Raw &x, int half, const uint8_t *head, uint32_t in, uint32_t S, const Offsets &o) {
-    const uint8_t *k = head + in * (D / 2), *ke = head + (S * D + in * (D / 32)), *v = head + (S + in) * (D / 2),
-                  *vs = head + (S * D + (S + in) * (D / 32));
+  __device__ static __forceinline__ void load(Raw &x, int half, const uint8_t *data, HalfStep at, const Offsets &o) {
+    const uint8_t *codes = data + at.codes, *scales = data + at.scales;
+    const uint32_t *k = reinterpret_cast<const uint32_t *>(codes + in_loop(o.k));
 #pragma unroll
-    for (int i = 0; i < KS; ++i) x.kw[half][i] = reinterpret_cast<const uint32_t *>(k + o.k)[i];
-    x.ke[half][0] = ke[o.ke[0]];
+    for (int i = 0; i < KS; ++i) x.kw[half][i] = k[i];
+    x.ke[half][0] = scales[in_loop(o.ke[0])];
     // a lane's fourth of the head lies in one block where D is 64 or 128
-    x.ke[half][1] = D == 64 || D == 128 ? 0 : ke[o.ke[1]];
+    x.ke[half][1] = D == 64 || D == 128 ? 0 : scales[in_loop(o.ke[1])];
 #pragma unroll
     for (int p = 0; p < P::count; ++p) {
-      x.v[half][p] = *reinterpret_cast<const u4_t *>(v + o.v[p]);
-      x.vs[half][p] = *reinterpret_cast<const uint32_t *>(vs + o.vs[p]);
+      x.v[half][p] = *reinterpret_cast<const u4_t *>(codes + in_loop(o.v[p]));
+      x.vs[half][p] = *reinterpret_cast<const uint32_t *>(scales + in_loop(o.vs[p]));
     }
   }
 
@@ -188,7 +207,7 @@ struct Tile {
       most[w] = fmaxf(fmaxf(fmaxf(t[w][0], t[w][1]), fmaxf(t[w][2], t[w][3])), fmaxf(fmaxf(t[w][4], t[w][5]), fmaxf(t[w][6], t[w][7])));
       raise |= most[w] > (base[w] == -__builtin_inff() ? -__builtin_inff() : kOff + 8.f);
     }
-    if (__any(raise)) {
+    if (__builtin_expect(__any(raise), 0)) {
 #pragma unroll
       for (int w = 0; w < R; ++w) {
         const float from = base[w] == -__builtin_inff() ? 0.f : base[w];
@@ -328,10 +347,6 @@ __device__ __forceinline__ int64_t wave_scan(int64_t v) {
     if (lane >= d) v += o;
   }
   return v;
-}
-__device__ __forceinline__ int64_t lane_of(int64_t v, int lane) {
-  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
-                   (uint32_t)__builtin_amdgcn_readlane((int)v, lane));
 }
 // The workgroup's steps [at, end) of the work (none left: end 0), and the sequence that holds `at` with the place where
 // it begins.

@@ -510,7 +510,7 @@ def test_attention_of_many_rows(case, dtype):
                for n, h in ((total, hkv), (total, hkv), (starts[-1], hq)))
     whole = [0, *np.cumsum(lengths).tolist()]
     mnb.kv_append(None, k, v, s.cache, s.pages, s.lengths, starts=ints(whole))
-    assert route(s, hq, starts[-1], starts, window).startswith("kv_prefill")
+    assert route(s, hq, starts[-1], starts, window).startswith(f"kv_attention tile={32 if D <= 128 else 16}")
     out = torch.full_like(q, 7.0)
     y = mnb.kv_attention(q, s.cache, s.pages, s.lengths, starts=ints(starts), window=window, out=out)
     kq, vq = mnb.kv_read(s.cache, s.pages, s.lengths, total, starts=ints(whole), dtype=torch.float32)
@@ -535,7 +535,7 @@ def test_many_rows_and_what_they_do_not_see(D):
     v[600, 3, D - 1] = v[333, 0, 0] = float("nan")
     k[500, 2, 5] = float("inf")
     mnb.kv_append(None, k, v, s.cache, s.pages, s.lengths, starts=ints([0, n]))
-    assert route(s, H, n, [0, n], 0).startswith("kv_prefill")
+    assert route(s, H, n, [0, n], 0).startswith(f"kv_attention tile={32 if D <= 128 else 16}")
     y = mnb.kv_attention(q, s.cache, s.pages, s.lengths, starts=ints([0, n]))
     bad = torch.zeros(n, H, D, dtype=torch.bool, device=DEV)
     bad[600:, 3, D - 32:] = bad[333:, 0, :32] = bad[500:, 2] = True
@@ -552,7 +552,7 @@ def test_many_rows_out_of_reach():
     q = torch.randn(3 * n + 5, H, D, device=DEV).to(t)
     out = torch.full_like(q, 7.0)
     starts = [0, n, 2 * n, 3 * n]
-    assert route(s, H, 3 * n + 5, starts, 0).startswith("kv_prefill")
+    assert route(s, H, 3 * n + 5, starts, 0).startswith("kv_attention tile=32")
     mnb.kv_attention(q, s.cache, s.pages, s.lengths, starts=ints(starts), out=out)
     assert not bool(out[:n].isnan().any()) and bool((out[3 * n:] == 7).all())
     assert bool(out[n + 64 * 4 + 128:2 * n].isnan().all()) and bool(out[2 * n:3 * n].isnan().all())
