@@ -5,9 +5,12 @@
 // q is rounded once to 16 bits; keys and values become MX FP4 codes (blocks of 32 along the head).
 //
 // Keys are computed in 64 bits throughout, so their codes are those of the exact key (32 bits would put
-// one element in some thousands on the wrong side of a border of the 4-bit grid); sums of squares are
-// in 64 bits for queries too.  A lane holds 8 elements and 8, 16 or 32 lanes a head, so a block of 32 is
+// one element in some thousands on the wrong side of a border of the 4-bit grid).  Queries have their sums of squares
+// in 64 bits and the products, at most 5 roundings of 2^-24 before the one to 16 bits, in 32.  A lane holds 8 elements and 8, 16 or 32 lanes a head, so a block of 32 is
 // four neighbouring lanes, and nothing goes through LDS.
+//
+// Many rows are bound by memory: 8192 rows of 32 + 8 + 8 heads of 128 in 51 us are 170 MB at 3.3 TB/s (a large copy: 4.7).
+// Few are bound by the chain of loads row -> sequence -> page number and angles: 64 rows 5.1 us, one row 3.3 us.
 #include "decode.h"
 
 namespace mnb {
@@ -59,46 +62,66 @@ __device__ __forceinline__ double head_sum(double v) {
   return v;
 }
 
-// norm and rotation of the 8 elements of lane l of a head, in T; every lane of the wave runs it together
+// The angle of a row's position for lane l of a head, the same for all its heads: v' = v c + o s, where o is the pair's other
+// element.
+struct Turn {
+  bool on;
+  int other;                   // lane that holds the pairs' other elements (halves turned against each other)
+  float c[8], s[8];
+};
+template <int LANES>
+__device__ __forceinline__ Turn find_turn(const KvAppendParams &p, int l, int pos) {
+  Turn t;
+  t.on = 8 * l < p.rot;
+  const int half = p.rot / 2, hl = p.rot / 16;           // elements and lanes of half a turn
+  const bool low = l < hl;
+  t.other = (threadIdx.x & 63 & ~(LANES - 1)) + (!t.on ? l : low ? l + hl : l - hl);
+  if (!t.on) return t;
+  const float *row = p.table + (int64_t)pos * p.rot + (p.interleaved ? 4 * l : 8 * (low ? l : l - hl));
+  const f4_t c0 = *reinterpret_cast<const f4_t *>(row), s0 = *reinterpret_cast<const f4_t *>(row + half);
+  if (p.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      t.c[i] = c0[i / 2];
+      t.s[i] = i & 1 ? s0[i / 2] : -s0[i / 2];
+    }
+  } else {
+    const f4_t c1 = *reinterpret_cast<const f4_t *>(row + 4), s1 = *reinterpret_cast<const f4_t *>(row + half + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t.c[i] = c0[i];
+      t.c[4 + i] = c1[i];
+      t.s[i] = low ? -s0[i] : s0[i];
+      t.s[4 + i] = low ? -s1[i] : s1[i];
+    }
+  }
+  return t;
+}
+
+// norm and rotation of the 8 elements of a lane of a head, in T; all lanes of the head run it together
 template <int DT, int LANES, typename T>
-__device__ __forceinline__ void norm_rotate(const KvAppendParams &p, T *v, const uint16_t *weight, int l, bool in, int pos) {
-  const int D = p.cache.D;
+__device__ __forceinline__ void norm_rotate(const KvAppendParams &p, const float *x, T *v, const uint16_t *weight, u4_t w8, const Turn &turn) {
   if (weight) {
     double ss = 0.0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fma((double)v[i], (double)v[i], ss);
+    for (int i = 0; i < 8; ++i) ss = fma((double)x[i], (double)x[i], ss);
     ss = head_sum<LANES>(ss);
-    const T r = (T)(1.0 / sqrt(ss / D + (double)p.eps));
-    float w[8] = {};
-    if (in) load8<DT>(weight + 8 * l, w);
+    const double r = 1.0 / sqrt(ss / p.cache.D + (double)p.eps);   // (as 32 bits it could pass their range)
+    float w[8];
+    load8<DT>(reinterpret_cast<const uint16_t *>(&w8), w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * r * (T)w[i];
+    for (int i = 0; i < 8; ++i) v[i] = (T)(x[i] * r) * (T)w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (T)x[i];
   }
   if (p.rot == 0) return;
-  const float *row = p.table + (int64_t)pos * p.rot;
-  const int half = p.rot / 2, hl = p.rot / 16;        // elements and lanes of half a turn
-  if (p.interleaved) {
-    if (8 * l < p.rot) {
+  T o[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const T c = (T)row[4 * l + i], s = (T)row[half + 4 * l + i], a = v[2 * i], b = v[2 * i + 1];
-        v[2 * i] = a * c - b * s;
-        v[2 * i + 1] = b * c + a * s;
-      }
-    }
-    return;
-  }
-  const int lane = threadIdx.x & 63, base = lane & ~(LANES - 1);
-  const bool low = l < hl;
-  const int other = base + (l < 2 * hl ? (low ? l + hl : l - hl) : l);
+  for (int i = 0; i < 8; ++i) o[i] = p.interleaved ? v[i ^ 1] : __shfl(v[i], turn.other);
+  if (turn.on) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const T o = __shfl(v[i], other);       // the pair's other half
-    if (l < 2 * hl) {
-      const int e = 8 * (low ? l : l - hl) + i;
-      const T c = (T)row[e], s = (T)row[half + e];
-      v[i] = low ? v[i] * c - o * s : v[i] * c + o * s;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = v[i] * (T)turn.c[i] + o[i] * (T)turn.s[i];
   }
 }
 
@@ -117,47 +140,61 @@ __device__ __forceinline__ uint32_t quantize8(const float *x, uint32_t &e) {
   return fp4_codes(v);
 }
 
-// One workgroup a row; heads in the order q, k, v, LANES lanes each.
+// One workgroup a row; heads in the order q, k, v, LANES lanes each.  Heads behind the workgroup's first are loaded while
+// the ones before are computed; the row's angles stay in registers.
 template <int DT, int LANES>
 __global__ __launch_bounds__(1024) void append_kernel(KvAppendParams p) {
   const int row = blockIdx.x, D = p.cache.D, S = 1 << p.cache.shift;
   const int l = threadIdx.x & (LANES - 1);
   const bool in = 8 * l < D;
+  const int kv = p.cache.heads, heads = p.q_heads + 2 * kv, step = blockDim.x / LANES;
+  auto fetch = [&](int h) {
+    const int hk = h - p.q_heads, hv = hk - kv;
+    const uint16_t *src = hk < 0   ? p.q + (int64_t)row * p.ldq + (int64_t)h * D
+                          : hv < 0 ? p.k + (int64_t)row * p.ldk + (int64_t)hk * D
+                                   : p.v + (int64_t)row * p.ldv + (int64_t)hv * D;
+    return h < heads && in ? *reinterpret_cast<const u4_t *>(src + 8 * l) : u4_t{0, 0, 0, 0};
+  };
+  u4_t next = fetch((int)threadIdx.x / LANES);
+  const u4_t none = {0, 0, 0, 0};
+  const u4_t wq = p.qw && in ? *reinterpret_cast<const u4_t *>(p.qw + 8 * l) : none;
+  const u4_t wk = p.kw && in ? *reinterpret_cast<const u4_t *>(p.kw + 8 * l) : none;
   Place at = find_place(p.cache, p.rows, row);
   if (at.where == kForeign) return;
   if (at.where == kHeld && p.rot && at.pos >= p.table_rows) at.where = kUnreachable;
-  const int kv = p.cache.heads, heads = p.q_heads + 2 * kv, step = blockDim.x / LANES;
   uint8_t *page = p.cache.data + (int64_t)at.page * p.cache.page_stride;
+  Turn turn{};
+  if (at.where == kHeld) turn = find_turn<LANES>(p, l, at.pos);
   for (int h0 = 0; h0 < heads; h0 += step) {            // uniform, so that the exchanges find all lanes
     const int h = h0 + (int)threadIdx.x / LANES;
+    const u4_t now = next;
+    next = fetch(h + step);
     const bool is_q = h < p.q_heads, is_k = !is_q && h < p.q_heads + kv;
     const int hk = h - p.q_heads - (is_k ? 0 : kv);      // head of the cache, for k and v
     const bool on = h < heads && in;
-    const uint16_t *src = is_q   ? p.q + (int64_t)row * p.ldq + (int64_t)h * D
-                          : is_k ? p.k + (int64_t)row * p.ldk + (int64_t)hk * D
-                                 : p.v + (int64_t)row * p.ldv + (int64_t)hk * D;
-    float x[8] = {};
-    if (on) load8<DT>(src + 8 * l, x);
+    uint16_t *out = p.out + (int64_t)row * p.ldo + (int64_t)h * D + 8 * l;
+    float x[8];
+    load8<DT>(reinterpret_cast<const uint16_t *>(&now), x);
     if (at.where != kHeld) {
       if (is_q && on) {
         const float fill = at.where == kNowhere ? 0.f : __builtin_nanf("");
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = fill;
-        store8<DT>(p.out + (int64_t)row * p.ldo + (int64_t)h * D + 8 * l, x);
+        store8<DT>(out, x);
       }
       continue;
     }
-    if (is_q || is_k) {
+    if (is_q) {
+      float v[8];
+      norm_rotate<DT, LANES, float>(p, x, v, p.qw, wq, turn);
+      if (on) store8<DT>(out, v);
+      continue;
+    }
+    if (is_k) {
       double v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = x[i];
-      norm_rotate<DT, LANES, double>(p, v, is_q ? p.qw : p.kw, l, in, at.pos);
+      norm_rotate<DT, LANES, double>(p, x, v, p.kw, wk, turn);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = to_odd(v[i]);
-    }
-    if (is_q) {
-      if (on) store8<DT>(p.out + (int64_t)row * p.ldo + (int64_t)h * D + 8 * l, x);
-      continue;
     }
     uint32_t e;
     const uint32_t codes = quantize8(x, e);
@@ -215,7 +252,12 @@ template <int DT>
 hipError_t append(const KvAppendParams &p, hipStream_t s) {
   const int lanes = p.cache.D <= 64 ? 8 : p.cache.D <= 128 ? 16 : 32;
   const int64_t need = (int64_t)(p.q_heads + 2 * p.cache.heads) * lanes;
-  const int threads = (int)(need > 1024 ? 1024 : (need + 63) / 64 * 64);
+  // A workgroup takes its row's heads in as many passes as leave all rows on the card at once (16 waves a CU, by
+  // registers), but has at least two waves: with 48 heads of 128, of 1024 threads against the rule's, 512 rows take
+  // 8.8 and 7.4 us, 2048 rows 27.7 and 17.3, 8192 rows 98.5 and 50.8; 256 rows of 128 threads 9.0, of 1024 5.6.
+  int64_t most = (int64_t)kCUs * 1024 / p.rows.rows / 64 * 64;
+  most = most < 128 ? 128 : most > 1024 ? 1024 : most;
+  const int threads = (int)(need > most ? most : (need + 63) / 64 * 64);
   const dim3 grid((uint32_t)p.rows.rows), block((uint32_t)threads);
   if (lanes == 8) hipLaunchKernelGGL((append_kernel<DT, 8>), grid, block, 0, s, p);
   else if (lanes == 16) hipLaunchKernelGGL((append_kernel<DT, 16>), grid, block, 0, s, p);
