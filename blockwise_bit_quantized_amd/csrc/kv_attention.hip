@@ -30,8 +30,9 @@ struct Joint {
 
 constexpr int kLeast = 2 * kWaves;   // steps of a workgroup's share at least
 
-// Workgroups of this kernel that share a CU, by the registers of its tile.
-constexpr int resident(int D, int R) { return D > 128 || R == 2 ? 2 : 3; }
+// Workgroups of this kernel that share a CU, by the registers of its tile (a third at 32 rows of 64: 4 x 333 rows over
+// 3001 tokens, 14/2 heads, 31.2 to 29.4 us; of 96 and 128 it would spill).
+constexpr int resident(int D, int R) { return D <= (R == 1 ? 128 : 64) ? 3 : 2; }
 
 // Tiles of 32 rows read and expand the cache half as often as those of 16.  They are taken where sequences have more than 16
 // rows and there is work for every CU, of heads whose tile leaves two waves to a SIMD.
