@@ -12,9 +12,9 @@
 //     same elements of these 8 tokens, so neither passes through LDS.
 // FP4 codes become 16-bit numbers by the conversion instruction that applies the block's scale.
 //
-// Items (sequence, tile of rows, head) are cut in steps of 32 tokens, laid end to end and shared out evenly, so
-// a long sequence among short ones does not keep one workgroup; a workgroup's first and last item
-// may be parts, which a second kernel joins in their order.
+// Items (sequence, tile of rows, head) go to a workgroup each where that is fast enough.  Else they are cut in steps of 32
+// tokens, laid end to end and shared out evenly, so a long sequence among short ones does not keep one workgroup; a
+// workgroup's first and last item may be parts, which a second kernel joins in their order.
 #include "kv_tile.h"
 
 namespace mnb {
@@ -56,10 +56,11 @@ __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAtt
   if (work.end == 0) return;
   int64_t at = work.at, begin = work.begin;
   int b = work.b;
+  const bool whole = work.whole;
   bool first_item = true;
   while (at < work.end && b < p.rows.batch) {
     const Cut c = cut_of(p, b);
-    const int64_t span = p.whole ? 1 : c.steps, mine = span * c.tiles * p.cache.heads;
+    const int64_t span = whole ? 1 : c.steps, mine = span * c.tiles * p.cache.heads;
     if (at >= begin + mine) {                            // on to the next sequence
       begin += mine;
       ++b;
@@ -68,7 +69,7 @@ __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAtt
     const int item = (int)((at - begin) / span);
     const int64_t item0 = begin + item * span, stop = item0 + span < work.end ? item0 + span : work.end;
     const bool part = !(at == item0 && stop == item0 + span);
-    const int s0 = p.whole ? 0 : (int)(at - item0), s1 = p.whole ? c.steps : (int)(stop - item0);
+    const int s0 = whole ? 0 : (int)(at - item0), s1 = whole ? c.steps : (int)(stop - item0);
     // the last rows, which see most, first
     const int h = item % p.cache.heads, tile = c.tiles - 1 - item / p.cache.heads;
 
@@ -294,8 +295,11 @@ KvPlan kv_attn_plan(const KvCache &c, const KvRows &r, int G, int window) {
   k.items = tiles(k.tile_rows) * c.heads;
   k.slot_rows = r.starts || G > k.tile_rows ? k.tile_rows : G;
   const int64_t most = k.items * steps / kLeast + 1, room = resident(c.D, k.tile_rows / 16) * kCUs;
-  k.whole = k.items >= 2 * room || steps <= 32;
-  k.workgroups = (int)(k.whole ? k.items : most < room ? most : room);
+  // By these sizes alone whole items are taken where there are two rounds of them or none is long (the kernel decides
+  // the rest by the lengths): cut against whole, 256 sequences of 1024 64.1 and 49.7 us, one of 700 (14/2 heads of 64) 13.0
+  // and 8.0.
+  k.whole = k.items >= 2 * room || steps <= 40;
+  k.workgroups = (int)(k.whole || k.items > room ? k.items : most < room ? most : room);
   k.bytes = k.whole ? 0 : (size_t)k.workgroups * (sizeof(Joint) + (size_t)2 * k.slot_rows * (c.D + 4) * 4);
   return k;
 }

@@ -332,10 +332,15 @@ __device__ __forceinline__ Cut cut_of(const KvAttnParams &p, int b) {
   c.steps = c.beyond ? 1 : max(1, (c.seq.len - c.from + kStep - 1) / kStep);
   return c;
 }
-__device__ __forceinline__ int64_t cost_of(const KvAttnParams &p, int b) {
-  if (b >= p.rows.batch) return 0;
+// A sequence's items (tiles of each head), and the steps of one.
+struct Cost {
+  int64_t items;
+  int steps;
+};
+__device__ __forceinline__ Cost cost_of(const KvAttnParams &p, int b) {
+  if (b >= p.rows.batch) return Cost{0, 0};
   const Cut c = cut_of(p, b);
-  return (int64_t)c.tiles * p.cache.heads * (p.whole ? 1 : c.steps);
+  return Cost{(int64_t)c.tiles * p.cache.heads, c.tiles ? c.steps : 0};
 }
 
 // Sums over the wave's lanes up to this one.  (Every wave finds the workgroup's place in the work by itself.)
@@ -348,16 +353,24 @@ __device__ __forceinline__ int64_t wave_scan(int64_t v) {
   }
   return v;
 }
-// The workgroup's steps [at, end) of the work (none left: end 0), and the sequence that holds `at` with the place where
-// it begins.
+// The workgroup's share [at, end) of the work, in items (`whole`) or in steps of them (none left: end 0), and the sequence
+// that holds `at` with the place where it begins.
 struct Work {
   int64_t at, end, begin, share;
   int b;
+  bool whole;
 };
+// Shares of steps balance what sequences of different lengths take, but cost a second kernel and parts of two items a
+// workgroup.  So where there is a workgroup for each item they are taken, by the lengths that the call finds, only if the
+// longest item is longer than two shares and kPatience steps: one row each of heads of 128 (32 query and 8 key/value),
+// cut against whole: 16 sequences of 4096 27.0 and 23.6 us, 32 of 4096 35.0 and 26.2, 64 of 4096 57.0 and 49.1, 32 of 1024 22.4
+// and 10.8; one of 131072 41 us against 4096 steps by one workgroup.
+constexpr int kPatience = 96;
 __device__ __forceinline__ Work find_work(const KvAttnParams &p) {
   Work w{};
   const int lane = threadIdx.x & 63;
   w.share = 1;
+  w.whole = p.whole;
   if (p.whole && !p.rows.starts) {                       // as many items for each sequence
     const int each = (p.G + p.tile_rows - 1) / p.tile_rows * p.cache.heads;
     w.at = blockIdx.x;
@@ -366,17 +379,35 @@ __device__ __forceinline__ Work find_work(const KvAttnParams &p) {
     w.begin = (int64_t)w.b * each;
     return w;
   }
-  const int64_t first = cost_of(p, lane), first_run = wave_scan(first);
+  const Cost first = cost_of(p, lane);
   if (!p.whole) {
-    int64_t total = lane_of(first_run, 63);
-    for (int b0 = 64; b0 < p.rows.batch; b0 += 64) total += lane_of(wave_scan(cost_of(p, b0 + lane)), 63);
-    w.share = (total + p.workgroups - 1) / p.workgroups;
+    int64_t items = 0, steps = 0;
+    int most = 0;
+    for (int b0 = 0; b0 < p.rows.batch; b0 += 64) {
+      const Cost c = b0 ? cost_of(p, b0 + lane) : first;
+      items += c.items;
+      steps += c.items * c.steps;
+      most = max(most, c.steps);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      items += __shfl_xor((long long)items, d);
+      steps += __shfl_xor((long long)steps, d);
+      most = max(most, __shfl_xor(most, d));
+    }
+    items = lane_of(items, 0);
+    steps = lane_of(steps, 0);
+    most = __builtin_amdgcn_readlane(most, 0);
+    w.share = (steps + p.workgroups - 1) / p.workgroups;
+    w.whole = items <= p.workgroups && most <= 2 * w.share + kPatience;
     if (w.share < 2 * kWaves) w.share = 2 * kWaves;       // no smaller parts than two steps a wave
+    if (w.whole) w.share = 1;
   }
   w.at = (int64_t)blockIdx.x * w.share;
   int64_t before = 0;
   for (int b0 = 0; b0 < p.rows.batch; b0 += 64) {
-    const int64_t mine = b0 ? cost_of(p, b0 + lane) : first, run = (b0 ? wave_scan(mine) : first_run) + before;
+    const Cost c = b0 ? cost_of(p, b0 + lane) : first;
+    const int64_t mine = w.whole ? c.items : c.items * c.steps, run = wave_scan(mine) + before;
     const uint64_t hit = __ballot(run > w.at);
     before = lane_of(run, 63);
     if (hit) {

@@ -7,6 +7,7 @@ import pytest
 
 import _decode_ref as dref
 from _util import ensure_lib
+from test_decode_gpu import run_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -218,6 +219,20 @@ def test_many_sequences(B):
             want, size = dref.attention(qb, kb, vb, int(lengths[b]) - len(qb), D ** -0.5, 0)
             score = float(np.einsum("nhd,thd->nht", np.abs(qb), np.repeat(np.abs(kb), hq // hkv, 1)).max()) * D ** -0.5
             assert (np.abs(y[at[b]:at[b + 1]] - want) <= bound(want, size, t, score, int(lengths[b]), D)).all(), b
+
+
+@pytest.mark.parametrize("t", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("lengths,starts,hq,hkv,D,S,window", [
+    ([4300, 10, 0, 900], None, 8, 2, 128, 16, 0), ([4200, 4100], [0, 3, 7], 10, 2, 96, 128, 0), ([4500, 4500], None, 4, 2, 256, 256, 4200),
+    ([5000, 1500, 1500, 0], None, 2, 1, 192, 32, 0), ([6000, 300], [0, 70, 100], 8, 2, 128, 64, 0), ([1] * 70 + [6000], None, 4, 2, 64, 16, 0),
+    ([200] * 40, None, 4, 2, 64, 2048, 0)])
+def test_long_among_short(lengths, starts, hq, hkv, D, S, window, t):
+    """Sequences long enough that an item is shared by workgroups whatever the others are, tiles of 32 rows too; and short ones in
+    tables that could hold long ones, of which each item is one workgroup's."""
+    _, q, y, st = run = run_attention(np.random.default_rng([len(lengths), D]), lengths, starts, hq, hkv, D, S, window, t)
+    s = run[0]
+    for _ in range(2):
+        assert torch.equal(y, mnb.kv_attention(q.to(DEV), s.cache, s.pages, s.lengths, starts=st, window=window))
 
 
 @pytest.mark.parametrize("t", [torch.float16, torch.bfloat16, torch.float32])
