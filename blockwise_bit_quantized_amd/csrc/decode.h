@@ -77,13 +77,13 @@ struct KvAttnParams {
   int window;          // 0: none
   float scale;         // |scale| times log2(e); a negative one turns q's signs by
   uint32_t flip;       // these bits
-  int whole;           // every item goes to one workgroup
+  int whole;           // every item goes to one workgroup, whatever the lengths are
   int workgroups;      // of the first kernel
   int tile_rows;       // 16 or 32
   int slot_rows;       // rows of a partial result
   float *part;         // what the second kernel is told of each workgroup, then [workgroups, 2, slot_rows, D + 4]
 };
-// The workgroups of the kernel of few rows for these sizes, and whether items are split over them.
+// The workgroups for these sizes, and whether items may be split over them.
 struct KvPlan {
   int workgroups, whole, tile_rows, slot_rows;
   int64_t items;       // at most

@@ -1,6 +1,6 @@
-// kv_attention.hip -- attention over the paged FP4 cache, for rows that are few for each sequence.
+// kv_attention.hip -- attention over the paged FP4 cache, of one row of each sequence or of many.
 //
-// y = softmax(scale q K^T) V over the tokens a row sees.  A tile is 16 rows: the query heads that
+// y = softmax(scale q K^T) V over the tokens a row sees.  A tile is 16 or 32 rows: the query heads that
 // share a key/value head, of one token or of several.  A wave takes 32 tokens a step:
 //   S^T [32 tokens x 16 rows] = K Q^T, two matrix instructions of 16 x 16 x 32 for each 32 elements.  The
 //     sum over the head may run in any order that K and Q share, so lane (g, r) takes a fourth of
@@ -15,6 +15,11 @@
 // Items (sequence, tile of rows, head) go to a workgroup each where that is fast enough.  Else they are cut in steps of 32
 // tokens, laid end to end and shared out evenly, so a long sequence among short ones does not keep one workgroup; a
 // workgroup's first and last item may be parts, which a second kernel joins in their order.
+//
+// Few rows are bound by memory and the latencies around it: 32 sequences of 4096 (32/8 heads of 128, 143 MB) take 26 us, 5.4 TB/s,
+// and 4 for the second kernel's launch, one of 131072 29 us and 6.5 to join its 768 parts; one of 700 (14/2 heads of 64) 7.5 us.  Many rows are bound by
+// the issue of vector instructions, about 220 a step for 33 matrix instructions at tiles of 32 rows of 128, of
+// which the expansion of FP4 is 96: 8192 rows of one sequence 620 to 760 us, 0.72 to 0.89 PFLOP/s.
 #include "kv_tile.h"
 
 namespace mnb {
@@ -35,7 +40,9 @@ constexpr int kLeast = 2 * kWaves;   // steps of a workgroup's share at least
 constexpr int resident(int D, int R) { return D <= (R == 1 ? 128 : 64) ? 3 : 2; }
 
 // Tiles of 32 rows read and expand the cache half as often as those of 16.  They are taken where sequences have more than 16
-// rows and there is work for every CU, of heads whose tile leaves two waves to a SIMD.
+// rows and there is work for every CU, of heads whose tile leaves two waves to a SIMD.  16 against 32: 2048 rows of one
+// sequence 77.5 and 66.0 us, 256 rows over 4096 45.9 and 35.8, 8 sequences of 16 rows over 2048 28.9 and 24.9 (32/8 heads
+// of 128); with less work 8 of 5 rows over 2001 17.7 and 20.1 (20/4 heads of 96).
 constexpr int kTwoTiles = 128;
 
 template <int DT, int D, int R>

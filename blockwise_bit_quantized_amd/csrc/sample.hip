@@ -17,6 +17,10 @@
 //   histograms over their order bits until one number is left, of which the first few by index stay.
 //   The token itself is the place where the running sum passes u times the whole: sums of the waves, of
 //   that wave's rounds (taken by all waves), of that round's lanes.
+//
+// Rows are bound by 64-bit instructions, about 22 a weight, on the one CU that has the row, and single rows by
+// the latencies of their passes: 1 x 49152 with all filters 14 us, 1024 x 49152 by temperature 63 to 68 us (1.5 TB/s),
+// 64 x 131072, of which some have no filter and some top-p alone (a weight for each logit twice, 116 us for such rows), 128 us.
 #include <type_traits>
 
 #include "decode.h"
@@ -28,7 +32,8 @@ constexpr int kCollect = 4096;       // logits collected in LDS
 constexpr int kSort = 1024;          // ... and sorted there
 constexpr int kFew = 128;            // ... or settled by one wave
 constexpr int kMostK = 1000;         // about 3900 logits reach the 1000th of 1024 maxima
-constexpr int kFewK = 180;           // about 310 logits reach the 180th of 256 maxima
+constexpr int kFewK = 180;           // about 310 logits reach the 180th of 256 maxima (1 x 49152, 1024 against 256
+                                     // groups: top-k 50 19.1 and 15.1 us, 150 33.2 and 29.2, 180 33.6 and 34.2, 250 38.5 and 43.1)
 constexpr int kHeld = 6;             // rounds of a wave whose pieces stay in registers for the collection
 constexpr int kBins = 2048;
 constexpr int kRound = 512;          // logits of a wave's round
@@ -894,6 +899,8 @@ __global__ __launch_bounds__(WAVES * 64, 4) void sample_kernel(SampleParams p, i
 template <int DT>
 hipError_t launch(const SampleParams &p, int fraction, hipStream_t s) {
   const dim3 grid((uint32_t)p.M);
+  // 8 waves leave a CU two rows at a time: 1024 x 49152 by temperature 64.5 us (16 waves: 81.2), with top-p 174 (219); a row
+  // alone on its CU is faster with 16: 64 x 131072 with top-p 116 (8 waves: 132)
   if (p.M > kCUs) hipLaunchKernelGGL((sample_kernel<DT, 8>), grid, dim3(512), 0, s, p, fraction);
   else hipLaunchKernelGGL((sample_kernel<DT, 16>), grid, dim3(1024), 0, s, p, fraction);
   return hipGetLastError();

@@ -73,8 +73,8 @@ size_t mnb_kv_page_bytes(int kv_heads, int head_dim, int page_size);
  * rot / 2 cosines and as many sines (FP32, [table_rows, rot]):
  *   (a, b) -> (a cos - b sin, b cos + a sin)   for the pairs (i, i + rot / 2), or
  *                                              (2 i, 2 i + 1) with `interleaved`.
- * q_out [rows, q_heads, head_dim] receives the queries, rounded once; keys, and values v as they are,
- * go to the cache as by mnb_mx_quantize of the exact (64-bit) keys.
+ * q_out [rows, q_heads, head_dim] receives the queries (means in 64 bits, products in 32, one rounding to dtype);
+ * keys, and values v as they are, go to the cache as by mnb_mx_quantize of the exact (64-bit) keys.
  * dtype fp16 or bf16 for q, k, v, weights and q_out.  rot a multiple of 16 up to head_dim, or 0 and no table.
  * q may be NULL with q_heads 0 (then q_out is not used); q_out may be q itself.
  * Tensors 16-byte aligned, as are their row distances in bytes; heads lie head_dim elements apart.
