@@ -1,5 +1,5 @@
-// kv_tile.h -- the mathematics of attention over the paged FP4 cache that its kernels share: a wave's tile of rows, the
-// loads of a step, and a workgroup's place in the work.
+// kv_tile.h -- the mathematics of attention over the paged FP4 cache: a wave's tile of rows, the loads of a step, and a
+// workgroup's place in the work.
 #pragma once
 
 #include <type_traits>

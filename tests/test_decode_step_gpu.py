@@ -235,6 +235,17 @@ def test_long_among_short(lengths, starts, hq, hkv, D, S, window, t):
         assert torch.equal(y, mnb.kv_attention(q.to(DEV), s.cache, s.pages, s.lengths, starts=st, window=window))
 
 
+@pytest.mark.parametrize("hq,D,long", [(24, 128, 4200), (40, 64, 4200), (24, 96, 700)])
+def test_many_heads_of_one(hq, D, long):
+    """Tiles of 32 rows of a single token's heads: a short one, one and a part, an item shared by workgroups."""
+    lengths = [long] + [150] * (39 if long > 1000 else 300)
+    s, q, y, _ = run_attention(np.random.default_rng(D), lengths, None, hq, 1, D, 64, 0, torch.bfloat16)
+    c = mnb.mnb_kv_cache(None, 0, s.cache.pages, 1, D, 64)
+    text = mnb.mnb_kv_describe_route(c, mnb.mnb_kv_rows(None, 0, None, None, len(lengths), s.width, len(lengths)), hq, 0)[1]
+    assert "tile=32" in text
+    assert torch.equal(y, mnb.kv_attention(q.to(DEV), s.cache, s.pages, s.lengths))
+
+
 @pytest.mark.parametrize("t", [torch.float16, torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("V", [1 << 20, 1 << 22])
 def test_sample_of_long_rows(V, t):
