@@ -360,12 +360,13 @@ struct Work {
   int b;
   bool whole;
 };
-// Shares of steps balance what sequences of different lengths take, but cost a second kernel and parts of two items a
-// workgroup.  So where there is a workgroup for each item they are taken, by the lengths that the call finds, only if the
-// longest item is longer than two shares and kPatience steps: one row each of heads of 128 (32 query and 8 key/value),
-// cut against whole: 16 sequences of 4096 27.0 and 23.6 us, 32 of 4096 35.0 and 26.2, 64 of 4096 57.0 and 49.1, 32 of 1024 22.4
-// and 10.8; one of 131072 41 us against 4096 steps by one workgroup.
-constexpr int kPatience = 96;
+// Shares of steps balance what sequences of different lengths take, but cost parts of two items a workgroup and their
+// join.  So where there is a workgroup for each item they are taken, by the lengths that the call finds, only if the
+// longest item is longer than five shares and kPatience steps.  One row each of heads of 128 (32 query and 8 key/value),
+// cut against whole: 32 sequences of 4096 35.0 and 30.2 us, 64 of 4096 57.0 and 51.3, 32 of 1024 22.4 and 10.9, 24 of 4096 28.0
+// and 27.6, 32 of different lengths up to 4096 41.5 and 27.8; but one of 2048 11.4 and 16.6, four of 2048 12.2 and 16.9, 16 of 8192
+// 35.3 and 36.4.
+constexpr int kPatience = 16;
 __device__ __forceinline__ Work find_work(const KvAttnParams &p) {
   Work w{};
   const int lane = threadIdx.x & 63;
@@ -399,7 +400,7 @@ __device__ __forceinline__ Work find_work(const KvAttnParams &p) {
     steps = lane_of(steps, 0);
     most = __builtin_amdgcn_readlane(most, 0);
     w.share = (steps + p.workgroups - 1) / p.workgroups;
-    w.whole = items <= p.workgroups && most <= 2 * w.share + kPatience;
+    w.whole = items <= p.workgroups && most <= 5 * w.share + kPatience;
     if (w.share < 2 * kWaves) w.share = 2 * kWaves;       // no smaller parts than two steps a wave
     if (w.whole) w.share = 1;
   }
