@@ -42,7 +42,9 @@ constexpr int resident(int D, int R) { return D <= (R == 1 ? 128 : 64) ? 3 : 2; 
 // Tiles of 32 rows read and expand the cache half as often as those of 16.  They are taken where sequences have more than 16
 // rows and there is work for every CU, of heads whose tile leaves two waves to a SIMD.  16 against 32: 2048 rows of one
 // sequence 77.5 and 66.0 us, 256 rows over 4096 45.9 and 35.8, 8 sequences of 16 rows over 2048 28.9 and 24.9 (32/8 heads
-// of 128); with less work 8 of 5 rows over 2001 17.7 and 20.1 (20/4 heads of 96).
+// of 128); with less work 8 of 5 rows over 2001 17.7 and 20.1 (20/4 heads of 96).  Heads of 192 are left out although 2048 rows
+// of one sequence (32/8 heads) would take 109 us for 127: their tile needs more registers than a wave has, and the
+// copies that the compiler then makes are those it has misplaced (see the queries' loads).
 constexpr int kTwoTiles = 128;
 
 template <int DT, int D, int R>
@@ -83,13 +85,16 @@ __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAtt
     T x;
     x.clear();
     const int tokens = c.seq.n, row0 = tile * kRows;     // row of the sequence: token row / G, head row % G
+    // Rows that the tile does not have take the last token's, as zeros: no load of a step or before it stands under a condition
+    // on lanes, so none part while the tile's registers are live.  (Where they did, at 32 rows of 192, whose registers pass
+    // a wave's 256, the compiler put its copies of others ahead of the lanes' return.)
 #pragma unroll
     for (int w = 0; w < R; ++w) {
-      const int row = row0 + 16 * w + r, i = row / p.G, gh = row - i * p.G;
-      const bool real = i < tokens;
-      const uint16_t *q = p.q + (int64_t)(c.seq.row0 + i) * p.ldq + (int64_t)(h * p.G + gh) * D + g * (D / 4);
+      const int row = row0 + 16 * w + r, token = row / p.G, gh = row - token * p.G, i = min(token, tokens - 1);
+      const uint32_t real = token < tokens ? 0xffffffffu : 0;
+      const u4_t *q = reinterpret_cast<const u4_t *>(p.q + (int64_t)(c.seq.row0 + i) * p.ldq + (int64_t)(h * p.G + gh) * D + g * (D / 4));
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) x.q[w][k] = real ? reinterpret_cast<const u4_t *>(q)[k] ^ p.flip : u4_t{0, 0, 0, 0};
+      for (int k = 0; k < D / 32; ++k) x.q[w][k] = (q[k] ^ p.flip) & real;
       x.pos[w] = real ? c.seq.first() + i : -1;
       x.lo[w] = p.window ? x.pos[w] - p.window + 1 : 0;
     }
@@ -104,13 +109,10 @@ __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAtt
     bool bad = c.beyond;
     const int32_t *pages = p.rows.pages + (int64_t)b * p.rows.ldp;
     auto page_of = [&](int t, bool needed) {
-      const int col = t >> p.cache.shift;
-      int page = needed && col < p.rows.width ? pages[col] : -1;
-      if ((uint32_t)page >= (uint32_t)p.cache.pages) {
-        bad |= needed;
-        page = 0;
-      }
-      return page;
+      const int col = t >> p.cache.shift, page = pages[min(col, p.rows.width - 1)];   // (no step is taken where the width is 0)
+      const bool there = col < p.rows.width && (uint32_t)page < (uint32_t)p.cache.pages;
+      bad |= needed && !there;
+      return needed && there ? page : 0;
     };
     // The places of 32 steps of the wave, two a step, a lane each; a step's data is loaded while the one before is used.
     for (int s = f0 + wave; s < f1;) {
