@@ -137,8 +137,8 @@ __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAtt
       }
       s += count * kWaves;
     }
-    for (int s = e0 + wave; s < e1; s += kWaves) {
-      if (s >= f0 && s < f1) continue;
+    // steps that some row does not see whole
+    auto alone = [&](auto far, int s) {
       const int t0 = c.from + s * kStep;
       typename T::Raw raw;
 #pragma unroll
@@ -146,7 +146,18 @@ __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAtt
         const int t = t0 + 16 * k;
         T::load(raw, k, p.cache.data, half_step(p.cache, h, page_of(t, t <= pos1 && t + 15 >= any_lo), t), offsets);
       }
-      x.template step<true>(raw, p.scale, t0, g, r, any_lo, pos1);
+      x.template step<true, decltype(far)::value>(raw, p.scale, t0, g, r, any_lo, pos1);
+    };
+    for (int s = e0 + wave; s < e1; s += kWaves)
+      if (s < f0 || s >= f1) alone(std::false_type(), s);
+    if constexpr (DT == DT_F16) {
+      if (__builtin_expect(__any(x.top >= T::kFar), 0)) {
+        x.clear();
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k)                      // the wave's whole steps, and its others
+          for (int s = (k ? e0 : f0) + wave; s < (k ? e1 : f1); s += kWaves)
+            if (k == 0 || s < f0 || s >= f1) alone(std::true_type(), s);
+      }
     }
     const int rows = (int)min((int64_t)kRows, (int64_t)tokens * p.G - row0);
     if (part && threadIdx.x == 0 && stop == item0 + span) {

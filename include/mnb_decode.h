@@ -95,8 +95,9 @@ int mnb_kv_read(const mnb_kv_cache *cache, const mnb_kv_rows *rows, void *k, int
  * position p and, where window > 0, behind p - window.  q_heads is a multiple of kv_heads; query
  * head h reads key/value head h / (q_heads / kv_heads).  A row that sees nothing is zeros.
  * q, y [rows, q_heads, head_dim] fp16 or bf16, aligned as above; y may be q itself.  Scores and sums are in
- * 32 bits; probabilities, keys and values enter the matrix instructions in q's type (bf16 holds every
- * key and value exactly; fp16 those up to 65504 and in steps of 2^-24, as fp16 data gives).
+ * 32 bits; probabilities, keys and values enter the matrix instructions in q's type.  bf16 holds every
+ * key and value exactly; fp16 in steps of 2^-24, values up to 65504, as fp16 data gives, and keys up to 2^31, more than a
+ * norm, weights and a rotation make of fp16 data.  What is larger (appended in bf16, read with fp16 queries) becomes infinite.
  * NaN or infinities among tokens that a row does not see do not reach it.
  * workspace: at least mnb_kv_attention_workspace_bytes bytes, 16-byte aligned (NULL if that is 0).
  */

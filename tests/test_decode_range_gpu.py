@@ -1,0 +1,59 @@
+"""Numbers at the ends of the ranges of include/mnb_decode.h, on the GPU, against plain 64-bit references."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+import _decode_ref as dref
+from _util import ensure_lib
+from test_decode_gpu import DEV, Setup, bound, dev, f64, heads, ints, rng
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+mnb = ensure_lib()
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("lengths,starts,hq,hkv,D,S,window", [
+    ([200, 33, 1], None, 4, 2, 64, 16, 0), ([150, 70], [0, 5, 40], 6, 2, 96, 32, 60), ([3000], None, 8, 2, 128, 64, 0),
+    ([100], [0, 100], 3, 1, 192, 16, 0), ([90, 64], [0, 40, 80], 4, 2, 256, 16, 0), ([1500], [0, 1500], 24, 24, 64, 64, 0)])
+def test_keys_past_fp16(lengths, starts, hq, hkv, D, S, window, norm):
+    """fp16 keys that a rotation (65504 turned by an eighth is 92637) or a weight takes past fp16 are in the cache as the numbers
+    they are, and attention takes them so, among ordinary ones.  A key's blocks are exact in both parts of the product, which
+    are summed in 32 bits as all scores are: the bound is theirs."""
+    t, r = torch.float16, rng(30, len(lengths), D)
+    s = Setup(r, lengths, hkv, D, S)
+    total, place = sum(lengths), dref.places(lengths, starts)
+    whole = [0, *np.cumsum(lengths).tolist()]
+    k, v = heads(r, total, hkv, D, t), heads(r, total, hkv, D, t)
+    large = torch.from_numpy(r.random((total, hkv, 1)) < 0.3) & (torch.arange(D) % (D // 2) < D // 4)      # both of a pair
+    weight = None
+    if norm:
+        weight = torch.where(torch.arange(D) % 96 < 40, 60000.0, 1.0).to(t)
+    else:
+        k = torch.where(large, (60000 + 5000 * torch.from_numpy(r.random(k.shape))) * torch.sign(k.double()), k.double()).to(t)
+    tab = mnb.rope_table(s.width * S, D, device=DEV)
+    mnb.kv_append(None, k.to(DEV), v.to(DEV), s.cache, s.pages, s.lengths, starts=ints(whole), rope=tab,
+                  k_weight=None if weight is None else weight.to(DEV))
+    pos = np.concatenate([np.arange(n) for n in lengths])
+    keys = dref.fp4(dref.norm_rotate(f64(k), None if weight is None else f64(weight), 1e-6, tab.cpu().numpy()[pos], False))
+    values = dref.fp4(f64(v))
+    assert (np.abs(keys) >= 65536).any() and np.isfinite(keys).all()
+    q = (heads(r, len(place), hq, D, t).double() * 2.0 ** -14).to(t)
+    c = D ** -0.5 * 0.25
+    y = f64(mnb.kv_attention(q.to(DEV), s.cache, s.pages, s.lengths, starts=None if starts is None else ints(starts), scale=c, window=window))
+    row = 0
+    for b, n in enumerate(lengths):
+        m = 1 if starts is None else starts[b + 1] - starts[b]
+        kb, vb, qb = keys[whole[b]:whole[b + 1]], values[whole[b]:whole[b + 1]], f64(q[row:row + m])
+        want, size = dref.attention(qb, kb, vb, n - m, c, window) if m <= 100 else (None, None)
+        at = np.arange(m)
+        if want is None:                                        # some rows are enough
+            at = np.array([0, 1, 31, 32, m // 2, m - 1])
+            got = [dref.attention(qb[i:i + 1], kb[:n - m + i + 1], vb[:n - m + i + 1], n - m + i, c, window) for i in at]
+            want, size = (np.concatenate(x) for x in zip(*got))
+        score = float(max(np.abs(qb[:, h] * 1.0).max(0) @ np.abs(kb[:, h // (hq // hkv)]).max(0) for h in range(hq))) * c
+        assert np.isfinite(y[row:row + m]).all()
+        assert (np.abs(y[row + at] - want) <= bound(want, size, t, score, n, D)).all(), (b, float(np.abs(y[row + at] - want).max()))
+        row += m
