@@ -31,7 +31,7 @@ __device__ __forceinline__ int find_sequence(const KvRows &r, int row) {
   return max(0, count - 1);
 }
 
-enum Where { kHeld, kNowhere, kUnreachable, kForeign };   // kForeign: the row of no sequence
+enum Where { kHeld, kNowhere, kUnreachable, kForeign, kUnturned };   // kForeign: the row of no sequence; kUnturned: past the table
 struct Place {
   Where where;
   int pos, page, at;
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(1024) void append_kernel(KvAppendParams p) {
   const u4_t wk = p.kw && in ? *reinterpret_cast<const u4_t *>(p.kw + 8 * l) : none;
   Place at = find_place(p.cache, p.rows, row);
   if (at.where == kForeign) return;
-  if (at.where == kHeld && p.rot && at.pos >= p.table_rows) at.where = kUnreachable;
+  if (at.where == kHeld && p.rot && at.pos >= p.table_rows) at.where = kUnturned;
   uint8_t *page = p.cache.data + (int64_t)at.page * p.cache.page_stride;
   Turn turn{};
   if (at.where == kHeld) turn = find_turn<LANES>(p, l, at.pos);
@@ -182,6 +182,12 @@ __global__ __launch_bounds__(1024) void append_kernel(KvAppendParams p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = fill;
         store8<DT>(out, x);
+      }
+      // what is read at that place later is NaN, not what it held before
+      if (at.where == kUnturned && !is_q && on && (l & 3) == 0) {
+        uint8_t *head = page + (int64_t)hk * kv_head_bytes(S, D);
+        const int key = kv_key_scales(S, D) + at.at * (D / 32) + l / 4;
+        head[is_k ? key : kv_value_scales(S, D) + ((at.at >> 2) * (D / 32) + l / 4) * 4 + (at.at & 3)] = 255;
       }
       continue;
     }

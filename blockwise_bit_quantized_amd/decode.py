@@ -169,8 +169,8 @@ def kv_append(q, k, v, cache: KvCache, pages, lengths, starts=None, rope=None, q
 
     Sequence b has ``lengths[b]`` tokens in the cache after the call (int32), the rows starts[b] .. starts[b + 1] - 1 last
     (``starts`` int32 [batch + 1]; None: one row each); position p lies in page ``pages[b, p // page_size]`` (int32
-    [batch, width]).  A row at a negative position gives zeros and is not stored; one past the pages' width, past the
-    table or in a page out of range gives NaN and is not stored; rows behind the last sequence are not
+    [batch, width]).  A row at a negative position gives zeros and is not stored; one past the pages' width or in a page
+    out of range gives NaN and is not stored; one past the table gives NaN and is stored as NaN; rows behind the last sequence are not
     written.  Positions of a call must not share a place in a page."""
     return ops._run(ops._ext.kv_append, k, q, v, *cache._args(), pages, lengths, starts, rope, q_weight, k_weight, eps,
                     interleaved, out)

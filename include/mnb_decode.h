@@ -51,9 +51,9 @@ typedef struct {
  * bounds:
  *   - a row at a negative position (a sequence of length 0 that is given a row) has no
  *     position: its results are zeros and nothing is stored for it;
- *   - a position past width * page_size, past the rotation table's end, or in a page whose number is not
- *     in [0, pages) stores nothing and its row becomes NaN, and attention over a sequence with such
- *     positions among those that its rows see gives NaN;
+ *   - a position past width * page_size, or in a page whose number is not in [0, pages), stores nothing and
+ *     its row becomes NaN; one past the rotation table's end stores NaN in its place (keys and values), and its
+ *     row becomes NaN.  Attention gives NaN in rows that see such a position, and may in other rows of that sequence;
  *   - rows at or behind starts[batch] belong to no sequence and are left as they were.
  */
 typedef struct {

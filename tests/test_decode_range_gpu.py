@@ -57,3 +57,38 @@ def test_keys_past_fp16(lengths, starts, hq, hkv, D, S, window, norm):
         assert np.isfinite(y[row:row + m]).all()
         assert (np.abs(y[row + at] - want) <= bound(want, size, t, score, n, D)).all(), (b, float(np.abs(y[row + at] - want).max()))
         row += m
+
+
+@pytest.mark.parametrize("t", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 96, 256])
+def test_positions_past_the_table(D, t):
+    """A row past the table is NaN, and so is what is read and attended to at its place, whatever the place held; nothing else is
+    touched.  A row past the table and the pages stores nothing."""
+    r, S, hkv, hq = rng(31, D), 16, 2, 4
+    s = Setup(r, [40, 41, 20, 70], hkv, D, S, width=4)           # the last one lies past the pages
+    s.data.zero_()
+    old = heads(r, 101, hkv, D, t).to(DEV)
+    old_starts = ints([0, 40, 81, 101, 101])
+    mnb.kv_append(None, old, old, s.cache, s.pages, s.lengths, starts=old_starts)
+    before = s.data.clone()
+    x, q = heads(r, 4, hkv, D, t).to(DEV), heads(r, 4, hq, D, t).to(DEV)
+    got = mnb.kv_append(q, x, x, s.cache, s.pages, s.lengths, rope=mnb.rope_table(39, 32, device=DEV))
+    assert bool(got[[0, 1, 3]].isnan().all()) and bool(got[2].isfinite().all())
+    k, v = mnb.kv_read(s.cache, s.pages, s.lengths, dtype=t)
+    for y in (k, v):
+        assert bool(y[[0, 1, 3]].isnan().all()) and bool(y[2].isfinite().all())
+    # the scales of positions 39 and 40 are 255, and beside them only what the third row wrote has changed
+    changed = (s.data != before).nonzero()
+    places = {int(s.pages_host[0, 2]), int(s.pages_host[1, 2]), int(s.pages_host[2, 1])}
+    assert set(changed[:, 0].tolist()) <= places
+    for b, p in ((0, 39), (1, 40)):
+        at = changed[changed[:, 0] == int(s.pages_host[b, 2])][:, 1].cpu().numpy() % (S * (D + D // 16))
+        i = p % S
+        mine = [*range(S * D + i * (D // 32), S * D + (i + 1) * (D // 32)),
+                *(S * D + S * D // 32 + (i // 4 * (D // 32) + j) * 4 + i % 4 for j in range(D // 32))]
+        assert sorted(set(at.tolist())) == sorted(mine)
+    # whoever sees that place later gets NaN, with any query
+    y = mnb.kv_attention(q, s.cache, s.pages, ints([40, 41, 20, 0]))
+    assert bool(y[:2].isnan().all()) and bool(y[2].isfinite().all())
+    y = mnb.kv_attention(q, s.cache, s.pages, ints([39, 40, 20, 0]))
+    assert bool(y.isfinite().all())
