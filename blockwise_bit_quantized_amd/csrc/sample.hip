@@ -1,10 +1,14 @@
 // sample.hip -- one token for each row of logits, by temperature, top-k, top-p and min-p, from a given number.
 //
 // With m the largest logit, weights are whole numbers w = rint(2^((x - m) log2(e) / temperature) 2^S) in 64
-// bits, S such that a row's sum stays below 2^63: their sums depend on no order, and a token is that of the
-// 64-bit definition unless u falls within about 2^-40 of a border between two tokens (sums in 32 bits
-// would move one in some thousand rows of a flat distribution).  The power is a polynomial in 64 bits, whose
-// instructions run at the rate of 32-bit ones here.
+// bits, S = min(46, 62 - ceil(log2 V)), so that a row's sum stays below 2^63: their sums depend on no order (sums in 32 bits
+// would move one token in some thousand rows of a flat distribution).  How exact they are, in units of 2^-S of the largest
+// weight: a running sum rounds that of each eight neighbours once, V / 16 + 1 at most (of up to 1024 collected logits each
+// weight, 512); the powers and their exponents are off by 3 2^-52 of a weight, V / 22 in a sum; u times the whole is rounded to 53
+// bits, V / 64; and both the whole and the running sum have these errors.  So the token is the definition's where u
+// times the whole lies further than V / 4 + 1024 units from every border: 2^-32 at 49152 logits, 2^-20 at 2^22.  The
+// sums that find the border of top-p round each weight, V / 2: there it is 5 V / 4 + 1024.  The power is a
+// polynomial in 64 bits, whose instructions run at the rate of 32-bit ones here.
 //
 // A workgroup of 8 or 16 waves takes a row, each wave a run of it, 512 logits a round, read again (from L2) in
 // each pass.  What stays is told by one key: order bits of the number over the complement of the index.

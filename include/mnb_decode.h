@@ -123,8 +123,9 @@ int mnb_kv_describe_route(const mnb_kv_cache *cache, const mnb_kv_rows *rows, in
  * A row that holds a NaN or +infinity or nothing but -infinity, a temperature that is negative, infinite or NaN, and a NaN in u, top_p
  * or min_p, have no distribution: tokens[m] = -1.
  * Each parameter is an array [M] (FP32, top_k int32) or, where that is NULL, the number beside it.
- * p and their sums are held in 64 bits as whole numbers of 2^-40 of the largest p, so the choice depends
- * on no order of summation.
+ * p and their sums are held in 64 bits as whole numbers of 2^-S of the largest p, S = min(46, 62 - ceil(log2 V)), so the choice
+ * depends on no order of summation.  It is that of exact arithmetic unless u times the whole sum lies within (V / 4 + 1024) 2^-S
+ * times the largest p of a border between tokens, or top_p times it within (5 V / 4 + 1024) 2^-S.
  */
 int mnb_sample(const void *logits, int dtype, int M, int V, int64_t ldl, const float *u, const float *temperature,
                float temperature_all, const int32_t *top_k, int top_k_all, const float *top_p, float top_p_all,

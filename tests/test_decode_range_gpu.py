@@ -92,3 +92,49 @@ def test_positions_past_the_table(D, t):
     assert bool(y[:2].isnan().all()) and bool(y[2].isfinite().all())
     y = mnb.kv_attention(q, s.cache, s.pages, ints([39, 40, 20, 0]))
     assert bool(y.isfinite().all())
+
+
+# Sampling over a peak and a flat tail of tiny weights, which are whole numbers of 2^-S of the peak.  In such units a running
+# sum rounds that of each eight neighbours once, V / 16 + 1; powers and exponents are off by 3 2^-52 of a weight, V / 22 of at most V
+# weights of at most 2^46 units; u times the whole is rounded to 53 bits, V / 64; goal and running sum both have
+# them: less than V / 4 + 4.
+def unit(V):
+    return 2.0 ** -min(46, 62 - int(np.ceil(np.log2(V))))
+
+
+@pytest.mark.parametrize("tail", [-44.0, -41.2, -38.3, -30.0])
+@pytest.mark.parametrize("V,peak", [(1 << 22, 1 << 21), ((1 << 22) - 5, (1 << 22) - 6), (131072, 70001)])
+def test_sample_of_a_flat_tail(V, peak, tail):
+    x = torch.full((1, V), tail * np.log(2.0), dtype=torch.float32, device=DEV)
+    x[0, peak] = 0.0
+    w = np.exp(f64(x)[0])
+    end = np.cumsum(w)
+    tol = (V / 4 + 4) * unit(V)
+    r = rng(50, V, int(-tail))
+    for u in [0.0, 1 - 2.0 ** -24, 0.5, *(r.random(6) * end[max(peak - 1, 0)] / end[-1])]:
+        u = float(np.float32(u))
+        got = int(mnb.sample(x, torch.tensor([u], device=DEV))[0])
+        assert 0 <= got < V
+        low, high, goal = (end[got - 1] if got else 0.0), end[got], u * end[-1]
+        assert low - tol <= goal < high + tol, (u, got, peak)
+
+
+@pytest.mark.parametrize("tail", [-38.3, -30.0, -24.5])
+@pytest.mark.parametrize("V", [1 << 22, 131072])
+def test_top_p_within_a_flat_tail(V, tail):
+    """The border of top-p in the tail, seen by the last token that stays.  The sums that find it round each weight, and
+    prefix and share of the whole are each off by V / 2 units for that, and by the other errors above: 5 V / 4; then those of u."""
+    x = torch.full((1, V), tail * np.log(2.0), dtype=torch.float32, device=DEV)
+    x[0, 0] = 0.0
+    w = np.exp(f64(x)[0])
+    end = np.cumsum(w)
+    tol = (5 * V / 4 + V / 4 + 4) * unit(V)
+    u = float(np.float32(1 - 2.0 ** -24))
+    for share in (0.1, 0.5, 0.93):
+        top_p = float(np.float32((1 + share * (end[-1] - 1)) / end[-1]))
+        if top_p >= 1 or top_p * end[-1] <= 1:
+            continue                                             # the tail is below a step of top_p
+        got = int(mnb.sample(x, torch.tensor([u], device=DEV), 1.0, 0, top_p)[0])
+        stays = min(V, int(np.searchsorted(end, top_p * end[-1])) + 1)
+        want = u * end[stays - 1]
+        assert end[got] > want - tol and (end[got - 1] if got else 0.0) < want + tol, (share, got, stays)
