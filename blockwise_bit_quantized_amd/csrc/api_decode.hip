@@ -212,6 +212,9 @@ int mnb_kv_attention(const mnb_kv_cache *cache, const mnb_kv_rows *rows, const v
   p.flip = scale < 0.f ? 0x80008000u : 0;
   p.whole = k.whole;
   p.workgroups = k.workgroups;
+  p.lone = k.lone;
+  p.sharers = k.sharers;
+  p.least = k.least;
   p.tile_rows = k.tile_rows;
   p.slot_rows = k.slot_rows;
   p.part = static_cast<float *>(workspace);

@@ -79,13 +79,16 @@ struct KvAttnParams {
   uint32_t flip;       // these bits
   int whole;           // every item goes to one workgroup, whatever the lengths are
   int workgroups;      // of the first kernel
+  int lone;            // the first of them, which take an item each (0: as the lengths say)
+  int sharers;         // those behind, which share out the steps of items that are cut
+  int least;           // an item of at most so many steps is not cut
   int tile_rows;       // 16 or 32
   int slot_rows;       // rows of a partial result
-  float *part;         // what the second kernel is told of each workgroup, then [workgroups, 2, slot_rows, D + 4]
+  float *part;         // what the second kernel is told of each sharer, then [sharers, 2, slot_rows, D + 4]
 };
 // The workgroups for these sizes, and whether items may be split over them.
 struct KvPlan {
-  int workgroups, whole, tile_rows, slot_rows;
+  int workgroups, lone, sharers, least, whole, tile_rows, slot_rows;
   int64_t items;       // at most
   size_t bytes;        // of the workspace
 };

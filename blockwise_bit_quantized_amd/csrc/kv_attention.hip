@@ -14,7 +14,8 @@
 //
 // Items (sequence, tile of rows, head) go to a workgroup each where that is fast enough.  Else they are cut in steps of 32
 // tokens, laid end to end and shared out evenly, so a long sequence among short ones does not keep one workgroup; a
-// workgroup's first and last item may be parts, which a second kernel joins in their order.
+// workgroup's first and last item may be parts, which a second kernel joins in their order.  Where items are many, only
+// those of long sequences are cut, by workgroups behind the others'.
 //
 // Few rows are bound by memory and the latencies around it: 32 sequences of 4096 (32/8 heads of 128, 143 MB) take 26 us, 5.4 TB/s,
 // and 4 for the second kernel's launch, one of 131072 29 us and 6.5 to join its 768 parts; one of 700 (14/2 heads of 64) 7.5 us.  Many rows are bound by
@@ -58,10 +59,11 @@ __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAtt
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, r = lane & 15;
   const uint32_t S = 1u << p.cache.shift;
   const typename T::Offsets offsets(g, r, S);
-  Joint *joint = reinterpret_cast<Joint *>(p.part) + blockIdx.x;
-  float *parts = p.part + (int64_t)p.workgroups * (sizeof(Joint) / 4);
-  const Work work = find_work(p);
-  if (!p.whole && threadIdx.x == 0) joint->rows = 0;
+  float *parts = p.part + (int64_t)p.sharers * (sizeof(Joint) / 4);
+  Work work = find_work(p);
+  const int sharer = (int)blockIdx.x - p.lone;           // (negative: takes an item alone)
+  Joint *joint = reinterpret_cast<Joint *>(p.part) + sharer;
+  if (!p.whole && threadIdx.x == 0 && sharer >= 0) joint->rows = 0;
   if (work.end == 0) return;
   int64_t at = work.at, begin = work.begin;
   int b = work.b;
@@ -69,10 +71,10 @@ __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAtt
   bool first_item = true;
   while (at < work.end && b < p.rows.batch) {
     const Cut c = cut_of(p, b);
-    const int64_t span = whole ? 1 : c.steps, mine = span * c.tiles * p.cache.heads;
+    const int64_t span = whole ? 1 : c.steps > p.least ? c.steps : 0, mine = span * c.tiles * p.cache.heads;
     if (at >= begin + mine) {                            // on to the next sequence
       begin += mine;
-      ++b;
+      b = next_holder(p, whole, b);
       continue;
     }
     const int item = (int)((at - begin) / span);
@@ -203,7 +205,7 @@ __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAtt
         }
         const int row = row0 + 16 * w + rr;
         if (part) {
-          float *to = parts + (((int64_t)blockIdx.x * 2 + (first_item ? 0 : 1)) * p.slot_rows + 16 * w + rr) * (D + 4);
+          float *to = parts + (((int64_t)sharer * 2 + (first_item ? 0 : 1)) * p.slot_rows + 16 * w + rr) * (D + 4);
           if (d == 0) {
             to[D] = m;
             to[D + 1] = l;
@@ -233,7 +235,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(KvAttnParams p) {
   const Joint j = reinterpret_cast<const Joint *>(p.part)[blockIdx.x];
   const int from_row = 16 * blockIdx.y, rows = min(16, j.rows - from_row);
   if (rows <= 0) return;
-  const float *parts = p.part + (int64_t)p.workgroups * (sizeof(Joint) / 4);
+  const float *parts = p.part + (int64_t)p.sharers * (sizeof(Joint) / 4);
   const int n = (int)blockIdx.x - j.first + 1, slots = rows * (D / 4);   // at most 1024, of 16 rows of 256
   const int groups = kJoinThreads / slots, t = threadIdx.x, group = t / slots, s = t - group * slots;
   const int rr = s / (D / 4), d = (s - rr * (D / 4)) * 4;
@@ -287,7 +289,7 @@ hipError_t launch(const KvAttnParams &p, hipStream_t s) {
   if (p.tile_rows == 16) hipLaunchKernelGGL((rows_kernel<DT, D, 1>), grid, block, 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.whole) return e;
-  hipLaunchKernelGGL((join_kernel<DT, D>), dim3((uint32_t)p.workgroups, p.tile_rows / 16), dim3(kJoinThreads), 0, s, p);
+  hipLaunchKernelGGL((join_kernel<DT, D>), dim3((uint32_t)p.sharers, p.tile_rows / 16), dim3(kJoinThreads), 0, s, p);
   return hipGetLastError();
 }
 template <int DT>
@@ -315,12 +317,17 @@ KvPlan kv_attn_plan(const KvCache &c, const KvRows &r, int G, int window) {
   k.items = tiles(k.tile_rows) * c.heads;
   k.slot_rows = r.starts || G > k.tile_rows ? k.tile_rows : G;
   const int64_t most = k.items * steps / kLeast + 1, room = resident(c.D, k.tile_rows / 16) * kCUs;
-  // By these sizes alone whole items are taken where there are two rounds of them or none is long (the kernel decides
-  // the rest by the lengths): cut against whole, 256 sequences of 1024 64.1 and 49.7 us, one of 700 (14/2 heads of 64) 13.0
-  // and 8.0.
-  k.whole = k.items >= 2 * room || steps <= 40;
-  k.workgroups = (int)(k.whole || k.items > room ? k.items : most < room ? most : room);
-  k.bytes = k.whole ? 0 : (size_t)k.workgroups * (sizeof(Joint) + (size_t)2 * k.slot_rows * (c.D + 4) * 4);
+  // By these sizes alone items are whole where none can be long against the rounds of them that a place on the card takes: a round
+  // takes 6 us or more, a step of a workgroup's four waves 0.15 to 0.2 (one of 700 tokens, 14/2 heads of 64, 7.5 us whole, 13.0
+  // cut).  Else the lengths decide, in the kernel: of up to two rounds for all items together, of more for those that are long.
+  const int64_t rounds = k.items / room;
+  const int short_steps = (int)(rounds < 2 ? 40 : 40 + 16 * rounds);
+  k.whole = steps <= short_steps;
+  k.lone = !k.whole && rounds >= 2 ? (int)k.items : 0;
+  k.least = k.lone ? short_steps : 0;
+  k.sharers = (int)(k.lone ? room : k.items > room ? k.items : most < room ? most : room);
+  k.workgroups = k.whole ? (int)k.items : k.lone + k.sharers;
+  k.bytes = k.whole ? 0 : (size_t)k.sharers * (sizeof(Joint) + (size_t)2 * k.slot_rows * (c.D + 4) * 4);
   return k;
 }
 

@@ -346,7 +346,7 @@ struct Cut {
 __device__ __forceinline__ Cut cut_of(const KvAttnParams &p, int b) {
   Cut c;
   c.seq = kv_seq(p.rows, b);
-  c.tiles = (int)(((int64_t)c.seq.n * p.G + p.tile_rows - 1) / p.tile_rows);
+  c.tiles = (int)(((int64_t)c.seq.n * p.G + p.tile_rows - 1) >> (p.tile_rows == 32 ? 5 : 4));
   const int lo = p.window ? max(0, c.seq.first() - p.window + 1) : 0;
   c.from = lo / kStep * kStep;
   c.beyond = c.seq.len > p.rows.width << p.cache.shift;
@@ -360,9 +360,9 @@ struct Cost {
   int steps;
 };
 __device__ __forceinline__ Cost cost_of(const KvAttnParams &p, int b) {
-  if (b >= p.rows.batch) return Cost{0, 0};
-  const Cut c = cut_of(p, b);
-  return Cost{(int64_t)c.tiles * p.cache.heads, c.tiles ? c.steps : 0};
+  const Cut c = cut_of(p, min(b, p.rows.batch - 1));
+  const int tiles = b < p.rows.batch ? c.tiles : 0;
+  return Cost{(int64_t)tiles * p.cache.heads, tiles ? c.steps : 0};
 }
 
 // Sums over the wave's lanes up to this one.  (Every wave finds the workgroup's place in the work by itself.)
@@ -382,65 +382,105 @@ struct Work {
   int b;
   bool whole;
 };
-// Shares of steps balance what sequences of different lengths take, but cost parts of two items a workgroup and their
-// join.  So where there is a workgroup for each item they are taken, by the lengths that the call finds, only if the
-// longest item is longer than five shares and kPatience steps.  One row each of heads of 128 (32 query and 8 key/value),
-// cut against whole: 32 sequences of 4096 35.0 and 30.2 us, 64 of 4096 57.0 and 51.3, 32 of 1024 22.4 and 10.9, 24 of 4096 28.0
-// and 27.6, 32 of different lengths up to 4096 41.5 and 27.8; but one of 2048 11.4 and 16.6, four of 2048 12.2 and 16.9, 16 of 8192
-// 35.3 and 36.4.
-constexpr int kPatience = 16;
-__device__ __forceinline__ Work find_work(const KvAttnParams &p) {
-  Work w{};
+// What a sequence adds to the work: items, or steps of those items that may be cut.
+__device__ __forceinline__ int64_t part_of(const KvAttnParams &p, bool whole, const Cost &c) {
+  return whole ? c.items : c.steps > p.least ? c.items * c.steps : 0;
+}
+// The sequence that holds w.at: w.b and w.begin, or w.end = 0 if none does.  (`first`: costs of the first 64.)
+__device__ __forceinline__ void find_holder(const KvAttnParams &p, Work &w, const Cost &first) {
   const int lane = threadIdx.x & 63;
-  w.share = 1;
-  w.whole = p.whole;
-  if (p.whole && !p.rows.starts) {                       // as many items for each sequence
-    const int each = (p.G + p.tile_rows - 1) / p.tile_rows * p.cache.heads;
-    w.at = blockIdx.x;
-    w.end = w.at + 1;
-    w.b = blockIdx.x / each;
-    w.begin = (int64_t)w.b * each;
-    return w;
-  }
-  const Cost first = cost_of(p, lane);
-  if (!p.whole) {
-    int64_t items = 0, steps = 0;
-    int most = 0;
-    for (int b0 = 0; b0 < p.rows.batch; b0 += 64) {
-      const Cost c = b0 ? cost_of(p, b0 + lane) : first;
-      items += c.items;
-      steps += c.items * c.steps;
-      most = max(most, c.steps);
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      items += __shfl_xor((long long)items, d);
-      steps += __shfl_xor((long long)steps, d);
-      most = max(most, __shfl_xor(most, d));
-    }
-    items = lane_of(items, 0);
-    steps = lane_of(steps, 0);
-    most = __builtin_amdgcn_readlane(most, 0);
-    w.share = (steps + p.workgroups - 1) / p.workgroups;
-    w.whole = items <= p.workgroups && most <= 5 * w.share + kPatience;
-    if (w.share < 2 * kWaves) w.share = 2 * kWaves;       // no smaller parts than two steps a wave
-    if (w.whole) w.share = 1;
-  }
-  w.at = (int64_t)blockIdx.x * w.share;
+  const int64_t end = w.end;
   int64_t before = 0;
+  w.end = 0;                                             // (set behind the loop alone, it would not stay in scalar registers)
   for (int b0 = 0; b0 < p.rows.batch; b0 += 64) {
-    const Cost c = b0 ? cost_of(p, b0 + lane) : first;
-    const int64_t mine = w.whole ? c.items : c.items * c.steps, run = wave_scan(mine) + before;
+    const int64_t mine = part_of(p, w.whole, b0 ? cost_of(p, b0 + lane) : first), run = wave_scan(mine) + before;
     const uint64_t hit = __ballot(run > w.at);
     before = lane_of(run, 63);
     if (hit) {
       const int l = __builtin_ctzll(hit);
       w.b = b0 + l;
       w.begin = lane_of(run - mine, l);
-      w.end = w.at + w.share;
-      break;
+      w.end = end;
+      return;
     }
   }
+}
+// The next sequence behind b that has work (the batch's size: none).  64 are looked at together: those without work in between cost no load
+// behind a load.
+__device__ __forceinline__ int next_holder(const KvAttnParams &p, bool whole, int b) {
+  const int lane = (int)in_loop(threadIdx.x & 63);       // (addresses of lanes kept through the steps cost the tile's registers)
+  for (int b0 = ++b & ~63; b0 < p.rows.batch; b0 += 64) {
+    const int mine = b0 + lane;
+    const uint64_t hit = __ballot(mine >= b && part_of(p, whole, cost_of(p, mine)) > 0);
+    if (hit) return b0 + __builtin_ctzll(hit);
+  }
+  return p.rows.batch;
+}
+// Shares of steps balance what sequences of different lengths take, but cost parts of two items a workgroup and their
+// join.  So where there is a workgroup for each item they are taken, by the lengths that the call finds, only if the
+// longest item is longer than five shares and kPatience steps.  One row each of heads of 128 (32 query and 8 key/value),
+// cut against whole: 32 sequences of 4096 35.0 and 30.2 us, 64 of 4096 57.0 and 51.3, 32 of 1024 22.4 and 10.9, 24 of 4096 28.0
+// and 27.6, 32 of different lengths up to 4096 41.5 and 27.8; but one of 2048 11.4 and 16.6, four of 2048 12.2 and 16.9, 16 of 8192
+// 35.3 and 36.4.
+// Where a place on the card takes two rounds of items or more, only long ones (of more than p.least steps) are ever cut, if the
+// longest is longer than an even share, by workgroups that wait for nothing else: those of other items need not know.  Cut
+// against whole: 256 sequences of 500 with one of 4096 40.5 and 50.5 us, with one of 131072 68 and 594; 2048 rows of a prompt beside 32
+// sequences of up to 32768 200 and 291; 200 of up to 8192 (none longer than a share) 189.1 and 190.8, 4096 rows over 32768 2274 and
+// 2033.  Knowing it costs 2.7 us, of which the second kernel has most: 256 of 1024 49.9 us, 47.2 where the tables are too short for long ones.
+constexpr int kPatience = 16;
+__device__ __forceinline__ Work find_work(const KvAttnParams &p) {
+  Work w{};
+  const bool alone = p.whole || (int)blockIdx.x < p.lone;
+  w.share = 1;
+  w.whole = true;
+  w.at = blockIdx.x;
+  w.end = w.at + 1;
+  if (alone && !p.rows.starts) {                         // as many items for each sequence
+    const int each = (p.G + p.tile_rows - 1) / p.tile_rows * p.cache.heads;
+    w.b = blockIdx.x / each;
+    w.begin = (int64_t)w.b * each;
+    if (p.whole || cut_of(p, w.b).steps <= p.least) return w;
+  }
+  const Cost first = cost_of(p, threadIdx.x & 63);
+  if (alone && p.rows.starts) {
+    find_holder(p, w, first);
+    if (p.whole || w.end == 0 || cut_of(p, w.b).steps <= p.least) return w;
+  }
+  int64_t items = 0, steps = 0, part = 0;                // of the lane's sequences
+  int most = 0;
+#pragma unroll 4
+  for (int b0 = 0; b0 < p.rows.batch; b0 += 64) {
+    const Cost c = b0 ? cost_of(p, b0 + (int)(threadIdx.x & 63)) : first;
+    items += c.items;
+    steps += c.items * c.steps;
+    part += c.steps > p.least ? c.items * c.steps : 0;
+    most = max(most, c.steps);
+  }
+  auto whole_sum = [](int64_t v) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor((long long)v, d);
+    return lane_of(v, 0);
+  };
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) most = max(most, __shfl_xor(most, d));
+  most = __builtin_amdgcn_readlane(most, 0);
+  const int64_t all = whole_sum(steps);
+  const int64_t cut = p.lone ? whole_sum(part) : all, count = p.lone ? 0 : whole_sum(items);
+  const int64_t even = lane_of((all + p.sharers - 1) / p.sharers, 0);   // (a division's result is in vector registers)
+  w.whole = p.lone ? most <= even : count <= p.workgroups && most <= 5 * even + kPatience;
+  if (alone || (p.lone && w.whole)) {
+    if (alone != w.whole) w.end = 0;                     // the others' work
+    return w;
+  }
+  if (!w.whole) {
+    w.share = p.lone ? lane_of((cut + p.sharers - 1) / p.sharers, 0) : even;
+    if (w.share < 2 * kWaves) w.share = 2 * kWaves;      // no smaller parts than two steps a wave
+  }
+  const int64_t total = w.whole ? count : cut;
+  w.at = ((int)blockIdx.x - p.lone) * w.share;
+  w.end = min(w.at + w.share, total);
+  if (w.at < total) find_holder(p, w, first);
+  else w.end = 0;
   return w;
 }
 
