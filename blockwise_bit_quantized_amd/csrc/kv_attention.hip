@@ -17,10 +17,10 @@
 // workgroup's first and last item may be parts, which a second kernel joins in their order.  Where items are many, only
 // those of long sequences are cut, by workgroups behind the others'.
 //
-// Few rows are bound by memory and the latencies around it: 32 sequences of 4096 (32/8 heads of 128, 143 MB) take 26 us, 5.4 TB/s,
-// and 4 for the second kernel's launch, one of 131072 29 us and 6.5 to join its 768 parts; one of 700 (14/2 heads of 64) 7.5 us.  Many rows are bound by
-// the issue of vector instructions, about 220 a step for 33 matrix instructions at tiles of 32 rows of 128, of
-// which the expansion of FP4 is 96: 8192 rows of one sequence 620 to 760 us, 0.72 to 0.89 PFLOP/s.
+// Few rows are bound by memory and the latencies around it: 32 sequences of up to 4096 (32/8 heads of 128, 85 MB) take 26.8 us, and 4 for
+// the second kernel's launch, one of 131072 (143 MB) 29 us, 4.9 TB/s, and 6.6 to join its 768 parts; one of 700 (14/2 heads of 64) 7.4 us.
+// Many rows are bound by the issue of vector instructions, 217 a step for 34 matrix instructions at tiles of 32 rows of 128, of
+// which the expansion of FP4 is 96: 8192 rows of one sequence 610 us, 0.90 PFLOP/s (770 in the first calls behind a pause, by the clocks).
 #include "kv_tile.h"
 
 namespace mnb {

@@ -55,6 +55,8 @@ typedef struct {
  *     its row becomes NaN; one past the rotation table's end stores NaN in its place (keys and values), and its
  *     row becomes NaN.  Attention gives NaN in rows that see such a position, and may in other rows of that sequence;
  *   - rows at or behind starts[batch] belong to no sequence and are left as they were.
+ * Limits, past which a call is MNB_ERR_UNSUPPORTED: width * page_size 2^30, rows and batch below 2^22, heads 65536, rows * q_heads
+ * 2^30, and attention's tiles of 16 or 32 rows of all key/value heads 2^23.
  */
 typedef struct {
   const int32_t *pages;
