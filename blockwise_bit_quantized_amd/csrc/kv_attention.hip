@@ -71,7 +71,7 @@ __global__ __launch_bounds__(kWaves * 64, resident(D, R)) void rows_kernel(KvAtt
   bool first_item = true;
   while (at < work.end && b < p.rows.batch) {
     const Cut c = cut_of(p, b);
-    const int64_t span = whole ? 1 : c.steps > p.least ? c.steps : 0, mine = span * c.tiles * p.cache.heads;
+    const int64_t span = whole ? 1 : c.steps, mine = span * c.tiles * p.cache.heads;
     if (at >= begin + mine) {                            // on to the next sequence
       begin += mine;
       b = next_holder(p, whole, b);
@@ -319,9 +319,10 @@ KvPlan kv_attn_plan(const KvCache &c, const KvRows &r, int G, int window) {
   const int64_t most = k.items * steps / kLeast + 1, room = resident(c.D, k.tile_rows / 16) * kCUs;
   // By these sizes alone items are whole where none can be long against the rounds of them that a place on the card takes: a round
   // takes 6 us or more, a step of a workgroup's four waves 0.15 to 0.2 (one of 700 tokens, 14/2 heads of 64, 7.5 us whole, 13.0
-  // cut).  Else the lengths decide, in the kernel: of up to two rounds for all items together, of more for those that are long.
+  // cut; 256 sequences of 500 with one of 4096 46 and 40, with one of 8192 63 and 43).  Else the lengths decide, in the kernel: of up
+  // to two rounds for all items together, of more for those that are long.
   const int64_t rounds = k.items / room;
-  const int short_steps = (int)(rounds < 2 ? 40 : 40 + 16 * rounds);
+  const int short_steps = (int)(rounds < 2 ? 40 : 96 + 32 * rounds);
   k.whole = steps <= short_steps;
   k.lone = !k.whole && rounds >= 2 ? (int)k.items : 0;
   k.least = k.lone ? short_steps : 0;

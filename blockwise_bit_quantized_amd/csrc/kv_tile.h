@@ -425,12 +425,13 @@ __device__ __forceinline__ int next_holder(const KvAttnParams &p, bool whole, in
 // longest item is longer than five shares and kPatience steps.  One row each of heads of 128 (32 query and 8 key/value),
 // cut against whole: 32 sequences of 4096 35.0 and 30.2 us, 64 of 4096 57.0 and 51.3, 32 of 1024 22.4 and 10.9, 24 of 4096 28.0
 // and 27.6, 32 of different lengths up to 4096 41.5 and 27.8; but one of 2048 11.4 and 16.6, four of 2048 12.2 and 16.9, 16 of 8192
-// 35.3 and 36.4.
+// 35.3 and 36.4.  With other heads (14/2 of 64, 20/4 of 96, 8/1 of 256, 16/16 of 128; 1 to 64 sequences of 1024 to 32768) it took the
+// faster of the two, or one within 2%, in all of 40 cases: 8/1 of 256, 32 of 4096 cut 22.0, whole 36.5; 16/16 of 128, 16 of 2048 26.4 and 19.4.
 // Where a place on the card takes two rounds of items or more, only long ones (of more than p.least steps) are ever cut, if the
 // longest is longer than an even share, by workgroups that wait for nothing else: those of other items need not know.  Cut
-// against whole: 256 sequences of 500 with one of 4096 40.5 and 50.5 us, with one of 131072 68 and 594; 2048 rows of a prompt beside 32
-// sequences of up to 32768 200 and 291; 200 of up to 8192 (none longer than a share) 189.1 and 190.8, 4096 rows over 32768 2274 and
-// 2033.  Knowing it costs 2.7 us, of which the second kernel has most: 256 of 1024 49.9 us, 47.2 where the tables are too short for long ones.
+// against whole: 256 sequences of 500 with one of 8192 42 and 67 us, with one of 131072 67 and 594; 2048 rows of a prompt beside 32
+// sequences of up to 32768 234 and 291; 4096 rows over 32768 (none longer than a share) 2274 and 2016.  Knowing it costs 2.7 us, of
+// which the second kernel has most: 256 of 1024 49.4 us, 46.9 where the tables are too short for long ones.
 constexpr int kPatience = 16;
 __device__ __forceinline__ Work find_work(const KvAttnParams &p) {
   Work w{};
