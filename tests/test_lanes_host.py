@@ -1,7 +1,7 @@
 """The built kernels' machine code, read for one mistake of the compiler that no result shows reliably.
 
-Where lanes part and meet again (`s_and_saveexec`, a branch past the part when no lane takes it, `s_or exec` at the join), nothing
-may be done for all lanes before the join has brought them back.  With more live registers than a wave has, the register
+Where lanes part and meet again (`s_and_saveexec`, a branch past the part when no lane takes it, `s_or exec` at the join, or at an `else`
+`s_andn2_saveexec`), nothing may be done for all lanes before the join has brought them back.  With more live registers than a wave has, the register
 allocator has put its copies there all the same: in a kernel of 32 rows of 192 elements, copies of lanes' load offsets to
 accumulation registers stood before the `s_or exec` behind the loads of the queries, so the lanes of rows that a tile does not
 have kept what the registers held before, and their later loads went anywhere."""
@@ -22,8 +22,8 @@ OBJDUMP = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "llvm", "bin", 
 
 
 def early(lines):
-    """(joins, [(kernel, label, instructions)]) of a listing with labels: vector instructions that stand at a join before
-    its `s_or exec`.  (Lanes of scalars kept in a vector register may be read and written whatever the mask is.)"""
+    """(joins, [(kernel, label, instructions)]) of a listing with labels: vector instructions that stand at a join, or an else, before
+    its lanes are set.  (Lanes of scalars kept in a vector register may be read and written whatever the mask is.)"""
     found, joins, kernel, saved, targets = [], 0, None, None, {}
     lines = [s for s in (l.split("//")[0].split(";")[0].strip() for l in lines) if s]
     for i, s in enumerate(lines):
@@ -42,9 +42,9 @@ def early(lines):
         before = []
         for t in lines[i + 1:i + 400]:
             op = t.split()[0]
-            m = re.match(r"s_or_b64 exec, exec, (\S+)", t)
+            m = re.match(r"s_or_b64 exec, exec, (\S+)|s_(?:or|andn2|xor)_saveexec_b64 [^,]+, (\S+)", t)
             if m:
-                if m.group(1) in targets[label]:
+                if (m.group(1) or m.group(2)) in targets[label]:
                     joins += 1
                     if before:
                         found.append((kernel, label, before))
@@ -64,6 +64,7 @@ def test_the_reader():
     assert early(head + [scalar, copy, back]) == (1, [("_Zkernel", "L9", [copy.strip()])])
     assert early(head + [scalar, back, copy]) == (1, [])
     assert early(head + [copy, "\ts_or_b64 exec, exec, s[6:7]"]) == (0, [])          # another join's lanes
+    assert early(head + [copy, "\ts_andn2_saveexec_b64 s[4:5], s[8:9]"])[1] == [("_Zkernel", "L9", [copy.strip()])]
 
 
 @pytest.mark.skipif(not os.path.exists(OBJDUMP) and not shutil.which("llvm-objdump"), reason="no disassembler")
